@@ -68,6 +68,8 @@ int q8a::set_error(int code, const char* fn, const char* msg) {
 
 int q8a::clear_error() { return ok(); }
 
+uint64_t q8a::wait_timeout_ns() { return g_timeout_ns.load(); }
+
 namespace {
 thread_local bool g_pdl = false;
 }  // namespace
@@ -112,6 +114,13 @@ uint32_t* q8a::host_status_word() {
   }
   return g_host_status_state.load(std::memory_order_relaxed) == 1 ? g_host_status_dev : nullptr;
 }
+
+namespace {
+int bad_index(const char* fn, uint32_t s) {
+  return fail(Q8A_ERR_INVALID_ARG,
+              "%s: a paged call met a slot, page, length or query offset out of range (status 0x%x)", fn, s);
+}
+}  // namespace
 
 const char* q8a::launch_note() { return g_note; }
 
@@ -615,9 +624,12 @@ int attn_finalize(const float* l, const float* o, void* out, int64_t batch, int3
 int q8a_device_status(void* stream, uint32_t* status_out, int32_t clear) {
   uint32_t s = 0;
   cudaError_t e = q8a::read_device_status(static_cast<cudaStream_t>(stream), &s, clear != 0);
+  // the paged kernels record in the host-mapped word alone
+  if (e == cudaSuccess && s == 0) s = __atomic_load_n(&g_host_status_page[0], __ATOMIC_ACQUIRE);
   if (e == cudaSuccess && clear) __atomic_store_n(&g_host_status_page[0], 0u, __ATOMIC_RELEASE);
   if (status_out) *status_out = s;
   if (e != cudaSuccess) return cuda_fail(e, "q8a_device_status");
+  if (s & 2u) return bad_index("q8a_device_status", s);
   if (s != 0)
     return fail(Q8A_ERR_TIMEOUT, "q8a_device_status: a device-side wait ran out (status 0x%x, role %u)",
                 s, (s >> 8) & 0xFFu);
@@ -633,6 +645,7 @@ int q8a_status(void* stream) {
     if (e != cudaSuccess && e != cudaErrorNotReady) return cuda_fail(e, "q8a_status");
   }
   const uint32_t s = __atomic_load_n(&g_host_status_page[0], __ATOMIC_ACQUIRE);
+  if (s & 2u) return bad_index("q8a_status", s);
   if (s != 0)
     return fail(Q8A_ERR_TIMEOUT, "q8a_status: a device-side wait ran out (status 0x%x, role %u)", s,
                 (s >> 8) & 0xFFu);

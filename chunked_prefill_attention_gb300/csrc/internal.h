@@ -145,6 +145,9 @@ int chunk_step_tiles(const void* q, int64_t q_pos0, const void* k_q8, const void
 // not be registered.
 uint32_t* host_status_word();
 
+// Budget of every device-side wait (q8a_set_wait_timeout_ns).
+uint64_t wait_timeout_ns();
+
 // Record `msg` as the calling thread's last error (q8a_last_error) and return code.
 int set_error(int code, const char* fn, const char* msg);
 // Clear the calling thread's last error and return Q8A_OK (a call that succeeded).

@@ -1,0 +1,86 @@
+// paged.h -- launchers of the paged Q8_0 cache and of the rotary positions,
+// shared by the C-ABI layer (paged_api.cu) and the kernel translation units.
+// Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace q8a {
+
+// Element types of the paged calls (Q8A_F16, Q8A_BF16, Q8A_F32 of the ABI).
+enum : int32_t { kF16 = 0, kBF16 = 1, kF32 = 2 };
+
+// Codes that the paged kernels store into the host-mapped status word: bit 0 a
+// wait that ran out, bit 1 an index or length out of range; bits 8..15 the role.
+enum : uint32_t { kRolePaged = 6, kRoleIndex = 7 };
+constexpr uint32_t kStatusTimeout = 1u | (kRolePaged << 8);
+constexpr uint32_t kStatusIndex = 2u | (kRoleIndex << 8);
+
+// Rotary positions of packed tokens: channel pairs of the first `rot` channels
+// turned by position * inv_freq.  inv_freq null (append only): no rotation.
+struct RopeArgs {
+  const int64_t* positions;   // [n_tokens]
+  const double* inv_freq;     // [rot / 2], radians per position
+  int32_t rot;
+  int32_t interleaved;
+  float mscale;
+  float sign;                 // +1, or -1 for the inverse rotation
+};
+
+cudaError_t launch_rope(const void* x, void* out, int32_t dtype, int64_t n_tokens, int32_t heads,
+                        int32_t head_dim, int64_t x_stride, int64_t out_stride, const RopeArgs& r,
+                        cudaStream_t stream);
+
+// A pool of pages: page p holds, for each K/V head, page_tokens rows.
+struct PagePool {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t n_pages;
+  int64_t page_stride;   // bytes between pages
+  int32_t page_shift;    // log2(page_tokens)
+  int32_t kv_heads;
+};
+
+cudaError_t launch_append(const void* k, const void* v, int32_t dtype, int64_t n_tokens, int32_t head_dim,
+                          int64_t k_stride, int64_t v_stride, const int64_t* slots, const RopeArgs& r,
+                          const PagePool& pool, uint32_t* status, cudaStream_t stream);
+
+cudaError_t launch_read(void* k, void* v, int32_t dtype, int64_t n_tokens, int32_t head_dim,
+                        const int64_t* slots, const PagePool& pool, uint32_t* status, cudaStream_t stream);
+
+// Arguments of the attention over pages.
+struct PagedArgs {
+  const void* q;              // [total_q][heads][D], token stride q_stride elements
+  void* out;                  // [total_q][heads][D], contiguous
+  const uint8_t* k;
+  const uint8_t* v;
+  const int32_t* table;       // [batch][table_stride] page numbers
+  const int32_t* kv_lens;     // [batch], the new tokens included
+  const int32_t* cu_q;        // [batch + 1], first query row of each sequence
+  float* part;                // partial states of the split units
+  uint32_t* status;           // device address of the host-mapped status word
+  int64_t n_pages;
+  int64_t page_stride;
+  int64_t q_stride;
+  int64_t table_stride;
+  int64_t total_q;
+  int32_t batch;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t group;              // heads / kv_heads
+  int32_t page_shift;
+  int32_t causal;
+  float scale_log2;           // scale * log2(e)
+  int32_t row_limit;          // sequences of more rows (tokens * group) are another kernel's
+  uint64_t timeout_ns;
+};
+
+// Few query rows per K/V head: one launch over key tiles plus the merge.
+// `rows`: the largest tokens * group of the sequences it takes (a bound).
+cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows,
+                             cudaStream_t stream);
+// Floats of PagedArgs::part that launch_paged_few needs.
+int64_t paged_few_floats(int32_t head_dim, int64_t rows);
+
+}  // namespace q8a

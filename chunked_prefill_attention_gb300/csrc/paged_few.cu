@@ -1,0 +1,804 @@
+// paged_few.cu -- attention of few query rows per K/V head over a paged Q8_0
+// cache: single tokens, bursts, short tails of prompts.
+//
+//   out_i = sum_j e^(S_ij - m_i) V_j / sum_j e^(S_ij - m_i),  S_ij = scale Q_i.K_j
+// with K_j = d c and V_j = d c per block of 32 channels (Q8_0) and the key j
+// visible when j < kv_len and, causal, j <= kv_len - n_q + token(i).
+//
+// What bounds it: HBM.  Each key and head is 2 * 34 * D / 32 bytes for at most
+// 32 rows (token, query head of the group), so the arithmetic has to stay under
+// one SM's share of the memory rate (about 23 bytes a cycle): 5.8 cycles per key
+// and head at D = 64.
+//
+// Products.  mma.sync m16n8k16 with the keys (or channels) on the side of 16
+// and the query rows on the side of 8, so that one row wastes the least:
+//   S^T = K Q^T  (A = codes of 16 keys x 16 channels, B = Q^T),
+//   O^T = V^T P^T  (A = codes of 16 channels x 16 keys, B = P^T).
+// The codes enter as fp16, exactly; the block scales d are applied in fp32 to
+// the block's partial scores, and for V they are folded into the weights before
+// those are rounded to fp16 (one rounding a weight, 2^-11 relative): the codes
+// of both tensors are never scaled in memory or rounded.  bf16 queries enter as
+// fp16 after scaling a row by a power of two (its largest value to [2^14,
+// 2^15)), which keeps their 8 bits down to 2^-38 of that value.
+// (tcgen05 wants 64 or 128 rows and fp16 operands in shared memory: the codes
+// would have to be converted and stored at more than twice their bytes, for
+// at most 32 useful rows.)
+//
+// Layout.  The order of keys inside a tile and of channels inside a block is
+// free as long as both operands agree, and is chosen so that every shared
+// memory load is one aligned word of four codes of one row and the 32 lanes of
+// a load touch 32 banks, although rows are 68 or 136 bytes: lane (g, t) = (lane
+// / 4, lane % 4) takes key S g + j for the scores and keys 2 S t + j for the
+// values, S = 4 (D = 64) or 2 (D = 128) keys of a group.  An even block's codes
+// straddle words by two bytes: the word left over is made of the row's first
+// and ninth words.  The weights come from the score fragments by one 8 x 8
+// transposition in registers (movmatrix).
+//
+// Work.  All key tiles of all (sequence, K/V head, row tile) units are laid end
+// to end and cut into equal shares, one per CTA (two CTAs per SM), so ragged
+// batches and single long sequences both fill the machine.  The warps of a CTA
+// take its tiles in turn, each with its own ring of asynchronous copies (page
+// rows are contiguous: one copy per page and tensor) and its own running
+// softmax; they are joined in a fixed order at the end of a unit's tiles.  A
+// unit cut between CTAs leaves partial states, which a second kernel joins in
+// order: no atomics, the same result every time.
+
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace q8a {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kMaxCtas = 320;      // two per SM of 160 SMs
+constexpr int kDescInts = 8;       // join record of a CTA boundary
+constexpr float kLazy = 8.0f;      // the reference moves when exceeded by more than 2^8
+constexpr int kMergeY = 8;         // blocks that join one unit
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+template <int D>
+struct Shape {
+  static constexpr int S = 256 / D;              // keys of a lane group and tile
+  static constexpr int KT = 8 * S;               // keys of a tile: 32 or 16
+  static constexpr int P = D / 64;               // pairs of Q8_0 blocks
+  static constexpr int RW = 17 * P;              // words of a row
+  static constexpr int TILE = KT * RW * 4;       // bytes of a tensor's tile: 2176
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int RING = kWarps * kStages * STAGE;
+};
+
+template <int D, int NT>
+struct Part {
+  static constexpr int R = 8 * NT;               // rows of a tile
+  static constexpr int NREG = D / 16 * NT * 4;   // O registers of a lane
+  static constexpr int FLOATS = NREG * 32 + 2 * R;
+};
+
+// Bounded waits of a warp on its own copies.  A wait that runs out is recorded;
+// the warp then starts no further copy and waits (again bounded) only for those
+// it has started, so that it never leaves one in flight.
+struct Waiter {
+  uint64_t budget;   // cycles
+  uint32_t* status;
+  bool bad;
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return;
+    const long long t0 = clock64();
+    while (!__all_sync(kFull, mbar_try_wait_sleep(bar, parity, 100000u))) {
+      const int out = static_cast<uint64_t>(clock64() - t0) > budget;
+      if (__any_sync(kFull, out)) {
+        bad = true;
+        if ((threadIdx.x & 31) == 0) *reinterpret_cast<volatile uint32_t*>(status) = kStatusTimeout;
+        return;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transposition of 16-bit values held two to a lane (lane 4 r + c: row r,
+// columns 2 c and 2 c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Four signed codes as two half2, exactly: u = c + 128 under the exponent of
+// 1024 is 1024 + u; minus 1152.
+__device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
+  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float half_bits(uint32_t b) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Weight of a partial state with reference m under the joint reference top.
+__device__ __forceinline__ float join_weight(float m, float top) {
+  return m == -INFINITY ? 0.0f : (m == top ? 1.0f : ex2_approx(m - top));
+}
+
+// A sequence as the device arrays give it, with every bound checked: rows that
+// do not exist and keys beyond the table are left out and recorded.
+struct Seq {
+  int64_t q0;      // first query row
+  int32_t n_q, kv;
+};
+__device__ __forceinline__ Seq read_seq(const PagedArgs& a, int b) {
+  Seq s;
+  int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+  const int64_t kv = a.kv_lens[b], most = i64min(a.table_stride << a.page_shift, 0x7FFF0000);
+  const bool wrong = q0 < 0 || q1 < q0 || q1 > a.total_q || kv < 0 || kv > most;
+  if (wrong) *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+  q0 = i64max(0, i64min(q0, a.total_q));
+  q1 = i64max(q0, i64min(q1, a.total_q));
+  s.q0 = q0;
+  s.n_q = static_cast<int32_t>(q1 - q0);
+  s.kv = static_cast<int32_t>(i64max(0, i64min(kv, most)));
+  return s;
+}
+
+template <int D, int NT>
+struct Units {
+  int32_t tiles;   // key tiles of one unit (at least 1, so that a row without keys is written)
+  int32_t row_tiles;
+  int64_t all;     // tiles of the sequence's units
+};
+template <int D, int NT>
+__device__ __forceinline__ Units<D, NT> units_of(const PagedArgs& a, const Seq& s) {
+  Units<D, NT> u;
+  const int64_t rows = static_cast<int64_t>(s.n_q) * a.group;
+  u.tiles = max(1, (s.kv + Shape<D>::KT - 1) / Shape<D>::KT);
+  u.row_tiles = rows > a.row_limit ? 0 : static_cast<int32_t>((rows + 8 * NT - 1) / (8 * NT));
+  u.all = static_cast<int64_t>(u.tiles) * u.row_tiles * a.kv_heads;
+  return u;
+}
+
+__device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t n = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += n;
+  }
+  return v;
+}
+
+template <typename QT, int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT * D <= 256 ? 2 : 1)
+paged_few_kernel(const PagedArgs a) {
+  using Sh = Shape<D>;
+  using Pt = Part<D, NT>;
+  constexpr int S = Sh::S, KT = Sh::KT, RW = Sh::RW, P = Sh::P, R = Pt::R, NREG = Pt::NREG;
+  static_assert(kWarps / 2 * (NREG + 4 * NT) * 128 <= Sh::RING, "the join of a CTA's warps reuses the ring");
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+  __shared__ int64_t sums[kWarps], found[2];
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  if (lane == 0)
+    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp * kStages + s]), 1);
+  fence_mbar_init();
+  pdl_wait();
+
+  // ---- this CTA's share of all key tiles
+  int64_t mine = 0;
+  for (int b = tid; b < a.batch; b += kThreads) mine += units_of<D, NT>(a, read_seq(a, b)).all;
+  const int64_t inc = warp_inclusive(mine, lane);
+  if (lane == 31) sums[warp] = inc;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
+  const int64_t share = i64max(kWarps, (total + gridDim.x - 1) / gridDim.x);
+  int32_t* desc = reinterpret_cast<int32_t*>(a.part) + static_cast<int64_t>(blockIdx.x) * kDescInts;
+  float* parts = a.part + kMaxCtas * kDescInts;
+  if (tid == 0) desc[0] = -1;   // nothing to join at this boundary, until found otherwise
+  int64_t pos = blockIdx.x * share;
+  const int64_t end = i64min(total, pos + share);
+  if (pos >= end) return;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    __syncthreads();
+    const int b = b0 + tid;
+    const int64_t v = b < a.batch ? units_of<D, NT>(a, read_seq(a, b)).all : 0;
+    const int64_t i = warp_inclusive(v, lane);
+    if (lane == 31) sums[warp] = i;
+    __syncthreads();
+    int64_t before = base;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    if (pos >= before + i - v && pos < before + i) {
+      found[0] = b;
+      found[1] = before + i - v;
+    }
+    for (int w = 0; w < kWarps; ++w) base += sums[w];
+    __syncthreads();
+    if (found[0] >= 0) break;
+  }
+  int b = static_cast<int>(found[0]);
+  base = found[1];
+
+  uint8_t* ring = smem + warp * (kStages * Sh::STAGE);
+  const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp * kStages]);
+  Waiter waiter{2 * a.timeout_ns, a.status, false};
+  uint32_t it = 0;   // tiles this warp has taken: stage and parity of the ring
+  const uint32_t sel_k = t == 3 ? 0x7610u : 0x3210u, sel_v = g == 7 ? 0x7610u : 0x3210u;
+  // pieces of a tile: one, or (pages of 16, D = 64) two pages' worth
+  const int piece_shift = min(a.page_shift, D == 64 ? 5 : 4);
+  const int pieces = KT >> piece_shift;
+  const uint32_t piece_bytes = static_cast<uint32_t>(RW * 4) << piece_shift;
+  const int64_t start = pos;
+
+  while (pos < end) {
+    const Seq sq = read_seq(a, b);
+    const auto un = units_of<D, NT>(a, sq);
+    if (pos >= base + un.all) {
+      base += un.all;
+      ++b;
+      continue;
+    }
+    const int64_t local = pos - base;
+    const int64_t unit = local / un.tiles;
+    const int tile0 = static_cast<int>(local - unit * un.tiles);
+    const int kvh = static_cast<int>(unit / un.row_tiles);
+    const int rt = static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
+    const int n = static_cast<int>(i64min(un.tiles - tile0, end - pos));
+    const int n_rows = sq.n_q * a.group;
+    const int nw = (n - warp + kWarps - 1) / kWarps;   // this warp's tiles
+
+    // ---- copies of this warp's tiles
+    const int32_t* table = a.table + b * a.table_stride;
+    const int64_t head_off = (static_cast<int64_t>(kvh) << a.page_shift) * (RW * 4);
+    auto fetch = [&](int j) -> int {   // page of this lane's piece of tile j
+      const int key = (tile0 + warp + kWarps * j) * KT + (lane << piece_shift);
+      return (lane < pieces && j < nw && key < sq.kv) ? table[key >> a.page_shift] : 0;
+    };
+    int issued = 0;
+    auto issue = [&](int j, int page) {
+      if (j >= nw || waiter.bad) return;
+      issued = j + 1;
+      const uint32_t c = it + j, s = c % kStages;
+      const int key0 = (tile0 + warp + kWarps * j) * KT;
+      const int have = max(0, min(pieces, (sq.kv - key0 + (1 << piece_shift) - 1) >> piece_shift));
+      if (lane == 0) mbar_arrive_expect_tx(bar_u + 8 * s, 2 * have * piece_bytes);
+      __syncwarp();
+      if (lane < have) {
+        if (page < 0 || page >= a.n_pages) {
+          *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+          page = 0;
+        }
+        const int off = (key0 + (lane << piece_shift)) & ((1 << a.page_shift) - 1);
+        const int64_t at = page * a.page_stride + head_off + static_cast<int64_t>(off) * (RW * 4);
+        const uint32_t dst = ring_u + s * Sh::STAGE + lane * piece_bytes;
+        bulk_load(dst, a.k + at, piece_bytes, bar_u + 8 * s);
+        bulk_load(dst + Sh::TILE, a.v + at, piece_bytes, bar_u + 8 * s);
+      }
+    };
+    {
+      int pg[kStages];
+#pragma unroll
+      for (int j = 0; j < kStages; ++j) pg[j] = fetch(j);
+#pragma unroll
+      for (int j = 0; j < kStages; ++j) issue(j, pg[j]);
+    }
+    int next_page = fetch(kStages);
+
+    // ---- Q^T fragments: lane (g, t) holds row 8 nt + g, the channels of its words
+    uint32_t qf[NT][P][4][2];
+    float sl2[NT][2];
+    int lim[NT][2];   // keys that the row of column 2 t (+ 1) sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = rt * R + 8 * nt + g;
+      const int tok = row / a.group;
+      const QT* qp = static_cast<const QT*>(a.q) + (sq.q0 + tok) * a.q_stride +
+                     static_cast<int64_t>(kvh * a.group + row - tok * a.group) * D;
+      float up = 1.0f, down = 1.0f;
+      uint32_t raw[P][4][2];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int st = 0; st < 4; ++st)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // first channel of the half word: see the words of a row above
+            const int c = st == 0 ? 4 * t + 2 + 2 * h
+                          : st == 1 ? (t == 3 && h == 1 ? 0 : 4 * t + 18 + 2 * h)
+                                    : 32 + 16 * (st - 2) + 4 * t + 2 * h;
+            raw[p][st][h] =
+                row < n_rows ? __ldg(reinterpret_cast<const uint32_t*>(qp + 64 * p + c)) : 0u;
+          }
+      if (sizeof(QT) == 2 && !std::is_same<QT, __half>::value) {
+        uint32_t top = 0;   // largest magnitude, as bits
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              top = max(top, max(raw[p][st][h] & 0x7FFFu, (raw[p][st][h] >> 16) & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        top = max(top, __shfl_xor_sync(kFull, top, 2));
+        const int e = static_cast<int>(top >> 7);   // biased exponent
+        const int f = (e == 0 || e == 255) ? 0 : min(141 - e, 100);
+        up = __int_as_float((127 + f) << 23);
+        down = __int_as_float((127 - f) << 23);
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int st = 0; st < 4; ++st)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x = raw[p][st][h];
+            if (!std::is_same<QT, __half>::value)
+              x = pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up);
+            qf[nt][p][st][h] = x;
+          }
+      const float sc = a.scale_log2 * down;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sl2[nt][c] = __shfl_sync(kFull, sc, 4 * (2 * t + c));
+        const int r = rt * R + 8 * nt + 2 * t + c;
+        lim[nt][c] = a.causal ? min(sq.kv, sq.kv - sq.n_q + r / a.group + 1) : sq.kv;
+      }
+    }
+    // keys that every row of the unit sees: tiles below need no mask
+    const int clear = a.causal ? sq.kv - sq.n_q + rt * R / a.group + 1 : sq.kv;
+
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.0f;
+      }
+    int v_exp = 0;   // largest exponent (fp16, biased) of V's scales so far; weights carry 2^(21 - v_exp)
+
+#pragma unroll 1
+    for (int j = 0; j < nw; ++j) {
+      const uint32_t c = it + j, st = c % kStages;
+      if (j >= issued) break;   // an earlier wait ran out
+      waiter.wait(bar_u + 8 * st, (c / kStages) & 1);
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(ring + st * Sh::STAGE);
+      const uint32_t* vw = kw + Sh::TILE / 4;
+      const int key0 = (tile0 + warp + kWarps * j) * KT;
+
+      // ---- scores: s[mt][nt][e], key S g + 2 mt (e < 2) or the next, column 2 t + (e & 1)
+      float s[S / 2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < S / 2; ++mt) {
+        const uint32_t* ra = kw + (S * g + 2 * mt) * RW;
+        const uint32_t* rb = ra + RW;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint32_t a0 = ra[17 * p], a8 = ra[17 * p + 8], b0 = rb[17 * p], b8 = rb[17 * p + 8];
+          uint32_t f[4][4];   // A fragments of the four steps of 16 channels
+          codes_to_half2(ra[17 * p + 1 + t], f[0][0], f[0][2]);
+          codes_to_half2(rb[17 * p + 1 + t], f[0][1], f[0][3]);
+          codes_to_half2(__byte_perm(ra[17 * p + 5 + t], a0, sel_k), f[1][0], f[1][2]);
+          codes_to_half2(__byte_perm(rb[17 * p + 5 + t], b0, sel_k), f[1][1], f[1][3]);
+          codes_to_half2(ra[17 * p + 9 + t], f[2][0], f[2][2]);
+          codes_to_half2(rb[17 * p + 9 + t], f[2][1], f[2][3]);
+          codes_to_half2(ra[17 * p + 13 + t], f[3][0], f[3][2]);
+          codes_to_half2(rb[17 * p + 13 + t], f[3][1], f[3][3]);
+          const float da0 = half_bits(a0), da1 = half_bits(a8 >> 16);
+          const float db0 = half_bits(b0), db1 = half_bits(b8 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16816(x, f[0], qf[nt][p][0][0], qf[nt][p][0][1]);
+            mma16816(y, f[2], qf[nt][p][2][0], qf[nt][p][2][1]);
+            mma16816(x, f[1], qf[nt][p][1][0], qf[nt][p][1][1]);
+            mma16816(y, f[3], qf[nt][p][3][0], qf[nt][p][3][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float d0 = e < 2 ? da0 : db0, d1 = e < 2 ? da1 : db1;
+              const float z = fmaf(d0, x[e], d1 * y[e]);
+              s[mt][nt][e] = p == 0 ? z : s[mt][nt][e] + z;
+            }
+          }
+        }
+      }
+      // ---- V's scales of keys S g + i
+      uint32_t dv_bits[S][D / 32];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const uint16_t* rv = reinterpret_cast<const uint16_t*>(vw + (S * g + i) * RW);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) dv_bits[i][k] = rv[17 * k];
+      }
+#pragma unroll
+      for (int mt = 0; mt < S / 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= sl2[nt][e & 1];
+      if (key0 + KT > clear) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int key = key0 + S * g + i;
+          // rows of the tile that hold no key of the sequence: whatever the page
+          // or the ring holds there
+          if (key >= sq.kv)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) dv_bits[i][k] = 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+              if (key >= lim[nt][cc]) s[i / 2][nt][2 * (i & 1) + cc] = -INFINITY;
+        }
+      }
+      {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) top = max(top, dv_bits[i][k] & 0x7FFFu);
+        const int e = static_cast<int>(__reduce_max_sync(kFull, top) >> 10);
+        if (e > v_exp) {   // uniform over the warp
+          const float f = __int_as_float((127 + v_exp - e) << 23);
+          v_exp = e;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i][nt][k] *= f;
+        }
+      }
+      const float v_up = __int_as_float((127 + 21 - v_exp) << 23);
+
+      // ---- the running reference: moved only when a score exceeds it by more than 2^8
+      bool over = false;
+#pragma unroll
+      for (int mt = 0; mt < S / 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over |= s[mt][nt][e] > m[nt][e & 1] + kLazy;
+      if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < S / 2; ++mt) top = fmaxf(top, fmaxf(s[mt][nt][cc], s[mt][nt][2 + cc]));
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+            if (top > m[nt][cc] + kLazy) {
+              const float al = m[nt][cc] == -INFINITY ? 0.0f : ex2_approx(m[nt][cc] - top);
+              m[nt][cc] = top;
+              l[nt][cc] *= al;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[i][nt][cc] *= al;
+                o[i][nt][2 + cc] *= al;
+              }
+            }
+          }
+      }
+      // ---- weights, per V block times its scale, and their transposition
+      uint32_t pb[NT][D / 32][S];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
+        const float r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const float w0 = ex2_approx(s[i / 2][nt][2 * (i & 1)] - r0);
+          const float w1 = ex2_approx(s[i / 2][nt][2 * (i & 1) + 1] - r1);
+          l[nt][0] += w0;
+          l[nt][1] += w1;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const float dv = half_bits(dv_bits[i][k]) * v_up;
+            pb[nt][k][i] = transpose8(pack_half2(w0 * dv, w1 * dv));
+          }
+        }
+      }
+      // ---- values: channels on the side of 16, keys 2 S t + ...
+#pragma unroll
+      for (int kk = 0; kk < S / 2; ++kk) {
+        const uint32_t* r0 = vw + (2 * S * t + 2 * kk) * RW;   // keys of columns 2 t, 2 t + 8
+        const uint32_t* r1 = r0 + S * RW;                      // of columns 2 t + 1, 2 t + 9
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const int w = 17 * p + (odd ? 9 : 1) + g;
+            uint32_t w0 = r0[w], w1 = r1[w], w2 = r0[w + RW], w3 = r1[w + RW];
+            if (!odd) {
+              w0 = __byte_perm(w0, r0[17 * p], sel_v);
+              w1 = __byte_perm(w1, r1[17 * p], sel_v);
+              w2 = __byte_perm(w2, r0[17 * p + RW], sel_v);
+              w3 = __byte_perm(w3, r1[17 * p + RW], sel_v);
+            }
+            uint32_t f[2][4];
+            codes_to_half2(__byte_perm(w0, w1, 0x5140), f[0][0], f[0][1]);
+            codes_to_half2(__byte_perm(w2, w3, 0x5140), f[0][2], f[0][3]);
+            codes_to_half2(__byte_perm(w0, w1, 0x7362), f[1][0], f[1][1]);
+            codes_to_half2(__byte_perm(w2, w3, 0x7362), f[1][2], f[1][3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[4 * p + 2 * odd + h][nt], f[h], pb[nt][2 * p + odd][2 * kk], pb[nt][2 * p + odd][2 * kk + 1]);
+          }
+      }
+      __syncwarp();
+      issue(j + kStages, next_page);
+      next_page = fetch(j + kStages + 1);
+    }
+    it += nw;
+
+    // ---- join the warps, in a fixed order
+    const float v_down = __int_as_float((127 - 21 + v_exp) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][nt][e] *= v_down;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[nt][cc] += __shfl_xor_sync(kFull, l[nt][cc], x);
+    float* xch = reinterpret_cast<float*>(smem);
+    constexpr int kXch = (NREG + 4 * NT) * 32;
+    __syncthreads();   // every warp's tiles are consumed: the ring is free
+#pragma unroll 1
+    for (int half = kWarps / 2; half > 0; half /= 2) {
+      if (warp >= half && warp < 2 * half) {
+        float* dst = xch + (warp - half) * kXch + lane;
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) dst[32 * i] = o[i / (4 * NT)][i / 4 % NT][i & 3];
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+          dst[32 * (NREG + i)] = m[i / 2][i & 1];
+          dst[32 * (NREG + 2 * NT + i)] = l[i / 2][i & 1];
+        }
+        fence_proxy_async_smem();   // these writes come before the next unit's copies
+      }
+      __syncthreads();
+      if (warp < half) {
+        const float* src = xch + warp * kXch + lane;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float wa[2], wb[2];
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const float mb = src[32 * (NREG + 2 * nt + cc)], lb = src[32 * (NREG + 2 * NT + 2 * nt + cc)];
+            const float top = fmaxf(m[nt][cc], mb);
+            wa[cc] = join_weight(m[nt][cc], top);
+            wb[cc] = join_weight(mb, top);
+            m[nt][cc] = top;
+            l[nt][cc] = fmaf(wa[cc], l[nt][cc], wb[cc] * lb);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[i][nt][e] = fmaf(wa[e & 1], o[i][nt][e], wb[e & 1] * src[32 * ((i * NT + nt) * 4 + e)]);
+        }
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+      if (n == un.tiles) {   // the whole unit: the rows of out
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int row = rt * R + 8 * nt + 2 * t + cc;
+            if (row >= n_rows) continue;
+            const int tok = row / a.group;
+            QT* op = static_cast<QT*>(a.out) +
+                     ((sq.q0 + tok) * a.heads + kvh * a.group + row - tok * a.group) * D;
+            const float inv = l[nt][cc] == 0.0f ? 0.0f : 1.0f / l[nt][cc];
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+              for (int odd = 0; odd < 2; ++odd) {
+                const int i = 4 * p + 2 * odd;
+                const float y0 = o[i][nt][cc] * inv, y1 = o[i][nt][2 + cc] * inv;
+                const float y2 = o[i + 1][nt][cc] * inv, y3 = o[i + 1][nt][2 + cc] * inv;
+                const int c = 64 * p + (odd ? 32 : 2) + 4 * g;
+                const int c2 = !odd && g == 7 ? 64 * p : c + 2;
+                uint32_t lo, hi;
+                if (std::is_same<QT, __half>::value) {
+                  lo = pack_half2(y0, y1);
+                  hi = pack_half2(y2, y3);
+                } else {
+                  const __nv_bfloat162 x0 = __floats2bfloat162_rn(y0, y1), x1 = __floats2bfloat162_rn(y2, y3);
+                  lo = *reinterpret_cast<const uint32_t*>(&x0);
+                  hi = *reinterpret_cast<const uint32_t*>(&x1);
+                }
+                *reinterpret_cast<uint32_t*>(op + c) = lo;
+                *reinterpret_cast<uint32_t*>(op + c2) = hi;
+              }
+          }
+      } else {
+        const bool first = pos == start;
+        float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1)) * Pt::FLOATS;
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) part[32 * i + lane] = o[i / (4 * NT)][i / 4 % NT][i & 3];
+        if (g == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              part[32 * NREG + 8 * nt + 2 * t + cc] = m[nt][cc];
+              part[32 * NREG + R + 8 * nt + 2 * t + cc] = l[nt][cc];
+            }
+        }
+        // the first boundary inside a unit names the unit's partial states:
+        // CTA c - 1 (its last) and the first of c, c + 1, ...
+        const int64_t u0 = pos - tile0;
+        if (first && tile0 > 0 && u0 >= start - share && lane == 0) {
+          desc[1] = kvh;
+          desc[2] = rt;
+          desc[3] = u0 == start - share ? 0 : 1;
+          desc[4] = static_cast<int32_t>((u0 + un.tiles - 1) / share) - static_cast<int32_t>(blockIdx.x) + 2;
+          desc[0] = b;
+        }
+      }
+    }
+    pos += n;
+  }
+}
+
+// Joins the partial states of a unit that several CTAs hold parts of: block
+// (c, y) a slice of the unit first cut at the start of CTA c + 1.
+template <typename QT, int D, int NT>
+__global__ void __launch_bounds__(256) paged_few_join_kernel(const PagedArgs a) {
+  using Pt = Part<D, NT>;
+  constexpr int R = Pt::R, NREG = Pt::NREG, E = NREG * 32 / kMergeY;   // elements of this block
+  static_assert(E % 64 == 0, "slices of 64 elements");
+  __shared__ float w[kMaxCtas + 1][R];
+  __shared__ float inv[R];
+  __shared__ float sum[4][64];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int32_t* desc = reinterpret_cast<const int32_t*>(a.part) + (static_cast<int64_t>(blockIdx.x) + 1) * kDescInts;
+  const int b = desc[0];
+  if (b < 0) return;
+  const int kvh = desc[1], rt = desc[2], n = min(desc[4], kMaxCtas + 1);
+  const float* parts = a.part + kMaxCtas * kDescInts;
+  const int64_t c = blockIdx.x;
+  // partial p of the unit: slot desc[3] of CTA c, then slot 0 of the CTAs after it
+  auto part = [&](int p) { return parts + (p == 0 ? 2 * c + desc[3] : 2 * (c + p)) * Pt::FLOATS; };
+  const Seq sq = read_seq(a, b);
+  for (int i = threadIdx.x; i < n * R; i += 256) w[i / R][i % R] = part(i / R)[32 * NREG + i % R];
+  __syncthreads();
+  {
+    constexpr int kPer = 256 / R;   // threads of a row (neighbours)
+    const int row = threadIdx.x / kPer, k = threadIdx.x % kPer;
+    float top = -INFINITY;
+    for (int p = k; p < n; p += kPer) top = fmaxf(top, w[p][row]);
+#pragma unroll
+    for (int x = 1; x < kPer; x *= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+    float l = 0.0f;
+    for (int p = k; p < n; p += kPer) {
+      const float f = join_weight(w[p][row], top);
+      w[p][row] = f;
+      l = fmaf(f, part(p)[32 * NREG + R + row], l);
+    }
+#pragma unroll
+    for (int x = 1; x < kPer; x *= 2) l += __shfl_xor_sync(kFull, l, x);
+    if (k == 0) inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
+  }
+  __syncthreads();
+  const int e64 = threadIdx.x & 63, pg = threadIdx.x >> 6;
+  const int n_rows = sq.n_q * a.group;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = blockIdx.y * E + e0 + e64;
+    const int reg = e / 32, lane = e % 32, g = lane >> 2, t = lane & 3;
+    const int i = reg / (4 * NT), nt = reg / 4 % NT, k = reg & 3;
+    const int row = 8 * nt + 2 * t + (k & 1);
+    float y = 0.0f;
+#pragma unroll 8
+    for (int p = pg; p < n; p += 4) y = fmaf(w[p][row], part(p)[e], y);
+    sum[pg][e64] = y;
+    __syncthreads();
+    const int r = rt * R + row;
+    if (pg == 0 && r < n_rows) {
+      y = ((sum[0][e64] + sum[1][e64]) + (sum[2][e64] + sum[3][e64])) * inv[row];
+      const int word = i & 1, odd = (i >> 1) & 1, ch = 2 * word + (k >> 1);   // code of the lane's word
+      int chan = 64 * (i / 4) + (odd ? 32 : 2) + 4 * g + ch;
+      if (!odd && g == 7 && ch >= 2) chan -= 32;   // the word of a row's first and ninth words
+      const int tok = r / a.group;
+      QT* op = static_cast<QT*>(a.out) + ((sq.q0 + tok) * a.heads + kvh * a.group + r - tok * a.group) * D + chan;
+      if (std::is_same<QT, __half>::value)
+        *reinterpret_cast<__half*>(op) = __float2half_rn(y);
+      else
+        *reinterpret_cast<__nv_bfloat16*>(op) = __float2bfloat16_rn(y);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename QT, int D, int NT>
+cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
+  auto kernel = paged_few_kernel<QT, D, NT>;
+  constexpr int smem = Shape<D>::RING;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
+  if (e != cudaSuccess || ctas < 2) return e;
+  return launch_kernel(paged_few_join_kernel<QT, D, NT>, dim3(ctas - 1, kMergeY), dim3(256), 0, stream, a);
+}
+
+template <typename QT, int D>
+cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  const int per_sm = nt * D <= 256 ? 2 : 1;
+  const int ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  if (nt == 1) return launch_few<QT, D, 1>(a, ctas, stream);
+  if (nt == 2) return launch_few<QT, D, 2>(a, ctas, stream);
+  return launch_few<QT, D, 4>(a, ctas, stream);
+}
+
+}  // namespace
+
+int64_t paged_few_floats(int32_t head_dim, int64_t rows) {
+  const int64_t r = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  return kMaxCtas * (kDescInts + 2 * (r * head_dim + 2 * r));
+}
+
+cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows, cudaStream_t stream) {
+  if (dtype == kF16)
+    return head_dim == 64 ? launch_few_d<__half, 64>(a, rows, stream) : launch_few_d<__half, 128>(a, rows, stream);
+  return head_dim == 64 ? launch_few_d<__nv_bfloat16, 64>(a, rows, stream)
+                        : launch_few_d<__nv_bfloat16, 128>(a, rows, stream);
+}
+
+}  // namespace q8a

@@ -7,6 +7,7 @@ include/q8attn.h.  There is no CPU fallback: if the library is missing or fails
 to load, every call raises.
 """
 
+import contextlib
 import ctypes
 import math
 import os
@@ -59,6 +60,14 @@ SIGNATURES = {
                                                 _I64, _I32, _I64, _F, _I32, ctypes.POINTER(_P)]),
     "q8a_prefill_graph_launch": (ctypes.c_int, [_P, _P]),
     "q8a_prefill_graph_destroy": (ctypes.c_int, [_P]),
+    "attn_rope": (ctypes.c_int, [_P, _P, _I32, _I64, _I32, _I32, _I64, _I64, _P, _P, _I32, _I32, _F, _I32,
+                                 _P]),
+    "q8kv_append_paged": (ctypes.c_int, [_P, _P, _I32, _I64, _I32, _I32, _I64, _I64, _P, _P, _P, _I64, _I32,
+                                         _I64, _P, _P, _I32, _I32, _F, _P]),
+    "q8kv_read_paged": (ctypes.c_int, [_P, _P, _I64, _I32, _I64, _P, _I64, _I32, _I32, _P, _P, _I32, _P]),
+    "attn_paged": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
+                                  _P, _P, _I64, _I64, _I64, _F, _I32, _P, _P, _I64, _P]),
+    "q8a_paged_workspace_floats": (_I64, [_I64, _I32, _I32, _I64, _I64, _I32]),
     "q8a_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_U32), _I32]),
     "q8a_status": (ctypes.c_int, [_P]),
     "q8a_set_wait_timeout_ns": (ctypes.c_int, [_U64]),
@@ -368,6 +377,199 @@ def attn_prefill_pipelined(q_host, k_host, v_host, out_host, bufs, scale=None, c
         _ptr(bufs.v8), bufs.stride, _ptr(st.m), _ptr(st.l), _ptr(st.o), _ptr(bufs.out),
         _stream(bufs.q), ctypes.c_void_p(bufs.copy_stream.cuda_stream)))
     return out_host
+
+
+# ---- rotary positions and the paged cache -----------------------------------
+# The device-side checks of these calls read indices from device tensors; what
+# can be told from shapes, types and devices is refused here, before the call.
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _need(ok, msg):
+    if not ok:
+        raise Q8AttnError(Q8A_ERR_INVALID_ARG, msg)
+
+
+def _need_tensor(name, t, dtype, ndim, device):
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == ndim and t.device == device and
+          (t.dtype in dtype if isinstance(dtype, (tuple, dict)) else t.dtype == dtype),
+          f"{name}: a {ndim}-dimensional CUDA tensor on {device} of {dtype} is needed")
+
+
+def _need_index(name, t, dtype, n, device):
+    _need_tensor(name, t, dtype, 1, device)
+    _need(t.shape[0] == n and t.is_contiguous(), f"{name}: {n} contiguous values are needed, got {tuple(t.shape)}")
+
+
+def _token_stride(name, t):
+    """Elements between tokens of a packed [T, H, D] tensor whose heads are contiguous."""
+    T, H, D = t.shape
+    _need((D <= 1 or t.stride(2) == 1) and (H <= 1 or t.stride(1) == D),
+          f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if T > 1 else max(H * D, 1)
+
+
+def _pool(k_pages, v_pages, device):
+    """(kv_heads, page_tokens, head_dim, page stride in bytes) of uint8 pages [n_pages, H_kv, page_tokens,
+    row bytes], contiguous within a page (the K and V pools may be interleaved, page by page)."""
+    _need_tensor("k_pages", k_pages, torch.uint8, 4, device)
+    _need_tensor("v_pages", v_pages, torch.uint8, 4, device)
+    n, H, P, rb = k_pages.shape
+    _need(v_pages.shape == k_pages.shape and v_pages.stride() == k_pages.stride(),
+          "k_pages and v_pages must have the same shape and strides")
+    _need(rb in (68, 136), f"rows of 68 or 136 bytes are needed, got {rb}")
+    _need(k_pages[0].is_contiguous() if n else True, "each page must be contiguous")
+    return H, P, rb // 34 * 32, k_pages.stride(0) if n > 1 else H * P * rb
+
+
+def _on(device):
+    """The calls launch on the tensors' device, whichever is current."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, scaling="linear", original_len=None, low=1.0, high=4.0,
+                  device=None):
+    """fp64 [rot_dim / 2] radians per position: base^(-2i / rot_dim), for a context
+    `factor` times as long as the original:
+      "linear"  every frequency divided by factor (positions interpolated);
+      "base"    the base raised to base * factor^(rot_dim / (rot_dim - 2)), which divides the lowest
+                frequency by factor and leaves the highest;
+      "bands"   frequencies that turn more than `high` times within original_len tokens are kept, those
+                that turn less than `low` times are divided by factor, those between are blended."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if factor <= 0 or base <= 0:
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot_dim > 2:
+            base = base * factor ** (rot_dim / (rot_dim - 2))
+        f = base ** (-i / rot_dim)
+    elif scaling == "linear":
+        f = base ** (-i / rot_dim) / factor
+    elif scaling == "bands":
+        if original_len is None or original_len <= 0 or high <= low:
+            raise ValueError("bands need original_len > 0 and high > low")
+        f = base ** (-i / rot_dim)
+        keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    else:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device) if device is not None else f
+
+
+def attn_rope(x, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False, out=None):
+    """Rotary positions of packed x [T, H, D] (fp16, bf16 or fp32; a slice of a wider buffer is fine):
+    the first 2 * len(inv_freq) channels of every head turned by positions [T] (int64) times inv_freq
+    (fp64, see rope_inv_freq).  `out` may be x.  `inverse` turns back (the gradient of the rotation)."""
+    _need_tensor("x", x, _DTYPES, 3, x.device)
+    T, H, D = x.shape
+    _need_index("positions", positions, torch.int64, T, x.device)
+    _need_tensor("inv_freq", inv_freq, torch.float64, 1, x.device)
+    _need(inv_freq.is_contiguous(), "inv_freq must be contiguous")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    else:
+        _need_tensor("out", out, x.dtype, 3, x.device)
+        _need(out.shape == x.shape, "out must have the shape of x")
+    with _on(x.device):
+        _check(load().attn_rope(_ptr(x), _ptr(out), _DTYPES[x.dtype], T, H, D, _token_stride("x", x),
+                                _token_stride("out", out), _ptr(positions), _ptr(inv_freq), 2 * inv_freq.shape[0],
+                                int(bool(interleaved)), mscale, int(bool(inverse)), _stream(x)))
+    return out
+
+
+def q8kv_append_paged(k, v, k_pages, v_pages, slots, positions=None, inv_freq=None, interleaved=False, mscale=1.0):
+    """Quantise packed k, v [T, H_kv, D] (fp16, bf16 or fp32) into pages: uint8 k_pages, v_pages
+    [n_pages, H_kv, page_tokens, D / 32 * 34], row t to slot slots[t] (int64: page * page_tokens + offset;
+    negative: skipped).  With positions and inv_freq the keys are rotated first, as attn_rope does."""
+    _need_tensor("k", k, _DTYPES, 3, k.device)
+    _need_tensor("v", v, k.dtype, 3, k.device)
+    T, H, D = k.shape
+    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, k.device)
+    _need(v.shape == k.shape and H == kv_heads and D == head_dim, "k, v and the pages must agree in heads and head_dim")
+    _need_index("slots", slots, torch.int64, T, k.device)
+    _need((positions is None) == (inv_freq is None), "positions and inv_freq come together")
+    rot = 0
+    if positions is not None:
+        _need_index("positions", positions, torch.int64, T, k.device)
+        _need_tensor("inv_freq", inv_freq, torch.float64, 1, k.device)
+        _need(inv_freq.is_contiguous(), "inv_freq must be contiguous")
+        rot = 2 * inv_freq.shape[0]
+    with _on(k.device):
+        _check(load().q8kv_append_paged(_ptr(k), _ptr(v), _DTYPES[k.dtype], T, H, D, _token_stride("k", k),
+                                        _token_stride("v", v), _ptr(slots), _ptr(k_pages), _ptr(v_pages),
+                                        k_pages.shape[0], page_tokens, stride, _ptr(positions), _ptr(inv_freq), rot,
+                                        int(bool(interleaved)), mscale, _stream(k)))
+
+
+def q8kv_read_paged(k_pages, v_pages, slots, dtype=torch.float16, out=None):
+    """The rows at `slots` (int64 [T]) dequantised: (k, v), each [T, H_kv, D] of dtype.  `out`: a pair of
+    such tensors to write into; a negative slot leaves its row there as it was."""
+    _need(isinstance(slots, torch.Tensor) and slots.is_cuda, "slots must be a CUDA tensor")
+    device = slots.device
+    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, device)
+    _need(slots.dim() == 1, "slots must have one dimension")
+    T = slots.shape[0]
+    _need_index("slots", slots, torch.int64, T, device)
+    _need(dtype in _DTYPES, f"dtype {dtype} is not supported")
+    if out is None:
+        out = tuple(torch.empty((T, kv_heads, head_dim), dtype=dtype, device=device) for _ in range(2))
+    for t in out:
+        _need_tensor("out", t, dtype, 3, device)
+        _need(t.shape == (T, kv_heads, head_dim) and t.is_contiguous(), "out must be contiguous [T, H_kv, D]")
+    with _on(device):
+        _check(load().q8kv_read_paged(_ptr(k_pages), _ptr(v_pages), k_pages.shape[0], page_tokens, stride,
+                                      _ptr(slots), T, kv_heads, head_dim, _ptr(out[0]), _ptr(out[1]),
+                                      _DTYPES[dtype], _stream(slots)))
+    return out
+
+
+def paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, head_dim=HEAD_DIM):
+    n = int(load().q8a_paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, head_dim))
+    if n < 0:
+        raise Q8AttnError(Q8A_ERR_INVALID_ARG, "invalid sizes for the paged workspace")
+    return n
+
+
+def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, scale=None, causal=True, out=None,
+               workspace=None):
+    """Attention of packed new tokens q [total_q, H, D] (fp16 or bf16) over the pages of their sequences,
+    one token to whole prompts a sequence: sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 (int32 [B + 1])
+    and kv_lens[b] keys (int32 [B], the new tokens' own keys last) in the pages block_table[b] (int32
+    [B, width]).  max_q, max_kv: bounds of the rows and keys of a sequence.  `workspace`: fp32 CUDA tensor
+    of paged_workspace_floats(...) elements (allocated here when None).  Returns [total_q, H, D]."""
+    _need_tensor("q", q, (torch.float16, torch.bfloat16), 3, q.device)
+    device = q.device
+    T, H, D = q.shape
+    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, device)
+    _need(D == head_dim, "q and the pages must have the same head_dim")
+    _need_tensor("block_table", block_table, torch.int32, 2, device)
+    B, width = block_table.shape
+    _need(width <= 1 or block_table.stride(1) == 1, "each row of block_table must be contiguous")
+    _need(B <= 1 or block_table.stride(0) == width, "block_table must be contiguous")
+    _need_index("kv_lens", kv_lens, torch.int32, B, device)
+    _need_index("cu_q", cu_q, torch.int32, B + 1, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=device)
+    else:
+        _need_tensor("out", out, q.dtype, 3, device)
+        _need(out.shape == q.shape and out.is_contiguous(), "out must be contiguous [total_q, H, D]")
+    if workspace is None:
+        workspace = torch.empty((paged_workspace_floats(B, H, kv_heads, max_q, max_kv, D),), dtype=torch.float32,
+                                device=device)
+    else:
+        _need_tensor("workspace", workspace, torch.float32, 1, device)
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
+    with _on(device):
+        _check(load().attn_paged(_ptr(q), _DTYPES[q.dtype], _token_stride("q", q), T, H, kv_heads, D, _ptr(k_pages),
+                                 _ptr(v_pages), k_pages.shape[0], page_tokens, stride, _ptr(block_table), width,
+                                 _ptr(kv_lens), _ptr(cu_q), B, max_q, max_kv, scale, int(bool(causal)), _ptr(out),
+                                 _ptr(workspace), workspace.numel(), _stream(q)))
+    return out
 
 
 def device_status(clear=True, stream=None):

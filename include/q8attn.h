@@ -15,8 +15,8 @@
  * Conventions shared by every call:
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library
  *     never allocates, frees or synchronises on its own (q8a_device_status, which
- *     says so, synchronises its stream; the first chunk-step call of the process
- *     pins one page of the library's own memory for q8a_status); every compute
+ *     says so, synchronises its stream; the first chunk-step or paged call of the
+ *     process pins one page of the library's own memory for q8a_status); every compute
  *     call is one or more asynchronous kernel launches on `stream` (a
  *     cudaStream_t passed as void*; NULL is the legacy default stream).
  *   - Return value: Q8A_OK (0) or a negative Q8A_ERR_* code.  Arguments are
@@ -61,7 +61,8 @@ extern "C" {
  * head_dim 128 and q8a_plane_stride_bytes_for.  5: the captured prefill
  * (q8a_prefill_graph_*).  6: attn_prefill_pipelined and the split calls at
  * head_dim 128, q8a_prefill_slot_floats_for, q8a_split_workspace_floats_for and
- * attn_chunk_step_split_gqa.  7: q8a_status. */
+ * attn_chunk_step_split_gqa.  7: q8a_status; the paged cache's calls and
+ * attn_rope came to it later and change no earlier call. */
 #define Q8A_ABI_VERSION 7u
 
 enum {
@@ -398,12 +399,132 @@ int q8a_prefill_graph_launch(q8a_prefill_graph *graph, void *stream);
 int q8a_prefill_graph_destroy(q8a_prefill_graph *graph);
 
 /*
+ * ---- Rotary positions and the paged cache -----------------------------------
+ *
+ * A server keeps the Q8_0 cache in pages: a pool of n_pages pages, page p at
+ * byte p * page_stride_bytes of k_pages (and of v_pages), holding for each of
+ * kv_heads heads page_tokens consecutive rows of D/32*34 bytes (rows as in the
+ * planes above).  A sequence is a row of a block table, the numbers of its pages
+ * in order; a token's row is named by its slot, page * page_tokens + offset.
+ * Tokens of all sequences are packed, one after another, with no padding.
+ *   page_tokens        a power of two, 16..4096.
+ *   page_stride_bytes  >= kv_heads*page_tokens*D/32*34, a multiple of 16.
+ *   dtype              Q8A_F16, Q8A_BF16 or (not attn_paged) Q8A_F32.
+ *   token strides      elements between tokens of a packed tensor whose heads
+ *                      are contiguous ([n_tokens][H][D] has stride H*D; a slice
+ *                      of a fused projection has the projection's width).
+ * Slots, page numbers, lengths and offsets live on the device, so a captured
+ * call may be replayed with others.  The kernels check each one: a slot, page or
+ * length beyond the pool or the table is never followed.  It is recorded, and
+ * q8a_status and q8a_device_status then return Q8A_ERR_INVALID_ARG until cleared.
+ */
+enum { Q8A_F16 = 0, Q8A_BF16 = 1, Q8A_F32 = 2 };
+enum { Q8A_ROPE_HALF = 0, Q8A_ROPE_INTERLEAVED = 1 };
+
+/*
+ * attn_rope -- rotary positions of packed queries (or keys): in every head row
+ * of token t the channel pairs (a, b) of the first rot_dim channels become
+ *   (a cos w - b sin w, a sin w + b cos w) * mscale,  w = positions[t] * inv_freq[i],
+ * pair i being channels (i, i + rot_dim/2) with Q8A_ROPE_HALF or (2i, 2i + 1)
+ * with Q8A_ROPE_INTERLEAVED; the other channels are copied.  `inverse` turns back
+ * (w -> -w): with mscale 1 it undoes the rotation, and it is the rotation's
+ * transpose, so also its gradient.  The angle is exact to 2^-25 half turns plus
+ * inv_freq's own fp64 rounding at any position; the arithmetic is fp32, rounded
+ * once to the type.
+ *   x, out      [n_tokens][H][D] of dtype with the given token strides.  out may
+ *               be x (same stride); otherwise they must not overlap.
+ *   positions   int64 [n_tokens] on the device, any value.
+ *   inv_freq    fp64 [rot_dim/2] on the device, radians per position (scaled for
+ *               long contexts as the caller wants).
+ *   rot_dim     even, 2..D.
+ * Errors: Q8A_ERR_INVALID_ARG, Q8A_ERR_MISALIGNED, Q8A_ERR_UNSUPPORTED, Q8A_ERR_CUDA.
+ */
+int attn_rope(const void *x, void *out, int32_t dtype, int64_t n_tokens, int32_t heads,
+              int32_t head_dim, int64_t x_token_stride, int64_t out_token_stride,
+              const int64_t *positions, const double *inv_freq, int32_t rot_dim, int32_t layout,
+              float mscale, int32_t inverse, void *stream);
+
+/*
+ * q8kv_append_paged -- write the keys and values of packed tokens into pages:
+ * keys rotated as attn_rope does (in fp32, not rounded in between; not at all
+ * when positions and inv_freq are NULL), both quantised as q8kv_quantize does,
+ * row t to slot slots[t] of every head.  A negative slot skips its token (padding
+ * of a captured step); bytes of other rows are not touched.  A slot should
+ * appear once: of two tokens with the same slot, parts of either may be kept.
+ *   k, v        [n_tokens][kv_heads][D] of dtype, 16-byte aligned, token strides
+ *               multiples of 16 bytes; finite.
+ *   slots       int64 [n_tokens] on the device.
+ * Errors: as attn_rope.
+ */
+int q8kv_append_paged(const void *k, const void *v, int32_t dtype, int64_t n_tokens,
+                      int32_t kv_heads, int32_t head_dim, int64_t k_token_stride,
+                      int64_t v_token_stride, const int64_t *slots, void *k_pages, void *v_pages,
+                      int64_t n_pages, int32_t page_tokens, int64_t page_stride_bytes,
+                      const int64_t *positions, const double *inv_freq, int32_t rot_dim,
+                      int32_t layout, float mscale, void *stream);
+
+/*
+ * q8kv_read_paged -- read rows back: the values d*q of the rows at `slots`, each
+ * rounded once to dtype, into k_out and v_out [n_tokens][kv_heads][D] (contiguous,
+ * 16-byte aligned).  Slots in any order and number; a negative slot leaves its
+ * token's output as it was.
+ * Errors: as attn_rope.
+ */
+int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, int32_t page_tokens,
+                    int64_t page_stride_bytes, const int64_t *slots, int64_t n_tokens,
+                    int32_t kv_heads, int32_t head_dim, void *k_out, void *v_out, int32_t dtype,
+                    void *stream);
+
+/*
+ * attn_paged -- attention of packed new tokens over their sequences' pages, from
+ * single tokens to whole prompts: for query row i of sequence b
+ *   out_i = sum_j e^(S_ij) V_j / sum_j e^(S_ij),  S_ij = scale * Q_i . K_j,
+ * over the keys j < kv_lens[b] of the sequence's pages; with `causal` only those at
+ * or before the row's position kv_lens[b] - n_q + (i - cu_q[b]), the new tokens
+ * being the sequence's last ones (their keys are appended before the call).  A
+ * row that sees no key gives 0.  Query head h reads K/V head h / (heads / kv_heads).
+ *   q            [total_q][heads][D] of Q8A_F16 or Q8A_BF16, 16-byte aligned, token
+ *                stride a multiple of 8.
+ *   block_table  int32 [batch][table_stride] on the device; only the pages that
+ *                kv_lens reaches are read.
+ *   kv_lens      int32 [batch] on the device, at most table_stride * page_tokens;
+ *                0 is allowed.
+ *   cu_q         int32 [batch + 1] on the device: sequence b's rows are
+ *                cu_q[b] .. cu_q[b + 1] - 1 of q (none is allowed); not decreasing,
+ *                at most total_q.  Rows from cu_q[batch] on are left as they were.
+ *   max_q, max_kv  upper bounds of the sequences' rows and kv_lens (they size the
+ *                launches).
+ *   out          [total_q][heads][D] of q's type, contiguous, 16-byte aligned; not q.
+ *   workspace    fp32 scratch, 16-byte aligned, of at least
+ *                q8a_paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, D)
+ *                floats; overwritten.  Calls (and captured graphs) that share one
+ *                must be ordered on one stream.
+ * Numerics: the codes enter the tensor cores exactly; scores, maxima, sums and the
+ * accumulated values are fp32; each weight is rounded once to fp16, the output
+ * once to its type.  The result does not depend on timing.  A sequence with a bad
+ * page number gets an unspecified result, the others theirs.
+ * Errors: as attn_rope; Q8A_ERR_INVALID_ARG also for a too small workspace.
+ */
+int attn_paged(const void *q, int32_t dtype, int64_t q_token_stride, int64_t total_q,
+               int32_t heads, int32_t kv_heads, int32_t head_dim, const void *k_pages,
+               const void *v_pages, int64_t n_pages, int32_t page_tokens,
+               int64_t page_stride_bytes, const int32_t *block_table, int64_t table_stride,
+               const int32_t *kv_lens, const int32_t *cu_q, int64_t batch, int64_t max_q,
+               int64_t max_kv, float scale, int32_t causal, void *out, float *workspace,
+               int64_t workspace_floats, void *stream);
+
+/* Floats of workspace attn_paged needs for these bounds; -1 for invalid sizes. */
+int64_t q8a_paged_workspace_floats(int64_t batch, int32_t heads, int32_t kv_heads, int64_t max_q,
+                                   int64_t max_kv, int32_t head_dim);
+
+/*
  * q8a_device_status -- read (and optionally clear) the status word of the
  * current device: 0 when no device-side wait has run out since the last clear.
  * Synchronises `stream`.  Returns Q8A_OK, Q8A_ERR_TIMEOUT (when the word is
  * nonzero; *status_out then holds it: bit 0 set, bits 8..15 the role that gave
- * up first: 1 softmax, 2 dequantisation, 3 producer, 4 MMA issue, 5 final drain)
- * or Q8A_ERR_CUDA.  status_out may be NULL.
+ * up first: 1 softmax, 2 dequantisation, 3 producer, 4 MMA issue, 5 final drain,
+ * 6 paged attention), Q8A_ERR_INVALID_ARG (bit 1: a paged call met an index out
+ * of range) or Q8A_ERR_CUDA.  status_out may be NULL.
  */
 int q8a_device_status(void *stream, uint32_t *status_out, int32_t clear);
 
@@ -416,12 +537,12 @@ int q8a_device_status(void *stream, uint32_t *status_out, int32_t clear);
  * the store reaches the host while the kernel runs, so the answer covers the
  * library's kernels that have run so far on any stream, not work still queued.  The word is one page of the
  * library's own memory, registered with CUDA (cudaHostRegister, mapped and
- * portable) by the first chunk-step call of the process; nothing is allocated.
+ * portable) by the first chunk-step or paged call of the process; nothing is allocated.
  * q8a_device_status with `clear` clears it too.
  *   stream   if not NULL, also asks cudaStreamQuery(stream), which does not
  *            block, and reports a CUDA error that the stream's work raised.
  * Returns Q8A_OK, Q8A_ERR_TIMEOUT (a wait ran out; q8a_last_error() names the
- * role), Q8A_ERR_CUDA (from cudaStreamQuery) or Q8A_ERR_UNSUPPORTED (the page
+ * role), Q8A_ERR_INVALID_ARG (a paged call met an index out of range), Q8A_ERR_CUDA (from cudaStreamQuery) or Q8A_ERR_UNSUPPORTED (the page
  * could not be registered: use q8a_device_status).
  */
 int q8a_status(void *stream);
