@@ -11,8 +11,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libq8attn.so")
 SOURCES = ["api.cu", "quantize.cu", "state.cu", "chunk_step.cu", "pipeline.cu", "graph.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_few.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "paged.h", "q8_codes.cuh"]
+           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_tiles.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "paged.h", "paged_seq.cuh",
+           "q8_codes.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -72,7 +72,10 @@ struct PagedArgs {
   int32_t page_shift;
   int32_t causal;
   float scale_log2;           // scale * log2(e)
-  int32_t row_limit;          // sequences of more rows (tokens * group) are another kernel's
+  int32_t row_limit;          // sequences of at most so many rows (tokens * group) are the few-row
+                              // kernel's, the others the tile kernel's
+  int32_t splits;             // tile kernel: shares of a unit's key tiles (grid rows)
+  int64_t part_ml;            // tile kernel: floats of `part` before the shares' (m, l)
   uint64_t timeout_ns;
 };
 
@@ -82,5 +85,18 @@ cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim
                              cudaStream_t stream);
 // Floats of PagedArgs::part that launch_paged_few needs.
 int64_t paged_few_floats(int32_t head_dim, int64_t rows);
+
+// Many query rows per K/V head.  The plan of a call from its bounds: blocks
+// (row units of 256 rows times K/V heads), shares of the key tiles, workspace.
+struct TilesPlan {
+  int64_t slots;
+  int32_t splits;
+  int64_t part_ml;
+  int64_t floats;
+};
+TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_kv,
+                           int32_t head_dim);
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t slots,
+                               cudaStream_t stream);
 
 }  // namespace q8a

@@ -173,13 +173,46 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
 }
 
-int64_t q8a_paged_workspace_floats(int64_t batch, int32_t heads, int32_t kv_heads, int64_t max_q, int64_t max_kv,
-                                   int32_t head_dim) {
-  if (batch < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads || max_q < 0 || max_kv < 0 ||
-      (head_dim != 64 && head_dim != 128))
+}  // extern "C"
+
+namespace {
+
+// Sequences of at most so many rows (tokens * group) go to the few-row kernel:
+// TUNE
+constexpr int64_t kFewRows = 64;
+
+// The launches of a call, from its bounds alone.
+struct Plan {
+  bool few, tiles;
+  q8a::TilesPlan t;
+  int64_t few_floats, floats;
+};
+Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, int32_t kv_heads, int64_t max_kv,
+                int32_t head_dim) {
+  Plan p{};
+  if (max_q > total_q) max_q = total_q;
+  p.tiles = max_q * group > kFewRows;
+  // a batch whose bounds leave no room for a short sequence is the tile kernel's
+  // alone (which then takes sequences of any length)
+  p.few = !p.tiles || (total_q - (batch - 1) * max_q) * group <= kFewRows;
+  if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
+  const int64_t few_rows = p.tiles ? kFewRows : max_q * group;
+  p.few_floats = p.few ? q8a::paged_few_floats(head_dim, few_rows) : 0;
+  p.floats = p.few_floats + p.t.floats;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads, int32_t kv_heads, int64_t max_q,
+                                   int64_t max_kv, int32_t head_dim) {
+  if (batch < 0 || batch > (1 << 20) || total_q < 0 || total_q >= kMaxTokens || heads <= 0 || kv_heads <= 0 ||
+      heads % kv_heads || max_q < 0 || max_kv < 0 || (head_dim != 64 && head_dim != 128))
     return -1;
-  if (batch == 0 || max_q == 0) return 0;
-  return q8a::paged_few_floats(head_dim, max_q * (heads / kv_heads));
+  if (batch == 0 || max_q == 0 || total_q == 0) return 0;
+  return plan_paged(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, head_dim).floats;
 }
 
 int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t total_q, int32_t heads, int32_t kv_heads,
@@ -201,7 +234,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   q8a::PagePool pool;
   if (int rc = check_pool(fn, k_pages, v_pages, n_pages, page_tokens, page_stride_bytes, kv_heads, head_dim, &pool))
     return rc;
-  if (!q || !out || !kv_lens || !cu_q || !workspace || (table_stride > 0 && !block_table))
+  if (!q || !out || !kv_lens || !cu_q || (table_stride > 0 && !block_table))
     return refuse(Q8A_ERR_INVALID_ARG, fn, "null pointer");
   if (table_stride < 0 || table_stride > 0x7FFFFFFFll)
     return refuse(Q8A_ERR_INVALID_ARG, fn, "table stride must be 0..2^31-1 (got %lld)", (long long)table_stride);
@@ -212,8 +245,11 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
       !aligned(kv_lens, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4))
     return refuse(Q8A_ERR_MISALIGNED, fn,
                   "q, its token stride, out and workspace need 16-byte, the index arrays 4-byte alignment");
-  if (max_q > total_q) max_q = total_q;
-  const int64_t need = q8a_paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, head_dim);
+  if (total_q * (heads / kv_heads) >= kMaxTokens)
+    return refuse(Q8A_ERR_UNSUPPORTED, fn, "total_q * heads / kv_heads must be below 2^31");
+  const Plan plan = plan_paged(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, head_dim);
+  const int64_t need = plan.floats;
+  if (need > 0 && !workspace) return refuse(Q8A_ERR_INVALID_ARG, fn, "null workspace");
   if (workspace_floats < need)
     return refuse(Q8A_ERR_INVALID_ARG, fn, "workspace of %lld floats < %lld needed", (long long)workspace_floats,
                   (long long)need);
@@ -238,11 +274,22 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   a.page_shift = pool.page_shift;
   a.causal = causal ? 1 : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.row_limit = 0x7FFFFFFF;
   a.timeout_ns = q8a::wait_timeout_ns();
   if (int rc = status_word(fn, &a.status)) return rc;
-  const cudaError_t e =
-      q8a::launch_paged_few(a, dtype, head_dim, max_q * a.group, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (plan.tiles) {
+    q8a::PagedArgs b = a;
+    b.row_limit = plan.few ? static_cast<int32_t>(kFewRows) : 0;
+    b.splits = plan.t.splits;
+    b.part = workspace + plan.few_floats;
+    b.part_ml = plan.t.part_ml;
+    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t.slots, st);
+  }
+  if (plan.few && e == cudaSuccess) {
+    a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;
+    e = q8a::launch_paged_few(a, dtype, head_dim, plan.tiles ? kFewRows : max_q * a.group, st);
+  }
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
 }
 

@@ -50,6 +50,7 @@
 
 #include "internal.h"
 #include "paged.h"
+#include "paged_seq.cuh"
 #include "ptx.cuh"
 
 namespace q8a {
@@ -142,26 +143,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Weight of a partial state with reference m under the joint reference top.
 __device__ __forceinline__ float join_weight(float m, float top) {
   return m == -INFINITY ? 0.0f : (m == top ? 1.0f : ex2_approx(m - top));
-}
-
-// A sequence as the device arrays give it, with every bound checked: rows that
-// do not exist and keys beyond the table are left out and recorded.
-struct Seq {
-  int64_t q0;      // first query row
-  int32_t n_q, kv;
-};
-__device__ __forceinline__ Seq read_seq(const PagedArgs& a, int b) {
-  Seq s;
-  int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-  const int64_t kv = a.kv_lens[b], most = i64min(a.table_stride << a.page_shift, 0x7FFF0000);
-  const bool wrong = q0 < 0 || q1 < q0 || q1 > a.total_q || kv < 0 || kv > most;
-  if (wrong) *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
-  q0 = i64max(0, i64min(q0, a.total_q));
-  q1 = i64max(q0, i64min(q1, a.total_q));
-  s.q0 = q0;
-  s.n_q = static_cast<int32_t>(q1 - q0);
-  s.kv = static_cast<int32_t>(i64max(0, i64min(kv, most)));
-  return s;
 }
 
 template <int D, int NT>

@@ -1,0 +1,812 @@
+// paged_tiles.cu -- attention of many query rows per K/V head over a paged Q8_0
+// cache: prompts and chunks of prompts.
+//
+// The function is the one of paged_few.cu.  With hundreds of rows per key the
+// bound is the tensor cores, so the products run on tcgen05 with the
+// accumulators in TMEM:
+//   S = Q K_hi^T + Q K_lo^T,   O += P V_hi (+ P V_lo),
+// where a dequantised key d c (18 significant bits) is split exactly into an fp16
+// value and an fp16 residual.  V is split the same way for fp16 outputs; for bf16
+// outputs (rounded at 2^-8) V is rounded once to fp16 (2^-11), which saves a third
+// of the products at D = 64.  Weights are rounded once to fp16, as everywhere.
+//
+// One CTA takes two tiles (A, B) of 128 rows of one (sequence, K/V head).  A row is
+// a (token, query head of the group) pair, so a dequantised key tile serves 256
+// rows whatever the group.  16 warps:
+//   WG0, WG1   softmax of A / B, one thread per row (TMEM lane).
+//   WG2        dequantisation, one thread per 34-byte block.
+//   warp 12    producer: asynchronous copies of the pages' rows into a raw ring.
+//   warp 13    issues the MMAs.
+//
+// Scores are kept in three TMEM buffers shared by the two tiles in turn: step n
+// (tile n & 1 of key tile n / 2) uses buffer n mod 3, and S of step n + 3 is issued
+// behind O's update of step n.  So the scores of a tile's next key tile are ready
+// before its softmax ends, and the softmax warps do not wait for
+// P -> O update -> next scores; with one buffer per tile they wait for
+// that chain 40 % of the time.  The room for the third buffer comes from key tiles of 96
+// keys (D = 64; N = 96 still runs at the tensor pipe's full rate) or 64 (D = 128),
+// and from O without separate residual columns.  Q is the A operand in TMEM (stored
+// there by the softmax threads, one row each), which halves the shared memory
+// that S's MMAs read; at D = 128 only tile A's fits and B's is in shared memory.
+//
+// Every wait is bounded, as in chunk_step.cu.
+
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "paged.h"
+#include "paged_seq.cuh"
+#include "ptx.cuh"
+
+namespace q8a {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int BM = 128;
+constexpr int NS = 3;            // score buffers
+constexpr int NR = 3;            // raw ring
+constexpr int ND = 2;            // dequantised K and V rings
+constexpr int kRows = 2 * BM;    // rows of a CTA
+constexpr float kLazy = 8.0f;    // the reference moves when exceeded by more than 2^8
+constexpr float kLift = 7.0f;    // weights carry 2^7, so they reach 2^15 and keep fp16's 11 bits down to 2^-21
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+template <int D>
+struct Geo {
+  static constexpr int BN = D == 64 ? 96 : 64;          // keys of a tile
+  static constexpr int RB = D / 32 * 34;                // bytes of a row
+  static constexpr int RAWB = BN * RB;
+  static constexpr int ATOMS = D / 64;                  // 64-channel swizzle columns of a tile
+  static constexpr int ATOM = BN * 128;                 // bytes of one such column
+  static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
+  static constexpr bool QB_SMEM = D == 128;             // tile B's Q in shared memory
+  // shared memory
+  static constexpr int OFF_K = 0;                       // [ND][hi | lo]
+  static constexpr int OFF_V = OFF_K + ND * 2 * TILE;   // [ND][hi | lo]
+  static constexpr int OFF_QB = OFF_V + ND * 2 * TILE;
+  static constexpr int OFF_RAW = OFF_QB + (QB_SMEM ? BM * D * 2 : 0);
+  static constexpr int OFF_BAR = OFF_RAW + NR * 2 * RAWB;
+  static constexpr int B_Q = 0, B_RAWFULL = 1, B_RAWEMPTY = B_RAWFULL + NR, B_KFULL = B_RAWEMPTY + NR,
+                       B_KEMPTY = B_KFULL + ND, B_VFULL = B_KEMPTY + ND, B_VEMPTY = B_VFULL + ND,
+                       B_SFULL = B_VEMPTY + ND, B_PFULL = B_SFULL + NS, B_PV = B_PFULL + NS, B_DRAIN = B_PV + 4,
+                       NBAR = B_DRAIN + 1;
+  static constexpr int OFF_CTL = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_CTL + 32 + 1024;      // + alignment slack
+  static_assert(SMEM <= 227 * 1024 && TILE % 1024 == 0 && OFF_RAW % 16 == 0 && RAWB % 16 == 0, "shared memory");
+  // TMEM columns
+  static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + (QB_SMEM ? 1 : 2) * (D / 2);
+  static_assert(T_END <= 512, "TMEM");
+  // registers of the softmax warpgroups and of the others: 2 x 128 x (sum) = 65536
+  static constexpr int REG_S = D == 64 ? 184 : 152, REG_O = 256 - REG_S;
+};
+
+struct Ctl {
+  uint32_t tmem;
+  uint32_t abort;
+  int32_t b;      // sequence of this CTA, or -1
+  int32_t unit;   // its row unit
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl* ctl, uint64_t budget, uint32_t* status,
+                                         bool honour_abort = true) {
+  if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (__all_sync(kFull, mbar_try_wait_sleep(bar, parity, 100000u))) return true;
+    int stop = 0;
+    if ((threadIdx.x & 31) == 0) {
+      if (honour_abort && *reinterpret_cast<volatile uint32_t*>(&ctl->abort) != 0u) {
+        stop = 1;
+      } else if (static_cast<uint64_t>(clock64() - t0) > budget) {
+        *reinterpret_cast<volatile uint32_t*>(&ctl->abort) = 1u;
+        *reinterpret_cast<volatile uint32_t*>(status) = kStatusTimeout;
+        stop = 1;
+      }
+    }
+    if (__shfl_sync(kFull, stop, 0)) return false;
+  }
+}
+
+template <uint32_t N>
+__device__ __forceinline__ void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Four signed codes as two half2, exactly (1024 + 128 + c under the exponent of
+// 1024, minus 1152).
+__device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& lo, __half2& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
+  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  lo = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  hi = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      Q8A_W8(r, 0), Q8A_W8(r, 8)
+      : "memory");
+}
+
+// The work of this CTA: rows r0 .. r0 + 255 of a (sequence, K/V head), key tiles
+// t0 .. of its share.
+struct Unit {
+  Seq sq;
+  int kvh, r0, n_rows;
+  int t0;     // first key tile of this CTA's share
+  int T[2];   // key tiles of A and B from there
+  int per;    // key tiles of a share
+};
+
+// Key tiles that rows r .. r + 127 of a sequence see.
+template <int D>
+__device__ __forceinline__ int tiles_of(const PagedArgs& a, const Seq& sq, int r, int n_rows) {
+  if (r >= n_rows) return 0;
+  const int last = min(r + BM - 1, n_rows - 1) / a.group;   // token of the last row
+  const int vis = a.causal ? min(sq.kv, sq.kv - sq.n_q + last + 1) : sq.kv;
+  return vis > 0 ? (vis + Geo<D>::BN - 1) / Geo<D>::BN : 0;
+}
+
+template <int D>
+__device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, int kvh, int split) {
+  Unit u;
+  u.sq = read_seq(a, ctl->b);
+  u.kvh = kvh;
+  u.n_rows = u.sq.n_q * a.group;
+  // the unit with the most visible keys first
+  u.r0 = ((u.n_rows + kRows - 1) / kRows - 1 - ctl->unit) * kRows;
+  const int ta = tiles_of<D>(a, u.sq, u.r0, u.n_rows), tb = tiles_of<D>(a, u.sq, u.r0 + BM, u.n_rows);
+  u.per = max(1, (max(ta, tb) + a.splits - 1) / a.splits);
+  u.t0 = split * u.per;
+  u.T[0] = max(0, min(u.per, ta - u.t0));
+  u.T[1] = max(0, min(u.per, tb - u.t0));
+  return u;
+}
+
+// Block x of the grid -> (sequence, row unit), by warp 0: the sequences' units
+// laid end to end, those of the few-row kernel left out.
+__device__ __forceinline__ void locate(const PagedArgs& a, int64_t slot, Ctl* ctl, int lane) {
+  int64_t base = 0;
+  int found = -1, unit = 0;
+  for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t n = 0;
+    if (b < a.batch) {
+      const int64_t rows = static_cast<int64_t>(read_seq(a, b).n_q) * a.group;
+      n = rows > a.row_limit && rows <= 0x7FFFFF00 ? (rows + kRows - 1) / kRows : 0;
+    }
+    int64_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const bool here = slot >= base + inc - n && slot < base + inc;
+    const unsigned who = __ballot_sync(kFull, here);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      found = b0 + src;
+      unit = static_cast<int>(__shfl_sync(kFull, slot - (base + inc - n), src));
+    }
+    base += __shfl_sync(kFull, inc, 31);
+  }
+  if (lane == 0) {
+    ctl->b = found;
+    ctl->unit = unit;
+  }
+}
+
+// Step n <-> (key tile t, tile x): A and B in turn, then the longer one alone.
+__device__ __forceinline__ int step_of(const Unit& u, int t, int x) {
+  const int m = min(u.T[0], u.T[1]);
+  return t < m ? 2 * t + x : m + t;
+}
+
+// ------------------------------------------------------------------ roles --
+
+template <int D>
+__device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int b, uint32_t sbase, Ctl* ctl) {
+  using G = Geo<D>;
+  const uint64_t budget = 2 * a.timeout_ns;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+  const int T = max(u.T[0], u.T[1]);
+  const int shift = min(a.page_shift, 5);   // pieces of 32 rows, or of a page of 16
+  const int pieces = G::BN >> shift;
+  const uint32_t bytes = static_cast<uint32_t>(G::RB) << shift;
+  const int32_t* table = a.table + b * a.table_stride;
+  const int64_t head_off = (static_cast<int64_t>(u.kvh) << a.page_shift) * G::RB;
+  auto fetch = [&](int t) -> int {
+    const int key = (u.t0 + t) * G::BN + (lane << shift);
+    return (lane < pieces && t < T && key < u.sq.kv) ? table[key >> a.page_shift] : 0;
+  };
+  int page = fetch(0);
+  int t = 0;
+  for (; t < T; ++t) {
+    const int next = fetch(t + 1);
+    const int s = t % NR;
+    if (!wait_bar(bar(G::B_RAWEMPTY + s), ((t / NR) & 1) ^ 1, ctl, budget, a.status)) break;
+    const int key0 = (u.t0 + t) * G::BN;
+    const int have = min(pieces, (u.sq.kv - key0 + (1 << shift) - 1) >> shift);   // > 0: the tile has a visible key
+    if (lane == 0) mbar_arrive_expect_tx(bar(G::B_RAWFULL + s), 2 * have * bytes);
+    __syncwarp();
+    if (lane < have) {
+      if (page < 0 || page >= a.n_pages) {
+        *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+        page = 0;
+      }
+      const int off = (key0 + (lane << shift)) & ((1 << a.page_shift) - 1);
+      const int64_t at = page * a.page_stride + head_off + static_cast<int64_t>(off) * G::RB;
+      const uint32_t dst = sbase + G::OFF_RAW + s * 2 * G::RAWB + lane * bytes;
+      bulk_load(dst, a.k + at, bytes, bar(G::B_RAWFULL + s));
+      bulk_load(dst + G::RAWB, a.v + at, bytes, bar(G::B_RAWFULL + s));
+    }
+    page = next;
+  }
+  // never leave with a copy in flight
+  for (int i = max(0, t - NR); i < t; ++i)
+    wait_bar(bar(G::B_RAWFULL + i % NR), (i / NR) & 1, ctl, budget, a.status, false);
+}
+
+// One block of one row (nine-word window w; even blocks start word-aligned, odd ones
+// two bytes into the first word) -> 16-byte chunks of the swizzled row.
+template <bool kLo>
+__device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], bool odd, uint8_t* hi_row, uint8_t* lo_row,
+                                              int chunk0, int sw) {
+  const __half2 d2 = __half2half2(__ushort_as_half(static_cast<unsigned short>(odd ? w[0] >> 16 : w[0] & 0xFFFFu)));
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t c0 = odd ? w[1 + 2 * c] : __byte_perm(w[2 * c], w[2 * c + 1], 0x5432);
+    const uint32_t c1 = odd ? w[2 + 2 * c] : __byte_perm(w[2 * c + 1], w[2 * c + 2], 0x5432);
+    __half2 q0, q1, q2, q3;
+    codes_to_half2(c0, q0, q1);
+    codes_to_half2(c1, q2, q3);
+    const __half2 h0 = __hmul2(q0, d2), h1 = __hmul2(q1, d2), h2 = __hmul2(q2, d2), h3 = __hmul2(q3, d2);
+    const int at = ((chunk0 + c) ^ sw) * 16;
+    *reinterpret_cast<uint4*>(hi_row + at) = make_uint4(h2u(h0), h2u(h1), h2u(h2), h2u(h3));
+    if (kLo) {
+      const __half2 l0 = __hfma2(q0, d2, __hneg2(h0)), l1 = __hfma2(q1, d2, __hneg2(h1));
+      const __half2 l2 = __hfma2(q2, d2, __hneg2(h2)), l3 = __hfma2(q3, d2, __hneg2(h3));
+      *reinterpret_cast<uint4*>(lo_row + at) = make_uint4(h2u(l0), h2u(l1), h2u(l2), h2u(l3));
+    }
+  }
+}
+
+// A warp takes whole (32 rows, block) groups, so that its lanes read consecutive
+// rows: 17 words apart, 32 banks (34 apart at D = 128: two lanes a bank).
+template <int D, bool kExactV>
+__device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, uint8_t* smem, uint32_t sbase, Ctl* ctl) {
+  using G = Geo<D>;
+  constexpr int kGroups = G::BN / 32 * (D / 32);   // (rows, block) groups of a tensor: 6 or 8
+  const uint64_t budget = 2 * a.timeout_ns;
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+  const int T = max(u.T[0], u.T[1]);
+  for (int t = 0; t < T; ++t) {
+    const int sr = t % NR, sd = t % ND;
+    const uint32_t fill = (t / ND) & 1;
+    if (!wait_bar(bar(G::B_RAWFULL + sr), (t / NR) & 1, ctl, budget, a.status)) return;
+    const int n_valid = min(G::BN, u.sq.kv - (u.t0 + t) * G::BN);
+    const uint8_t* raw = smem + G::OFF_RAW + sr * 2 * G::RAWB;
+    if (!wait_bar(bar(G::B_KEMPTY + sd), fill ^ 1, ctl, budget, a.status)) return;
+    bool waited_v = false;
+#pragma unroll 1
+    for (int i = warp; i < 2 * kGroups; i += 4) {
+      const bool is_v = i >= kGroups;
+      if (is_v && !waited_v) {
+        fence_proxy_async_smem();
+        mbar_arrive(bar(G::B_KFULL + sd));
+        if (!wait_bar(bar(G::B_VEMPTY + sd), fill ^ 1, ctl, budget, a.status)) return;
+        waited_v = true;
+      }
+      const int j = is_v ? i - kGroups : i;
+      const int row = (j % (G::BN / 32)) * 32 + lane, blk = j / (G::BN / 32);
+      const bool odd = blk & 1;
+      uint8_t* hi = smem + (is_v ? G::OFF_V : G::OFF_K) + sd * 2 * G::TILE + (blk >> 1) * G::ATOM + row * 128;
+      uint8_t* lo = hi + G::TILE;
+      const int chunk0 = odd ? 4 : 0;
+      if (row < n_valid) {
+        const uint32_t* p =
+            reinterpret_cast<const uint32_t*>(raw + (is_v ? G::RAWB : 0) + row * G::RB) + 17 * (blk >> 1) + (odd ? 8 : 0);
+        uint32_t w[9];
+#pragma unroll
+        for (int k = 0; k < 9; ++k) w[k] = p[k];
+        if (!kExactV && is_v)
+          dequant_block<false>(w, odd, hi, lo, chunk0, row & 7);
+        else
+          dequant_block<true>(w, odd, hi, lo, chunk0, row & 7);
+      } else {   // keys that the sequence does not have: whatever the page holds is not read
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int at = ((chunk0 + c) ^ (row & 7)) * 16;
+          *reinterpret_cast<uint4*>(hi + at) = z;
+          if (kExactV || !is_v) *reinterpret_cast<uint4*>(lo + at) = z;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(bar(G::B_VFULL + sd));
+    mbar_arrive(bar(G::B_RAWEMPTY + sr));
+  }
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred = 0;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
+template <int D, bool kExactV>
+__device__ __forceinline__ void mma_issue(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
+  using G = Geo<D>;
+  const uint64_t budget = 2 * a.timeout_ns;
+  auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+  constexpr uint32_t kIdescS = idesc_f16_f32(128, G::BN, 0, 0);
+  constexpr uint32_t kIdescO = idesc_f16_f32(128, D, 0, 1);
+  const bool leader = elect_one();
+  // K tiles K-major in 64-channel swizzle columns, k-step = 16 channels (32 bytes
+  // of the swizzled rows); V tiles MN-major: the 64-channel halves of N one column
+  // apart (leading offset), k-step = 16 keys = 2 KB.  P of keys 16k .. sits in
+  // columns 8k .. of its S buffer, Q's channels 16k .. in columns 8k .. of Q.
+  const uint64_t kdesc = smem_desc(sbase + G::OFF_K, 1024, 1024, kSwizzle128);
+  const uint64_t vdesc = smem_desc(sbase + G::OFF_V, G::ATOM, 1024, kSwizzle128);
+  const uint64_t qdesc = smem_desc(sbase + G::OFF_QB, 1024, 1024, kSwizzle128);
+  const int m = min(u.T[0], u.T[1]), N = u.T[0] + u.T[1];
+  const int longer = u.T[1] > u.T[0] ? 1 : 0;
+  auto key_tile = [&](int n) { return n < 2 * m ? n >> 1 : n - m; };
+  auto tile = [&](int n) { return n < 2 * m ? n & 1 : longer; };
+  auto commit = [&](int b) {
+    if (leader) mma_commit(bar(b));
+  };
+  // the step that reads key tile t last: B's, or A's where B has none
+  auto last = [&](int t, int x) { return x == 1 || t >= u.T[1]; };
+  auto issue_s = [&](int n) -> bool {
+    const int t = key_tile(n), x = tile(n), sd = t % ND, buf = n % NS;
+    if (!wait_bar(bar(G::B_KFULL + sd), (t / ND) & 1, ctl, budget, a.status)) return false;
+    tc_fence_after();
+    const uint32_t d = tmem + G::T_S + G::BN * buf;
+    const uint64_t kd = kdesc + static_cast<uint64_t>(sd * 2 * (G::TILE >> 4));
+    if (leader) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t kb = kd + static_cast<uint64_t>((part * G::TILE + (k >> 2) * G::ATOM + (k & 3) * 32) >> 4);
+          if (G::QB_SMEM && x == 1)
+            mma_ss(d, qdesc + static_cast<uint64_t>(((k >> 2) * BM * 128 + (k & 3) * 32) >> 4), kb, kIdescS,
+                   (part | k) != 0 ? 1u : 0u);
+          else
+            mma_ts(d, tmem + G::T_Q + (D / 2) * x + 8 * k, kb, kIdescS, (part | k) != 0 ? 1u : 0u);
+        }
+    }
+    commit(G::B_SFULL + buf);
+    if (last(t, x)) commit(G::B_KEMPTY + sd);
+    return true;
+  };
+  bool ok = wait_bar(bar(G::B_Q), 0, ctl, budget, a.status);
+  tc_fence_after();
+  for (int n = 0; ok && n < min(NS, N); ++n) ok = issue_s(n);
+  for (int n = 0; ok && n < N; ++n) {
+    const int t = key_tile(n), x = tile(n), sd = t % ND, buf = n % NS;
+    if (!wait_bar(bar(G::B_VFULL + sd), (t / ND) & 1, ctl, budget, a.status) ||
+        !wait_bar(bar(G::B_PFULL + buf), (n / NS) & 1, ctl, budget, a.status))
+      break;
+    tc_fence_after();
+    const uint32_t o = tmem + G::T_O + D * x, p = tmem + G::T_S + G::BN * buf;
+    const uint64_t vd = vdesc + static_cast<uint64_t>(sd * 2 * (G::TILE >> 4));
+    if (leader) {
+#pragma unroll
+      for (int part = 0; part < (kExactV ? 2 : 1); ++part)
+#pragma unroll
+        for (int k = 0; k < G::BN / 16; ++k)
+          mma_ts(o, p + 8 * k, vd + static_cast<uint64_t>((part * G::TILE + k * 2048) >> 4), kIdescO, 1u);
+    }
+    commit(G::B_PV + 2 * x + (t & 1));
+    if (last(t, x)) commit(G::B_VEMPTY + sd);
+    if (n + NS < N) ok = issue_s(n + NS);
+  }
+  // never leave with an MMA in flight
+  commit(G::B_DRAIN);
+  __syncwarp();
+  wait_bar(bar(G::B_DRAIN), 0, ctl, budget, a.status, false);
+}
+
+template <typename QT, int D>
+__device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, int64_t slot, uint8_t* smem,
+                                        uint32_t sbase, uint32_t tmem, Ctl* ctl) {
+  using G = Geo<D>;
+  constexpr int BN = G::BN;
+  const uint64_t budget = 2 * a.timeout_ns;
+  const int lane_row = threadIdx.x & 127;
+  const uint32_t lane_off = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
+  auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+  const int row = u.r0 + x * BM + lane_row;
+  const bool active = row < u.n_rows;
+  const int tok = row / a.group;
+  const int head = u.kvh * a.group + row - tok * a.group;
+  const uint32_t t_o = tmem + lane_off + G::T_O + D * x;
+  const int T = u.T[x];
+
+  // ---- Q's row, as fp16 (bf16 scaled by a power of two), into TMEM or shared memory
+  float sl2 = a.scale_log2;
+  {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + (u.sq.q0 + tok) * a.q_stride +
+                                                      static_cast<int64_t>(head) * D);
+    float up = 1.0f;
+    if (!std::is_same<QT, __half>::value) {
+      uint32_t top = 0;
+      if (active) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = __ldg(src + i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        }
+      }
+      const int e = static_cast<int>(top >> 7);
+      const int f = (e == 0 || e == 255) ? 0 : min(141 - e, 100);
+      up = __int_as_float((127 + f) << 23);
+      sl2 *= __int_as_float((127 - f) << 23);
+    }
+#pragma unroll 1
+    for (int h = 0; h < D / 64; ++h) {   // 64 channels at a time
+      uint32_t q[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (active) v = __ldg(src + 8 * h + i);
+        q[4 * i] = v.x;
+        q[4 * i + 1] = v.y;
+        q[4 * i + 2] = v.z;
+        q[4 * i + 3] = v.w;
+      }
+      if (!std::is_same<QT, __half>::value) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          q[i] = pack_half2(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xFFFF0000u) * up);
+      }
+      if (G::QB_SMEM && x == 1) {
+        uint8_t* dst = smem + G::OFF_QB + h * BM * 128 + lane_row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(dst + ((c ^ (lane_row & 7)) * 16)) =
+              make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
+      } else {
+        tmem_st32(tmem + lane_off + G::T_Q + (D / 2) * x + 32 * h, q);
+      }
+    }
+#pragma unroll 1
+    for (int h = 0; h < D / 32; ++h) {   // O = 0
+      uint32_t z[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = 0u;
+      tmem_st32(t_o + 32 * h, z);
+    }
+    tmem_wait_st();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    mbar_arrive(bar(G::B_Q));
+  }
+
+  float m_run = -INFINITY, l_run = 0.0f;
+  const float2 sl22 = make_float2(sl2, sl2);
+  // keys that this row, and that every row of the tile, sees
+  const int lim = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + tok + 1) : u.sq.kv;
+  const int clear = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + (u.r0 + x * BM) / a.group + 1) : u.sq.kv;
+  // O's update of step t - 1 may still run when the scores of step t are there, but
+  // that of t - 3 does not (the scores were issued behind it).  Two barriers in turn,
+  // so that a wait for step t - 1 cannot take an older phase's parity for its own.
+  auto wait_pv = [&](int t) {
+    return wait_bar(bar(G::B_PV + 2 * x + (t & 1)), (t >> 1) & 1, ctl, budget, a.status);
+  };
+#pragma unroll 1
+  for (int t = 0; t < T; ++t) {
+    const int n = step_of(u, t, x), buf = n % NS;
+    const uint32_t t_s = tmem + lane_off + G::T_S + BN * buf;
+    if (!wait_bar(bar(G::B_SFULL + buf), (n / NS) & 1, ctl, budget, a.status)) return;
+    tc_fence_after();
+    uint32_t s[BN / 32][32];
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) tmem_ld32(t_s + 32 * i, s[i]);
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) tmem_wait_ld(s[i]);
+    const int key0 = (u.t0 + t) * BN;
+    if (__builtin_expect(key0 + BN > clear, 0)) {
+      const int li = lim - key0;
+#pragma unroll
+      for (int j = 0; j < BN; ++j)
+        if (j >= li) s[j / 32][j % 32] = __float_as_uint(-INFINITY);
+    }
+    float pm[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pm[i] = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < BN / 2; ++p)
+      pm[p & 7] = max3(pm[p & 7], __uint_as_float(s[p / 16][2 * p % 32]), __uint_as_float(s[p / 16][2 * p % 32 + 1]));
+    const float mx = fmaxf(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], max3(pm[5], pm[6], pm[7]))) * sl2;
+    float alpha = 1.0f;
+    const bool move = mx > m_run + kLazy;   // the reference moves
+    if (move) {
+      alpha = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - mx);
+      m_run = mx;
+    }
+    const float ref = m_run == -INFINITY ? 0.0f : m_run - kLift;
+    const float2 nm2 = make_float2(-ref, -ref);
+    float2 rs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rs[i] = make_float2(0.0f, 0.0f);
+    uint32_t p[BN / 2];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) {
+      const float2 sv = make_float2(__uint_as_float(s[i / 16][2 * i % 32]), __uint_as_float(s[i / 16][2 * i % 32 + 1]));
+      const float2 e = __ffma2_rn(sv, sl22, nm2);
+      const float2 w = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+      rs[i & 3] = __fadd2_rn(rs[i & 3], w);
+      p[i] = pack_half2(w.x, w.y);
+    }
+    tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&p[0]));
+    if (BN == 96) tmem_st16(t_s + 32, &p[BN / 2 - 16]);
+    if (__any_sync(kFull, move) && t > 0) {
+      // O is free once its update of the step before has completed
+      if (!wait_pv(t - 1)) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int h = 0; h < D / 32; ++h) {
+        uint32_t o[32];
+        tmem_ld32(t_o + 32 * h, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st32(t_o + 32 * h, o);
+      }
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(G::B_PFULL + buf));
+    const float2 r = __fadd2_rn(__fadd2_rn(rs[0], rs[1]), __fadd2_rn(rs[2], rs[3]));
+    // the largest weight counts as it was rounded, so that a row dominated by
+    // one key divides by exactly that key's weight
+    float fix = 0.0f;
+    if (mx != -INFINITY) {
+      const float w = ex2_approx(mx - ref);
+      fix = __half2float(__float2half_rn(w)) - w;
+    }
+    l_run = fmaf(l_run, alpha, (r.x + r.y) + fix);
+  }
+  if (T > 0) {
+    if ((T > 1 && !wait_pv(T - 2)) || !wait_pv(T - 1)) return;
+    tc_fence_after();
+  }
+  if (a.splits > 1) {
+    // the share's partial state; shares without key tiles are not read
+    if (T == 0) return;
+    const int64_t at = (slot * a.splits + blockIdx.y) * kRows + x * BM + lane_row;
+    if (active) {
+      float2* ml = reinterpret_cast<float2*>(a.part + a.part_ml);
+      ml[at] = make_float2(m_run, l_run);
+    }
+    float4* dst = reinterpret_cast<float4*>(a.part + at * D);
+#pragma unroll 1
+    for (int h = 0; h < D / 32; ++h) {
+      uint32_t o[32];
+      tmem_ld32(t_o + 32 * h, o);
+      tmem_wait_ld(o);
+      if (active)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[8 * h + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+    }
+    return;
+  }
+  const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<QT*>(a.out) + ((u.sq.q0 + tok) * a.heads + head) * D);
+#pragma unroll 1
+  for (int h = 0; h < D / 32; ++h) {
+    uint32_t o[32];
+    tmem_ld32(t_o + 32 * h, o);
+    tmem_wait_ld(o);
+    if (active) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y0 = __uint_as_float(o[8 * i + 2 * k]) * inv, y1 = __uint_as_float(o[8 * i + 2 * k + 1]) * inv;
+          if (std::is_same<QT, __half>::value) {
+            y[k] = pack_half2(y0, y1);
+          } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(y0, y1);
+            y[k] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        }
+        dst[4 * h + i] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+  }
+}
+
+template <typename QT, int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
+  using G = Geo<D>;
+  constexpr bool kExactV = std::is_same<QT, __half>::value;
+  extern __shared__ uint8_t smem_raw[];
+  pdl_launch_dependents();
+  pdl_wait();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + G::OFF_CTL);
+  const int warp = threadIdx.x >> 5, wg = warp >> 2;
+  const int64_t slot = blockIdx.x;   // row unit * kv_heads + K/V head
+  if (warp == 0) locate(a, slot / a.kv_heads, ctl, threadIdx.x & 31);
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < G::NBAR; ++i) {
+      uint32_t count = 1;
+      if (i == G::B_Q) count = 256;                                      // softmax threads
+      if (i >= G::B_RAWEMPTY && i < G::B_RAWEMPTY + NR) count = 128;     // dequantising threads
+      if (i >= G::B_KFULL && i < G::B_KFULL + ND) count = 128;
+      if (i >= G::B_VFULL && i < G::B_VFULL + ND) count = 128;
+      if (i >= G::B_PFULL && i < G::B_PFULL + NS) count = 128;           // softmax threads of a tile
+      mbar_init(sbase + G::OFF_BAR + 8u * i, count);
+    }
+    ctl->abort = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ctl->b < 0) return;   // uniform over the CTA: more blocks than row units
+  const int b = ctl->b;
+  const Unit u = make_unit<D>(a, ctl, static_cast<int>(slot % a.kv_heads), blockIdx.y);
+  if (a.splits > 1 && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
+  if (warp == 13) {
+    tmem_alloc(sbase + G::OFF_CTL, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  if (wg < 2) {
+    reg_alloc<G::REG_S>();
+    softmax<QT, D>(a, u, wg, slot, smem, sbase, tmem, ctl);
+  } else {
+    reg_dealloc<G::REG_O>();
+    if (wg == 2)
+      dequant<D, kExactV>(a, u, smem, sbase, ctl);
+    else if (warp == 12)
+      producer<D>(a, u, b, sbase, ctl);
+    else if (warp == 13)
+      mma_issue<D, kExactV>(a, u, sbase, tmem, ctl);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the shares of a unit's rows, a warp per row, in order.
+template <typename QT, int D>
+__global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a) {
+  __shared__ Ctl ctl;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t slot = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) locate(a, slot / a.kv_heads, &ctl, lane);
+  __syncthreads();
+  if (ctl.b < 0) return;
+  const int kvh = static_cast<int>(slot % a.kv_heads);
+  const Unit u = make_unit<D>(a, &ctl, kvh, 0);
+  const int in_unit = blockIdx.y * 8 + warp;
+  const int row = u.r0 + in_unit;
+  if (row >= u.n_rows) return;
+  const int tiles = tiles_of<D>(a, u.sq, u.r0 + in_unit / BM * BM, u.n_rows);
+  const int n = (tiles + u.per - 1) / u.per;   // shares with key tiles of this row's tile
+  const float2* ml = reinterpret_cast<const float2*>(a.part + a.part_ml);
+  const int64_t at0 = slot * a.splits * kRows + in_unit;
+  float top = -INFINITY;
+  for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + static_cast<int64_t>(z) * kRows].x);
+  float l = 0.0f, y[D / 32] = {};
+  for (int z = 0; z < n; ++z) {
+    const int64_t at = at0 + static_cast<int64_t>(z) * kRows;
+    const float2 v = ml[at];
+    const float w = v.x == -INFINITY ? 0.0f : (v.x == top ? 1.0f : ex2_approx(v.x - top));
+    l = fmaf(w, v.y, l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) y[i] = fmaf(w, a.part[at * D + 32 * i + lane], y[i]);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = row / a.group;
+  QT* dst = static_cast<QT*>(a.out) + ((u.sq.q0 + tok) * a.heads + kvh * a.group + row - tok * a.group) * D;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    if (std::is_same<QT, __half>::value)
+      reinterpret_cast<__half*>(dst)[32 * i + lane] = __float2half_rn(y[i] * inv);
+    else
+      reinterpret_cast<__nv_bfloat16*>(dst)[32 * i + lane] = __float2bfloat16_rn(y[i] * inv);
+  }
+}
+
+template <typename QT, int D>
+cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream) {
+  using G = Geo<D>;
+  auto kernel = paged_tiles_kernel<QT, D>;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e != cudaSuccess) return e;
+    // the register split draws on the launch's allocation: with fewer registers an
+    // increase could wait for ever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kThreads != 65536 || fa.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
+    configured_device = dev;
+  }
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(a.splits));
+  e = launch_kernel(kernel, grid, dim3(kThreads), G::SMEM, stream, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return launch_kernel(paged_tiles_join_kernel<QT, D>, dim3(grid.x, kRows / 8), dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_kv,
+                           int32_t head_dim) {
+  TilesPlan p;
+  int64_t units = batch * ((max_rows + kRows - 1) / kRows);
+  if (units > total_rows / kRows + batch) units = total_rows / kRows + batch;
+  p.slots = units * kv_heads;
+  // One CTA runs on an SM at a time.  Fewer units than SMs share their key tiles among
+  // as many CTAs as fit into one wave, of at least eight key tiles each.
+  constexpr int64_t kSms = 152;
+  const int64_t bn = head_dim == 64 ? Geo<64>::BN : Geo<128>::BN;
+  int64_t n = p.slots > 0 ? kSms / p.slots : 1;
+  if (n > max_kv / (8 * bn)) n = max_kv / (8 * bn);
+  p.splits = static_cast<int32_t>(n < 1 ? 1 : n);
+  p.part_ml = p.splits > 1 ? p.slots * p.splits * kRows * head_dim : 0;
+  p.floats = p.splits > 1 ? p.part_ml + p.slots * p.splits * kRows * 2 : 0;
+  return p;
+}
+
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t slots,
+                               cudaStream_t stream) {
+  if (slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (dtype == kF16)
+    return head_dim == 64 ? launch_tiles<__half, 64>(a, slots, stream) : launch_tiles<__half, 128>(a, slots, stream);
+  return head_dim == 64 ? launch_tiles<__nv_bfloat16, 64>(a, slots, stream)
+                        : launch_tiles<__nv_bfloat16, 128>(a, slots, stream);
+}
+
+}  // namespace q8a

@@ -67,7 +67,7 @@ SIGNATURES = {
     "q8kv_read_paged": (ctypes.c_int, [_P, _P, _I64, _I32, _I64, _P, _I64, _I32, _I32, _P, _P, _I32, _P]),
     "attn_paged": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
                                   _P, _P, _I64, _I64, _I64, _F, _I32, _P, _P, _I64, _P]),
-    "q8a_paged_workspace_floats": (_I64, [_I64, _I32, _I32, _I64, _I64, _I32]),
+    "q8a_paged_workspace_floats": (_I64, [_I64, _I64, _I32, _I32, _I64, _I64, _I32]),
     "q8a_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_U32), _I32]),
     "q8a_status": (ctypes.c_int, [_P]),
     "q8a_set_wait_timeout_ns": (ctypes.c_int, [_U64]),
@@ -526,8 +526,8 @@ def q8kv_read_paged(k_pages, v_pages, slots, dtype=torch.float16, out=None):
     return out
 
 
-def paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, head_dim=HEAD_DIM):
-    n = int(load().q8a_paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, head_dim))
+def paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim=HEAD_DIM):
+    n = int(load().q8a_paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim))
     if n < 0:
         raise Q8AttnError(Q8A_ERR_INVALID_ARG, "invalid sizes for the paged workspace")
     return n
@@ -559,7 +559,7 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
         _need_tensor("out", out, q.dtype, 3, device)
         _need(out.shape == q.shape and out.is_contiguous(), "out must be contiguous [total_q, H, D]")
     if workspace is None:
-        workspace = torch.empty((paged_workspace_floats(B, H, kv_heads, max_q, max_kv, D),), dtype=torch.float32,
+        workspace = torch.empty((paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D),), dtype=torch.float32,
                                 device=device)
     else:
         _need_tensor("workspace", workspace, torch.float32, 1, device)

@@ -493,15 +493,16 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *                cu_q[b] .. cu_q[b + 1] - 1 of q (none is allowed); not decreasing,
  *                at most total_q.  Rows from cu_q[batch] on are left as they were.
  *   max_q, max_kv  upper bounds of the sequences' rows and kv_lens (they size the
- *                launches).
+ *                launches; rows beyond max_q may be left as they were).
  *   out          [total_q][heads][D] of q's type, contiguous, 16-byte aligned; not q.
  *   workspace    fp32 scratch, 16-byte aligned, of at least
- *                q8a_paged_workspace_floats(batch, heads, kv_heads, max_q, max_kv, D)
- *                floats; overwritten.  Calls (and captured graphs) that share one
+ *                q8a_paged_workspace_floats(batch, total_q, heads, kv_heads,
+ *                max_q, max_kv, D) floats; overwritten.  Calls (and captured graphs) that share one
  *                must be ordered on one stream.
- * Numerics: the codes enter the tensor cores exactly; scores, maxima, sums and the
- * accumulated values are fp32; each weight is rounded once to fp16, the output
- * once to its type.  The result does not depend on timing.  A sequence with a bad
+ * Numerics: keys and values enter the tensor cores exactly (with bf16 output and
+ * more than 64 rows per K/V head, values rounded once to fp16); scores, maxima, sums
+ * and the accumulated values are fp32; each weight is rounded once to fp16, the
+ * output once to its type.  Values d*q are within fp16's range.  The result does not depend on timing.  A sequence with a bad
  * page number gets an unspecified result, the others theirs.
  * Errors: as attn_rope; Q8A_ERR_INVALID_ARG also for a too small workspace.
  */
@@ -514,8 +515,8 @@ int attn_paged(const void *q, int32_t dtype, int64_t q_token_stride, int64_t tot
                int64_t workspace_floats, void *stream);
 
 /* Floats of workspace attn_paged needs for these bounds; -1 for invalid sizes. */
-int64_t q8a_paged_workspace_floats(int64_t batch, int32_t heads, int32_t kv_heads, int64_t max_q,
-                                   int64_t max_kv, int32_t head_dim);
+int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads, int32_t kv_heads,
+                                   int64_t max_q, int64_t max_kv, int32_t head_dim);
 
 /*
  * q8a_device_status -- read (and optionally clear) the status word of the

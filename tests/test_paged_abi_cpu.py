@@ -82,14 +82,14 @@ def test_attention_refusals(lib):
         assert call(**kw) == bad, kw
     for kw in (dict(q=A8), dict(out=A8), dict(ws=A8), dict(qs=516), dict(kp=A8), dict(lens=P(0x100002))):
         assert call(**kw) == mis, kw
-    for kw in (dict(D=96), dict(dtype=2)):
+    for kw in (dict(D=96), dict(dtype=2), dict(total=1 << 29)):
         assert call(**kw) == uns, kw
     for kw in (dict(batch=0, q=N), dict(total=0, q=N), dict(mq=0, q=N)):
         assert call(**kw) == Q.Q8A_OK
-    assert lib.q8a_paged_workspace_floats(1, 8, 3, 1, 1, 64) == -1
-    assert lib.q8a_paged_workspace_floats(1, 8, 2, 1, 1, 96) == -1
-    assert lib.q8a_paged_workspace_floats(0, 8, 2, 1, 1, 64) == 0
-    assert lib.q8a_paged_workspace_floats(1, 8, 2, 1, 1, 64) > 0
+    assert lib.q8a_paged_workspace_floats(1, 1, 8, 3, 1, 1, 64) == -1
+    assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1, 96) == -1
+    assert lib.q8a_paged_workspace_floats(0, 1, 8, 2, 1, 1, 64) == 0
+    assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1, 64) > 0
 
 
 def test_rope_frequencies():
