@@ -12,22 +12,28 @@
 //
 // One CTA takes two tiles (A, B) of 128 rows of one (sequence, K/V head).  A row is
 // a (token, query head of the group) pair, so a dequantised key tile serves 256
-// rows whatever the group.  16 warps:
-//   WG0, WG1   softmax of A / B, one thread per row (TMEM lane).
-//   WG2        dequantisation, one thread per 34-byte block.
-//   warp 12    producer: asynchronous copies of the pages' rows into a raw ring.
-//   warp 13    issues the MMAs.
+// rows whatever the group.  Warps:
+//   0-7     softmax of A / B, one thread per row (TMEM lane);
+//   12      producer: asynchronous copies of the pages' rows into a raw ring;
+//   13, 14  issue the MMAs of S and of O.  One warp for both spends about 1,340 cycles a
+//           step at D = 64 on its waits and issues, against 768 of tensor work; apart,
+//           neither is the limit (key tiles of 96 keys, 256 rows: 654 -> 701 TFLOP/s).
+//   others  dequantisation, a lane per 34-byte block: nine warps at D = 64, where five
+//           were the limit (701 -> 807 TFLOP/s), five at D = 128, where nine take
+//           shared memory from the MMAs (803 -> 697).
 //
-// Scores are kept in three TMEM buffers shared by the two tiles in turn: step n
-// (tile n & 1 of key tile n / 2) uses buffer n mod 3, and S of step n + 3 is issued
-// behind O's update of step n.  So the scores of a tile's next key tile are ready
-// before its softmax ends, and the softmax warps do not wait for
-// P -> O update -> next scores; with one buffer per tile they wait for
-// that chain 40 % of the time.  The room for the third buffer comes from key tiles of 96
-// keys (D = 64; N = 96 still runs at the tensor pipe's full rate) or 64 (D = 128),
-// and from O without separate residual columns.  Q is the A operand in TMEM (stored
-// there by the softmax threads, one row each), which halves the shared memory
-// that S's MMAs read; at D = 128 only tile A's fits and B's is in shared memory.
+// D = 64: key tiles of 96 keys and three score buffers in TMEM, which the steps (A and B
+// of each key tile in turn) use one after another, so that the scores of a tile's next key
+// tile are ready before its softmax ends.  D = 128: key tiles of 64 keys and two buffers;
+// TMEM then has room for both Q tiles.  Q is the A operand in TMEM (stored there by the
+// softmax threads, one row each): 64 keys take 32 cycles a k-step so, 48 with Q in
+// shared memory, and with B's Q there for a third buffer D = 128 reached 747 TFLOP/s
+// instead of 803.  O has no separate columns for the residuals of V.
+//
+// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 807 (fp16) and
+// 821 (bf16) TFLOP/s, D = 128 822 and 900, of 1,699 sustained for a plain bf16 product;
+// K's residuals make S cost twice its nominal work, V's (fp16) O.  At D = 64 softmax
+// (1,290 cycles a step), dequantisation and MMA issue are now within 20 % of one another.
 //
 // Every wait is bounded, as in chunk_step.cu.
 
@@ -44,10 +50,7 @@
 namespace q8a {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int BM = 128;
-constexpr int NS = 3;            // score buffers
-constexpr int NR = 3;            // raw ring
 constexpr int ND = 2;            // dequantised K and V rings
 constexpr int kRows = 2 * BM;    // rows of a CTA
 constexpr float kLazy = 8.0f;    // the reference moves when exceeded by more than 2^8
@@ -62,7 +65,11 @@ struct Geo {
   static constexpr int ATOMS = D / 64;                  // 64-channel swizzle columns of a tile
   static constexpr int ATOM = BN * 128;                 // bytes of one such column
   static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
-  static constexpr bool QB_SMEM = D == 128;             // tile B's Q in shared memory
+  static constexpr int NR = D == 64 ? 4 : 3;            // raw ring
+  static constexpr int NS = D == 64 ? 3 : 2;            // score buffers
+  static constexpr int kThreads = D == 64 ? 640 : 512;
+  static constexpr int kDq = kThreads / 32 - 11;        // dequantising warps
+  static constexpr bool QB_SMEM = false;             // tile B's Q in shared memory
   // shared memory
   static constexpr int OFF_K = 0;                       // [ND][hi | lo]
   static constexpr int OFF_V = OFF_K + ND * 2 * TILE;   // [ND][hi | lo]
@@ -71,16 +78,17 @@ struct Geo {
   static constexpr int OFF_BAR = OFF_RAW + NR * 2 * RAWB;
   static constexpr int B_Q = 0, B_RAWFULL = 1, B_RAWEMPTY = B_RAWFULL + NR, B_KFULL = B_RAWEMPTY + NR,
                        B_KEMPTY = B_KFULL + ND, B_VFULL = B_KEMPTY + ND, B_VEMPTY = B_VFULL + ND,
-                       B_SFULL = B_VEMPTY + ND, B_PFULL = B_SFULL + NS, B_PV = B_PFULL + NS, B_DRAIN = B_PV + 4,
-                       NBAR = B_DRAIN + 1;
+                       B_SFULL = B_VEMPTY + ND, B_PFULL = B_SFULL + NS, B_PV = B_PFULL + NS, B_ODONE = B_PV + NS, B_DRAIN = B_ODONE + 2,
+                       NBAR = B_DRAIN + 2;
   static constexpr int OFF_CTL = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_CTL + 32 + 1024;      // + alignment slack
   static_assert(SMEM <= 227 * 1024 && TILE % 1024 == 0 && OFF_RAW % 16 == 0 && RAWB % 16 == 0, "shared memory");
   // TMEM columns
   static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + (QB_SMEM ? 1 : 2) * (D / 2);
   static_assert(T_END <= 512, "TMEM");
-  // registers of the softmax warpgroups and of the others: 2 x 128 x (sum) = 65536
-  static constexpr int REG_S = D == 64 ? 184 : 152, REG_O = 256 - REG_S;
+  // registers of the softmax warpgroups and of the others, out of the launch's REG_L a thread
+  static constexpr int REG_S = D == 64 ? 144 : 136, REG_O = D == 64 ? 64 : 120, REG_L = D == 64 ? 96 : 128;
+  static_assert(2 * 128 * REG_S + (kThreads - 256) * REG_O <= kThreads * REG_L, "register split");
 };
 
 struct Ctl {
@@ -244,8 +252,8 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
   int t = 0;
   for (; t < T; ++t) {
     const int next = fetch(t + 1);
-    const int s = t % NR;
-    if (!wait_bar(bar(G::B_RAWEMPTY + s), ((t / NR) & 1) ^ 1, ctl, budget, a.status)) break;
+    const int s = t % G::NR;
+    if (!wait_bar(bar(G::B_RAWEMPTY + s), ((t / G::NR) & 1) ^ 1, ctl, budget, a.status)) break;
     const int key0 = (u.t0 + t) * G::BN;
     const int have = min(pieces, (u.sq.kv - key0 + (1 << shift) - 1) >> shift);   // > 0: the tile has a visible key
     if (lane == 0) mbar_arrive_expect_tx(bar(G::B_RAWFULL + s), 2 * have * bytes);
@@ -264,8 +272,8 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
     page = next;
   }
   // never leave with a copy in flight
-  for (int i = max(0, t - NR); i < t; ++i)
-    wait_bar(bar(G::B_RAWFULL + i % NR), (i / NR) & 1, ctl, budget, a.status, false);
+  for (int i = max(0, t - G::NR); i < t; ++i)
+    wait_bar(bar(G::B_RAWFULL + i % G::NR), (i / G::NR) & 1, ctl, budget, a.status, false);
 }
 
 // One block of one row (nine-word window w; even blocks start word-aligned, odd ones
@@ -292,62 +300,74 @@ __device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], bool odd, 
   }
 }
 
-// A warp takes whole (32 rows, block) groups, so that its lanes read consecutive
-// rows: 17 words apart, 32 banks (34 apart at D = 128: two lanes a bank).
-template <int D, bool kExactV>
-__device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, uint8_t* smem, uint32_t sbase, Ctl* ctl) {
+// One (32 rows, block) group of a tile: the lanes read consecutive rows, 17 words apart
+// (32 banks; 34 apart at D = 128: two lanes a bank).
+template <int D, bool kLo>
+__device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile, int group, int n_valid, int lane) {
   using G = Geo<D>;
-  constexpr int kGroups = G::BN / 32 * (D / 32);   // (rows, block) groups of a tensor: 6 or 8
+  const int row = (group % (G::BN / 32)) * 32 + lane, blk = group / (G::BN / 32);
+  const bool odd = blk & 1;
+  uint8_t* hi = tile + (blk >> 1) * G::ATOM + row * 128;
+  uint8_t* lo = hi + G::TILE;
+  const int chunk0 = odd ? 4 : 0;
+  if (row < n_valid) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(raw + row * G::RB) + 17 * (blk >> 1) + (odd ? 8 : 0);
+    uint32_t c[9];
+#pragma unroll
+    for (int k = 0; k < 9; ++k) c[k] = p[k];
+    dequant_block<kLo>(c, odd, hi, lo, chunk0, row & 7);
+  } else {   // keys that the sequence does not have: whatever the page holds is not read
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int at = ((chunk0 + c) ^ (row & 7)) * 16;
+      *reinterpret_cast<uint4*>(hi + at) = z;
+      if (kLo) *reinterpret_cast<uint4*>(lo + at) = z;
+    }
+  }
+}
+
+// K of key tile i + 1, then V of key tile i: V's place in the ring is free only after
+// O's update of key tile i - 2, and K must not wait behind it.  The groups go
+// round the warps from tile to tile, so five warps share twelve (sixteen) evenly.
+template <int D, bool kExactV>
+__device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w, uint8_t* smem, uint32_t sbase,
+                                        Ctl* ctl) {
+  using G = Geo<D>;
+  constexpr int kGroups = G::BN / 32 * (D / 32);   // groups of a tensor's tile: 6 or 8
   const uint64_t budget = 2 * a.timeout_ns;
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
   const int T = max(u.T[0], u.T[1]);
-  for (int t = 0; t < T; ++t) {
-    const int sr = t % NR, sd = t % ND;
-    const uint32_t fill = (t / ND) & 1;
-    if (!wait_bar(bar(G::B_RAWFULL + sr), (t / NR) & 1, ctl, budget, a.status)) return;
-    const int n_valid = min(G::BN, u.sq.kv - (u.t0 + t) * G::BN);
-    const uint8_t* raw = smem + G::OFF_RAW + sr * 2 * G::RAWB;
-    if (!wait_bar(bar(G::B_KEMPTY + sd), fill ^ 1, ctl, budget, a.status)) return;
-    bool waited_v = false;
+  int mine = w;   // this warp's next group of the iteration: K's, then V's behind them
+  for (int i = -1; i < T; ++i) {
+    const int k = i + 1;
+    if (k < T) {
+      const int sd = k % ND;
+      if (!wait_bar(bar(G::B_RAWFULL + k % G::NR), (k / G::NR) & 1, ctl, budget, a.status)) return;
+      if (!wait_bar(bar(G::B_KEMPTY + sd), ((k / ND) & 1) ^ 1, ctl, budget, a.status)) return;
+      const int n_valid = u.sq.kv - (u.t0 + k) * G::BN;
 #pragma unroll 1
-    for (int i = warp; i < 2 * kGroups; i += 4) {
-      const bool is_v = i >= kGroups;
-      if (is_v && !waited_v) {
-        fence_proxy_async_smem();
-        mbar_arrive(bar(G::B_KFULL + sd));
-        if (!wait_bar(bar(G::B_VEMPTY + sd), fill ^ 1, ctl, budget, a.status)) return;
-        waited_v = true;
-      }
-      const int j = is_v ? i - kGroups : i;
-      const int row = (j % (G::BN / 32)) * 32 + lane, blk = j / (G::BN / 32);
-      const bool odd = blk & 1;
-      uint8_t* hi = smem + (is_v ? G::OFF_V : G::OFF_K) + sd * 2 * G::TILE + (blk >> 1) * G::ATOM + row * 128;
-      uint8_t* lo = hi + G::TILE;
-      const int chunk0 = odd ? 4 : 0;
-      if (row < n_valid) {
-        const uint32_t* p =
-            reinterpret_cast<const uint32_t*>(raw + (is_v ? G::RAWB : 0) + row * G::RB) + 17 * (blk >> 1) + (odd ? 8 : 0);
-        uint32_t w[9];
-#pragma unroll
-        for (int k = 0; k < 9; ++k) w[k] = p[k];
-        if (!kExactV && is_v)
-          dequant_block<false>(w, odd, hi, lo, chunk0, row & 7);
-        else
-          dequant_block<true>(w, odd, hi, lo, chunk0, row & 7);
-      } else {   // keys that the sequence does not have: whatever the page holds is not read
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = ((chunk0 + c) ^ (row & 7)) * 16;
-          *reinterpret_cast<uint4*>(hi + at) = z;
-          if (kExactV || !is_v) *reinterpret_cast<uint4*>(lo + at) = z;
-        }
-      }
+      for (; mine < kGroups; mine += G::kDq)
+        dequant_group<D, true>(smem + G::OFF_RAW + k % G::NR * 2 * G::RAWB, smem + G::OFF_K + sd * 2 * G::TILE, mine,
+                               n_valid, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(G::B_KFULL + sd));
+      mine -= kGroups;
     }
-    fence_proxy_async_smem();
-    mbar_arrive(bar(G::B_VFULL + sd));
-    mbar_arrive(bar(G::B_RAWEMPTY + sr));
+    if (i >= 0) {
+      const int sd = i % ND;
+      if (!wait_bar(bar(G::B_VEMPTY + sd), ((i / ND) & 1) ^ 1, ctl, budget, a.status)) return;
+      const int n_valid = u.sq.kv - (u.t0 + i) * G::BN;
+#pragma unroll 1
+      for (; mine < kGroups; mine += G::kDq)
+        dequant_group<D, kExactV>(smem + G::OFF_RAW + i % G::NR * 2 * G::RAWB + G::RAWB,
+                                  smem + G::OFF_V + sd * 2 * G::TILE, mine, n_valid, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(G::B_VFULL + sd));
+      mbar_arrive(bar(G::B_RAWEMPTY + i % G::NR));
+      mine -= kGroups;
+    }
   }
 }
 
@@ -361,33 +381,35 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
-template <int D, bool kExactV>
-__device__ __forceinline__ void mma_issue(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
+// Step n's key tile and tile.
+__device__ __forceinline__ int step_key(const Unit& u, int n) {
+  const int m = min(u.T[0], u.T[1]);
+  return n < 2 * m ? n >> 1 : n - m;
+}
+__device__ __forceinline__ int step_tile(const Unit& u, int n) {
+  return n < 2 * min(u.T[0], u.T[1]) ? n & 1 : (u.T[1] > u.T[0] ? 1 : 0);
+}
+// Whether tile x's step is the one that reads key tile t last: B's, or A's where B has none.
+__device__ __forceinline__ bool last_reader(const Unit& u, int t, int x) { return x == 1 || t >= u.T[1]; }
+
+// Scores.  K tiles K-major in 64-channel swizzle columns, a k-step 16 channels (32
+// bytes of the swizzled rows); Q's channels 16 k .. in TMEM columns 8 k .. of Q.
+template <int D>
+__device__ __forceinline__ void score_mma(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
   using G = Geo<D>;
   const uint64_t budget = 2 * a.timeout_ns;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-  constexpr uint32_t kIdescS = idesc_f16_f32(128, G::BN, 0, 0);
-  constexpr uint32_t kIdescO = idesc_f16_f32(128, D, 0, 1);
+  constexpr uint32_t kIdesc = idesc_f16_f32(128, G::BN, 0, 0);
   const bool leader = elect_one();
-  // K tiles K-major in 64-channel swizzle columns, k-step = 16 channels (32 bytes
-  // of the swizzled rows); V tiles MN-major: the 64-channel halves of N one column
-  // apart (leading offset), k-step = 16 keys = 2 KB.  P of keys 16k .. sits in
-  // columns 8k .. of its S buffer, Q's channels 16k .. in columns 8k .. of Q.
   const uint64_t kdesc = smem_desc(sbase + G::OFF_K, 1024, 1024, kSwizzle128);
-  const uint64_t vdesc = smem_desc(sbase + G::OFF_V, G::ATOM, 1024, kSwizzle128);
   const uint64_t qdesc = smem_desc(sbase + G::OFF_QB, 1024, 1024, kSwizzle128);
-  const int m = min(u.T[0], u.T[1]), N = u.T[0] + u.T[1];
-  const int longer = u.T[1] > u.T[0] ? 1 : 0;
-  auto key_tile = [&](int n) { return n < 2 * m ? n >> 1 : n - m; };
-  auto tile = [&](int n) { return n < 2 * m ? n & 1 : longer; };
-  auto commit = [&](int b) {
-    if (leader) mma_commit(bar(b));
-  };
-  // the step that reads key tile t last: B's, or A's where B has none
-  auto last = [&](int t, int x) { return x == 1 || t >= u.T[1]; };
-  auto issue_s = [&](int n) -> bool {
-    const int t = key_tile(n), x = tile(n), sd = t % ND, buf = n % NS;
-    if (!wait_bar(bar(G::B_KFULL + sd), (t / ND) & 1, ctl, budget, a.status)) return false;
+  const int N = u.T[0] + u.T[1];
+  bool ok = wait_bar(bar(G::B_Q), 0, ctl, budget, a.status);
+  for (int n = 0; ok && n < N; ++n) {
+    const int t = step_key(u, n), x = step_tile(u, n), sd = t % ND, buf = n % G::NS;
+    if (!wait_bar(bar(G::B_KFULL + sd), (t / ND) & 1, ctl, budget, a.status)) break;
+    // the buffer's weights have been used by O's update of step n - G::NS
+    if (n >= G::NS && !wait_bar(bar(G::B_PV + buf), (n / G::NS - 1) & 1, ctl, budget, a.status)) break;
     tc_fence_after();
     const uint32_t d = tmem + G::T_S + G::BN * buf;
     const uint64_t kd = kdesc + static_cast<uint64_t>(sd * 2 * (G::TILE >> 4));
@@ -398,23 +420,38 @@ __device__ __forceinline__ void mma_issue(const PagedArgs& a, const Unit& u, uin
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t kb = kd + static_cast<uint64_t>((part * G::TILE + (k >> 2) * G::ATOM + (k & 3) * 32) >> 4);
           if (G::QB_SMEM && x == 1)
-            mma_ss(d, qdesc + static_cast<uint64_t>(((k >> 2) * BM * 128 + (k & 3) * 32) >> 4), kb, kIdescS,
+            mma_ss(d, qdesc + static_cast<uint64_t>(((k >> 2) * BM * 128 + (k & 3) * 32) >> 4), kb, kIdesc,
                    (part | k) != 0 ? 1u : 0u);
           else
-            mma_ts(d, tmem + G::T_Q + (D / 2) * x + 8 * k, kb, kIdescS, (part | k) != 0 ? 1u : 0u);
+            mma_ts(d, tmem + G::T_Q + (D / 2) * x + 8 * k, kb, kIdesc, (part | k) != 0 ? 1u : 0u);
         }
+      mma_commit(bar(G::B_SFULL + buf));
+      if (last_reader(u, t, x)) mma_commit(bar(G::B_KEMPTY + sd));
     }
-    commit(G::B_SFULL + buf);
-    if (last(t, x)) commit(G::B_KEMPTY + sd);
-    return true;
-  };
-  bool ok = wait_bar(bar(G::B_Q), 0, ctl, budget, a.status);
-  tc_fence_after();
-  for (int n = 0; ok && n < min(NS, N); ++n) ok = issue_s(n);
-  for (int n = 0; ok && n < N; ++n) {
-    const int t = key_tile(n), x = tile(n), sd = t % ND, buf = n % NS;
+    __syncwarp();
+  }
+  // never leave with an MMA in flight
+  if (leader) mma_commit(bar(G::B_DRAIN));
+  __syncwarp();
+  wait_bar(bar(G::B_DRAIN), 0, ctl, budget, a.status, false);
+}
+
+// O's updates.  V tiles MN-major: the 64-channel halves of N one column apart (leading
+// offset), a k-step 16 keys = 2 KB.  P of keys 16 k .. sits in columns 8 k .. of its S
+// buffer.
+template <int D, bool kExactV>
+__device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
+  using G = Geo<D>;
+  const uint64_t budget = 2 * a.timeout_ns;
+  auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+  constexpr uint32_t kIdesc = idesc_f16_f32(128, D, 0, 1);
+  const bool leader = elect_one();
+  const uint64_t vdesc = smem_desc(sbase + G::OFF_V, G::ATOM, 1024, kSwizzle128);
+  const int N = u.T[0] + u.T[1];
+  for (int n = 0; n < N; ++n) {
+    const int t = step_key(u, n), x = step_tile(u, n), sd = t % ND, buf = n % G::NS;
     if (!wait_bar(bar(G::B_VFULL + sd), (t / ND) & 1, ctl, budget, a.status) ||
-        !wait_bar(bar(G::B_PFULL + buf), (n / NS) & 1, ctl, budget, a.status))
+        !wait_bar(bar(G::B_PFULL + buf), (n / G::NS) & 1, ctl, budget, a.status))
       break;
     tc_fence_after();
     const uint32_t o = tmem + G::T_O + D * x, p = tmem + G::T_S + G::BN * buf;
@@ -424,16 +461,16 @@ __device__ __forceinline__ void mma_issue(const PagedArgs& a, const Unit& u, uin
       for (int part = 0; part < (kExactV ? 2 : 1); ++part)
 #pragma unroll
         for (int k = 0; k < G::BN / 16; ++k)
-          mma_ts(o, p + 8 * k, vd + static_cast<uint64_t>((part * G::TILE + k * 2048) >> 4), kIdescO, 1u);
+          mma_ts(o, p + 8 * k, vd + static_cast<uint64_t>((part * G::TILE + k * 2048) >> 4), kIdesc, 1u);
+      mma_commit(bar(G::B_PV + buf));
+      if (t == u.T[x] - 1) mma_commit(bar(G::B_ODONE + x));
+      if (last_reader(u, t, x)) mma_commit(bar(G::B_VEMPTY + sd));
     }
-    commit(G::B_PV + 2 * x + (t & 1));
-    if (last(t, x)) commit(G::B_VEMPTY + sd);
-    if (n + NS < N) ok = issue_s(n + NS);
+    __syncwarp();
   }
-  // never leave with an MMA in flight
-  commit(G::B_DRAIN);
+  if (leader) mma_commit(bar(G::B_DRAIN + 1));
   __syncwarp();
-  wait_bar(bar(G::B_DRAIN), 0, ctl, budget, a.status, false);
+  wait_bar(bar(G::B_DRAIN + 1), 0, ctl, budget, a.status, false);
 }
 
 template <typename QT, int D>
@@ -519,17 +556,11 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   // keys that this row, and that every row of the tile, sees
   const int lim = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + tok + 1) : u.sq.kv;
   const int clear = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + (u.r0 + x * BM) / a.group + 1) : u.sq.kv;
-  // O's update of step t - 1 may still run when the scores of step t are there, but
-  // that of t - 3 does not (the scores were issued behind it).  Two barriers in turn,
-  // so that a wait for step t - 1 cannot take an older phase's parity for its own.
-  auto wait_pv = [&](int t) {
-    return wait_bar(bar(G::B_PV + 2 * x + (t & 1)), (t >> 1) & 1, ctl, budget, a.status);
-  };
 #pragma unroll 1
   for (int t = 0; t < T; ++t) {
-    const int n = step_of(u, t, x), buf = n % NS;
+    const int n = step_of(u, t, x), buf = n % G::NS;
     const uint32_t t_s = tmem + lane_off + G::T_S + BN * buf;
-    if (!wait_bar(bar(G::B_SFULL + buf), (n / NS) & 1, ctl, budget, a.status)) return;
+    if (!wait_bar(bar(G::B_SFULL + buf), (n / G::NS) & 1, ctl, budget, a.status)) return;
     tc_fence_after();
     uint32_t s[BN / 32][32];
 #pragma unroll
@@ -572,9 +603,12 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     }
     tmem_st32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(&p[0]));
     if (BN == 96) tmem_st16(t_s + 32, &p[BN / 2 - 16]);
-    if (__any_sync(kFull, move) && t > 0) {
-      // O is free once its update of the step before has completed
-      if (!wait_pv(t - 1)) return;
+    if (t > 0 && __any_sync(kFull, move)) {
+      // O is free once this tile's update before, of step p, has completed.  p is n - 2
+      // (or n - 1), the buffer's earlier use p - G::NS has completed (scores n were
+      // issued behind it) and its next one waits for this step, so the phase is p's.
+      const int p = step_of(u, t - 1, x);
+      if (!wait_bar(bar(G::B_PV + p % G::NS), (p / G::NS) & 1, ctl, budget, a.status)) return;
       tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < D / 32; ++h) {
@@ -600,7 +634,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     l_run = fmaf(l_run, alpha, (r.x + r.y) + fix);
   }
   if (T > 0) {
-    if ((T > 1 && !wait_pv(T - 2)) || !wait_pv(T - 1)) return;
+    if (!wait_bar(bar(G::B_ODONE + x), 0, ctl, budget, a.status)) return;
     tc_fence_after();
   }
   if (a.splits > 1) {
@@ -653,7 +687,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
 }
 
 template <typename QT, int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
   using G = Geo<D>;
   constexpr bool kExactV = std::is_same<QT, __half>::value;
   extern __shared__ uint8_t smem_raw[];
@@ -670,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const PagedArg
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t count = 1;
       if (i == G::B_Q) count = 256;                                      // softmax threads
-      if (i >= G::B_RAWEMPTY && i < G::B_RAWEMPTY + NR) count = 128;     // dequantising threads
-      if (i >= G::B_KFULL && i < G::B_KFULL + ND) count = 128;
-      if (i >= G::B_VFULL && i < G::B_VFULL + ND) count = 128;
-      if (i >= G::B_PFULL && i < G::B_PFULL + NS) count = 128;           // softmax threads of a tile
+      if (i >= G::B_RAWEMPTY && i < G::B_RAWEMPTY + G::NR) count = 32 * G::kDq;   // dequantising threads
+      if (i >= G::B_KFULL && i < G::B_KFULL + ND) count = 32 * G::kDq;
+      if (i >= G::B_VFULL && i < G::B_VFULL + ND) count = 32 * G::kDq;
+      if (i >= G::B_PFULL && i < G::B_PFULL + G::NS) count = 128;           // softmax threads of a tile
       mbar_init(sbase + G::OFF_BAR + 8u * i, count);
     }
     ctl->abort = 0u;
@@ -697,12 +731,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const PagedArg
     softmax<QT, D>(a, u, wg, slot, smem, sbase, tmem, ctl);
   } else {
     reg_dealloc<G::REG_O>();
-    if (wg == 2)
-      dequant<D, kExactV>(a, u, smem, sbase, ctl);
-    else if (warp == 12)
+    if (warp == 12) {
       producer<D>(a, u, b, sbase, ctl);
-    else if (warp == 13)
-      mma_issue<D, kExactV>(a, u, sbase, tmem, ctl);
+    } else if (warp == 13) {
+      score_mma<D>(a, u, sbase, tmem, ctl);
+    } else if (warp == 14) {
+      value_mma<D, kExactV>(a, u, sbase, tmem, ctl);
+    } else {
+      dequant<D, kExactV>(a, u, warp < 12 ? warp - 8 : warp - 11, smem, sbase, ctl);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -771,11 +808,12 @@ cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream)
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * kThreads != 65536 || fa.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs * G::kThreads < 2 * 128 * G::REG_S + (G::kThreads - 256) * G::REG_O || fa.maxThreadsPerBlock < G::kThreads)
+      return cudaErrorInvalidConfiguration;
     configured_device = dev;
   }
   const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(a.splits));
-  e = launch_kernel(kernel, grid, dim3(kThreads), G::SMEM, stream, a);
+  e = launch_kernel(kernel, grid, dim3(G::kThreads), G::SMEM, stream, a);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch_kernel(paged_tiles_join_kernel<QT, D>, dim3(grid.x, kRows / 8), dim3(256), 0, stream, a);
 }
