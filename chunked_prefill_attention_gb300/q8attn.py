@@ -7,8 +7,8 @@ include/q8attn.h.  There is no CPU fallback: if the library is missing or fails
 to load, every call raises.
 """
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -380,52 +380,91 @@ def attn_prefill_pipelined(q_host, k_host, v_host, out_host, bufs, scale=None, c
 
 
 # ---- rotary positions and the paged cache -----------------------------------
-# The device-side checks of these calls read indices from device tensors; what
-# can be told from shapes, types and devices is refused here, before the call.
+# What can be told from shapes, types and devices is refused here, before the call;
+# the indices that device tensors hold are checked by the kernels.  A step of a
+# server makes these calls once per layer, so an accepted call costs one
+# condition: the messages are formed only by the functions that refuse.
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _need(ok, msg):
-    if not ok:
-        raise Q8AttnError(Q8A_ERR_INVALID_ARG, msg)
+def _refuse(msg):
+    raise Q8AttnError(Q8A_ERR_INVALID_ARG, msg)
 
 
-def _need_tensor(name, t, dtype, ndim, device):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == ndim and t.device == device and
-          (t.dtype in dtype if isinstance(dtype, (tuple, dict)) else t.dtype == dtype),
-          f"{name}: a {ndim}-dimensional CUDA tensor on {device} of {dtype} is needed")
+def _bad_packed(**tensors):
+    """Refuse packed [T, H, D] tensors: type, device, shape or strides."""
+    for name, t in tensors.items():
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.dtype in _DTYPES):
+            _refuse(f"{name}: a CUDA tensor [tokens, heads, head_dim] of fp16, bf16 or fp32 is needed")
+    shapes = {n: (tuple(t.shape), t.dtype, str(t.device)) for n, t in tensors.items()}
+    _refuse(f"packed tensors must agree in shape, type and device, each token's heads contiguous: {shapes}")
 
 
-def _need_index(name, t, dtype, n, device):
-    _need_tensor(name, t, dtype, 1, device)
-    _need(t.shape[0] == n and t.is_contiguous(), f"{name}: {n} contiguous values are needed, got {tuple(t.shape)}")
+def _bad_index(name, t, dtype, n, device):
+    got = (t.dtype, tuple(t.shape), str(t.device)) if isinstance(t, torch.Tensor) else type(t)
+    _refuse(f"{name}: {n} contiguous values of {dtype} on cuda:{device} are needed, got {got}")
 
 
-def _token_stride(name, t):
-    """Elements between tokens of a packed [T, H, D] tensor whose heads are contiguous."""
+def _index(name, t, dtype, n, device):
+    """Check a one-dimensional index tensor of n values; its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and
+            t.is_contiguous() and t.get_device() == device):
+        _bad_index(name, t, dtype, n, device)
+    return t.data_ptr()
+
+
+def _packed(name, t, device):
+    """(dtype code, T, H, D, token stride in elements) of a packed tensor whose heads are contiguous."""
+    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 else None
+    if code is None or t.get_device() != device:
+        _bad_packed(**{name: t})
     T, H, D = t.shape
-    _need((D <= 1 or t.stride(2) == 1) and (H <= 1 or t.stride(1) == D),
-          f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if T > 1 else max(H * D, 1)
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        _bad_packed(**{name: t})
+    return code, T, H, D, (st if T > 1 else max(H * D, 1))
+
+
+def _device_of(t):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _refuse("CUDA tensors are needed")
+    return t.get_device()
 
 
 def _pool(k_pages, v_pages, device):
-    """(kv_heads, page_tokens, head_dim, page stride in bytes) of uint8 pages [n_pages, H_kv, page_tokens,
-    row bytes], contiguous within a page (the K and V pools may be interleaved, page by page)."""
-    _need_tensor("k_pages", k_pages, torch.uint8, 4, device)
-    _need_tensor("v_pages", v_pages, torch.uint8, 4, device)
-    n, H, P, rb = k_pages.shape
-    _need(v_pages.shape == k_pages.shape and v_pages.stride() == k_pages.stride(),
-          "k_pages and v_pages must have the same shape and strides")
-    _need(rb in (68, 136), f"rows of 68 or 136 bytes are needed, got {rb}")
-    _need(k_pages[0].is_contiguous() if n else True, "each page must be contiguous")
-    return H, P, rb // 34 * 32, k_pages.stride(0) if n > 1 else H * P * rb
+    """(n_pages, kv_heads, page_tokens, head_dim, page stride in bytes) of uint8 pages [n_pages, H_kv,
+    page_tokens, row bytes], contiguous within a page (the pools may be interleaved, page by page)."""
+    ok = (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and k_pages.dim() == 4 and
+          k_pages.dtype == v_pages.dtype == torch.uint8 and k_pages.get_device() == v_pages.get_device() == device and
+          k_pages.shape == v_pages.shape and k_pages.stride() == v_pages.stride())
+    if ok:
+        n, H, P, rb = k_pages.shape
+        sn, sh, sp, sb = k_pages.stride()
+        ok = rb in (68, 136) and sb == 1 and (sp == rb or P <= 1) and (sh == P * rb or H <= 1)
+    if not ok:
+        _refuse(f"k_pages and v_pages: uint8 tensors [n_pages, kv_heads, page_tokens, 68 or 136] of the same shape "
+                f"and strides on cuda:{device}, each page contiguous, are needed")
+    return n, H, P, rb // 34 * 32, (sn if n > 1 else H * P * rb)
 
 
-def _on(device):
-    """The calls launch on the tensors' device, whichever is current."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _rope_table(inv_freq, device):
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and
+            inv_freq.is_contiguous() and inv_freq.get_device() == device):
+        _bad_index("inv_freq", inv_freq, torch.float64, "rot_dim / 2", device)
+    return inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+
+
+def _call(fn, device, *args):
+    """fn(*args, current stream of `device`) with that device current."""
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != Q8A_OK:
+        _check(rc)
 
 
 def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, scaling="linear", original_len=None, low=1.0, high=4.0,
@@ -463,20 +502,19 @@ def attn_rope(x, positions, inv_freq, interleaved=False, mscale=1.0, inverse=Fal
     """Rotary positions of packed x [T, H, D] (fp16, bf16 or fp32; a slice of a wider buffer is fine):
     the first 2 * len(inv_freq) channels of every head turned by positions [T] (int64) times inv_freq
     (fp64, see rope_inv_freq).  `out` may be x.  `inverse` turns back (the gradient of the rotation)."""
-    _need_tensor("x", x, _DTYPES, 3, x.device)
-    T, H, D = x.shape
-    _need_index("positions", positions, torch.int64, T, x.device)
-    _need_tensor("inv_freq", inv_freq, torch.float64, 1, x.device)
-    _need(inv_freq.is_contiguous(), "inv_freq must be contiguous")
+    device = _device_of(x)
+    code, T, H, D, stride = _packed("x", x, device)
+    pos = _index("positions", positions, torch.int64, T, device)
+    table, rot = _rope_table(inv_freq, device)
     if out is None:
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        out_stride = max(H * D, 1)
     else:
-        _need_tensor("out", out, x.dtype, 3, x.device)
-        _need(out.shape == x.shape, "out must have the shape of x")
-    with _on(x.device):
-        _check(load().attn_rope(_ptr(x), _ptr(out), _DTYPES[x.dtype], T, H, D, _token_stride("x", x),
-                                _token_stride("out", out), _ptr(positions), _ptr(inv_freq), 2 * inv_freq.shape[0],
-                                int(bool(interleaved)), mscale, int(bool(inverse)), _stream(x)))
+        out_code, *shape, out_stride = _packed("out", out, device)
+        if out_code != code or shape != [T, H, D]:
+            _bad_packed(x=x, out=out)
+    _call(load().attn_rope, device, x.data_ptr(), out.data_ptr(), code, T, H, D, stride, out_stride, pos, table, rot,
+          1 if interleaved else 0, mscale, 1 if inverse else 0)
     return out
 
 
@@ -484,49 +522,52 @@ def q8kv_append_paged(k, v, k_pages, v_pages, slots, positions=None, inv_freq=No
     """Quantise packed k, v [T, H_kv, D] (fp16, bf16 or fp32) into pages: uint8 k_pages, v_pages
     [n_pages, H_kv, page_tokens, D / 32 * 34], row t to slot slots[t] (int64: page * page_tokens + offset;
     negative: skipped).  With positions and inv_freq the keys are rotated first, as attn_rope does."""
-    _need_tensor("k", k, _DTYPES, 3, k.device)
-    _need_tensor("v", v, k.dtype, 3, k.device)
-    T, H, D = k.shape
-    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, k.device)
-    _need(v.shape == k.shape and H == kv_heads and D == head_dim, "k, v and the pages must agree in heads and head_dim")
-    _need_index("slots", slots, torch.int64, T, k.device)
-    _need((positions is None) == (inv_freq is None), "positions and inv_freq come together")
-    rot = 0
+    device = _device_of(k)
+    code, T, H, D, k_stride = _packed("k", k, device)
+    v_code, *shape, v_stride = _packed("v", v, device)
+    n_pages, kv_heads, page_tokens, head_dim, page_stride = _pool(k_pages, v_pages, device)
+    if v_code != code or shape != [T, H, D] or H != kv_heads or D != head_dim:
+        _refuse(f"k {tuple(k.shape)}, v {tuple(v.shape)} and the pages ({kv_heads} heads, head_dim {head_dim}) must agree")
+    at = _index("slots", slots, torch.int64, T, device)
+    if (positions is None) != (inv_freq is None):
+        _refuse("positions and inv_freq come together")
+    pos = table = rot = 0
     if positions is not None:
-        _need_index("positions", positions, torch.int64, T, k.device)
-        _need_tensor("inv_freq", inv_freq, torch.float64, 1, k.device)
-        _need(inv_freq.is_contiguous(), "inv_freq must be contiguous")
-        rot = 2 * inv_freq.shape[0]
-    with _on(k.device):
-        _check(load().q8kv_append_paged(_ptr(k), _ptr(v), _DTYPES[k.dtype], T, H, D, _token_stride("k", k),
-                                        _token_stride("v", v), _ptr(slots), _ptr(k_pages), _ptr(v_pages),
-                                        k_pages.shape[0], page_tokens, stride, _ptr(positions), _ptr(inv_freq), rot,
-                                        int(bool(interleaved)), mscale, _stream(k)))
+        pos = _index("positions", positions, torch.int64, T, device)
+        table, rot = _rope_table(inv_freq, device)
+    _call(load().q8kv_append_paged, device, k.data_ptr(), v.data_ptr(), code, T, H, D, k_stride, v_stride, at,
+          k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_tokens, page_stride, pos or None, table or None, rot,
+          1 if interleaved else 0, mscale)
 
 
 def q8kv_read_paged(k_pages, v_pages, slots, dtype=torch.float16, out=None):
     """The rows at `slots` (int64 [T]) dequantised: (k, v), each [T, H_kv, D] of dtype.  `out`: a pair of
     such tensors to write into; a negative slot leaves its row there as it was."""
-    _need(isinstance(slots, torch.Tensor) and slots.is_cuda, "slots must be a CUDA tensor")
-    device = slots.device
-    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, device)
-    _need(slots.dim() == 1, "slots must have one dimension")
-    T = slots.shape[0]
-    _need_index("slots", slots, torch.int64, T, device)
-    _need(dtype in _DTYPES, f"dtype {dtype} is not supported")
+    device = _device_of(slots)
+    n_pages, kv_heads, page_tokens, head_dim, page_stride = _pool(k_pages, v_pages, device)
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    at = _index("slots", slots, torch.int64, T, device)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _refuse(f"dtype {dtype} is not supported")
+    shape = (T, kv_heads, head_dim)
     if out is None:
-        out = tuple(torch.empty((T, kv_heads, head_dim), dtype=dtype, device=device) for _ in range(2))
-    for t in out:
-        _need_tensor("out", t, dtype, 3, device)
-        _need(t.shape == (T, kv_heads, head_dim) and t.is_contiguous(), "out must be contiguous [T, H_kv, D]")
-    with _on(device):
-        _check(load().q8kv_read_paged(_ptr(k_pages), _ptr(v_pages), k_pages.shape[0], page_tokens, stride,
-                                      _ptr(slots), T, kv_heads, head_dim, _ptr(out[0]), _ptr(out[1]),
-                                      _DTYPES[dtype], _stream(slots)))
+        k, v = torch.empty((2, *shape), dtype=dtype, device=slots.device).unbind(0)
+        out = (k, v)
+    else:
+        k, v = out
+        for t in (k, v):
+            if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == device and
+                    t.shape == shape and t.is_contiguous()):
+                _refuse(f"out: two contiguous tensors {shape} of {dtype} on cuda:{device} are needed")
+    _call(load().q8kv_read_paged, device, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page_tokens, page_stride, at,
+          T, kv_heads, head_dim, k.data_ptr(), v.data_ptr(), code)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim=HEAD_DIM):
+    """Floats of attn_paged's workspace for these bounds."""
     n = int(load().q8a_paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim))
     if n < 0:
         raise Q8AttnError(Q8A_ERR_INVALID_ARG, "invalid sizes for the paged workspace")
@@ -540,35 +581,32 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
     and kv_lens[b] keys (int32 [B], the new tokens' own keys last) in the pages block_table[b] (int32
     [B, width]).  max_q, max_kv: bounds of the rows and keys of a sequence.  `workspace`: fp32 CUDA tensor
     of paged_workspace_floats(...) elements (allocated here when None).  Returns [total_q, H, D]."""
-    _need_tensor("q", q, (torch.float16, torch.bfloat16), 3, q.device)
-    device = q.device
-    T, H, D = q.shape
-    kv_heads, page_tokens, head_dim, stride = _pool(k_pages, v_pages, device)
-    _need(D == head_dim, "q and the pages must have the same head_dim")
-    _need_tensor("block_table", block_table, torch.int32, 2, device)
+    device = _device_of(q)
+    code, T, H, D, stride = _packed("q", q, device)
+    n_pages, kv_heads, page_tokens, head_dim, page_stride = _pool(k_pages, v_pages, device)
+    if D != head_dim:
+        _refuse(f"q has head_dim {D}, the pages {head_dim}")
+    if not (isinstance(block_table, torch.Tensor) and block_table.dtype == torch.int32 and block_table.dim() == 2 and
+            block_table.is_contiguous() and block_table.get_device() == device):
+        _refuse(f"block_table: a contiguous int32 tensor [batch, width] on cuda:{device} is needed")
     B, width = block_table.shape
-    _need(width <= 1 or block_table.stride(1) == 1, "each row of block_table must be contiguous")
-    _need(B <= 1 or block_table.stride(0) == width, "block_table must be contiguous")
-    _need_index("kv_lens", kv_lens, torch.int32, B, device)
-    _need_index("cu_q", cu_q, torch.int32, B + 1, device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    lens = _index("kv_lens", kv_lens, torch.int32, B, device)
+    cu = _index("cu_q", cu_q, torch.int32, B + 1, device)
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=device)
-    else:
-        _need_tensor("out", out, q.dtype, 3, device)
-        _need(out.shape == q.shape and out.is_contiguous(), "out must be contiguous [total_q, H, D]")
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype == q.dtype and out.get_device() == device and
+              out.shape == q.shape and out.is_contiguous()):
+        _refuse(f"out: a contiguous tensor {(T, H, D)} of {q.dtype} on cuda:{device} is needed")
     if workspace is None:
-        workspace = torch.empty((paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D),), dtype=torch.float32,
-                                device=device)
-    else:
-        _need_tensor("workspace", workspace, torch.float32, 1, device)
-        _need(workspace.is_contiguous(), "workspace must be contiguous")
-    with _on(device):
-        _check(load().attn_paged(_ptr(q), _DTYPES[q.dtype], _token_stride("q", q), T, H, kv_heads, D, _ptr(k_pages),
-                                 _ptr(v_pages), k_pages.shape[0], page_tokens, stride, _ptr(block_table), width,
-                                 _ptr(kv_lens), _ptr(cu_q), B, max_q, max_kv, scale, int(bool(causal)), _ptr(out),
-                                 _ptr(workspace), workspace.numel(), _stream(q)))
+        workspace = torch.empty(paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D), dtype=torch.float32,
+                                device=q.device)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32 and
+              workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(f"workspace: a contiguous fp32 tensor on cuda:{device} is needed")
+    _call(load().attn_paged, device, q.data_ptr(), code, stride, T, H, kv_heads, D, k_pages.data_ptr(),
+          v_pages.data_ptr(), n_pages, page_tokens, page_stride, block_table.data_ptr(), width, lens, cu, B, max_q,
+          max_kv, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return out
 
 
