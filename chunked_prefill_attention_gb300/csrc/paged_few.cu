@@ -35,13 +35,15 @@
 // transposition in registers (movmatrix).
 //
 // Work.  All key tiles of all (sequence, K/V head, row tile) units are laid end
-// to end and cut into equal shares, one per CTA (two CTAs per SM), so ragged
-// batches and single long sequences both fill the machine.  The warps of a CTA
-// take its tiles in turn, each with its own ring of asynchronous copies (page
-// rows are contiguous: one copy per page and tensor) and its own running
-// softmax; they are joined in a fixed order at the end of a unit's tiles.  A
-// unit cut between CTAs leaves partial states, which a second kernel joins in
-// order: no atomics, the same result every time.
+// to end and cut into equal shares, one per warp (16 warps per SM), so ragged
+// batches and single long sequences both fill the machine.  A warp works alone:
+// its own ring of asynchronous copies (page rows are contiguous: one copy per page
+// and tensor), its own running softmax, no barrier with other warps, so the start
+// and end of a unit in one warp hide behind the others' tiles (64 sequences of 256
+// to 16,384 keys, 8 heads x 64: 157 us with shares and barriers of whole CTAs, 127 us
+// so).  A unit cut between warps leaves partial states, which a second kernel joins
+// in order: no atomics, the same result every time.  Where a CTA's eight shares all
+// lie in one unit, the CTA joins them first, which leaves an eighth of the parts.
 
 #include <type_traits>
 
@@ -60,9 +62,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 320;      // two per SM of 160 SMs
-constexpr int kDescInts = 8;       // join record of a CTA boundary
+constexpr int kMaxWarps = kMaxCtas * kWarps;
+constexpr int kMinShare = 2;       // tiles of a warp's share
+constexpr int kDescInts = 8;       // join record of a share boundary
 constexpr float kLazy = 8.0f;      // the reference moves when exceeded by more than 2^8
-constexpr int kMergeY = 8;         // blocks that join one unit
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 template <int D>
@@ -170,16 +173,33 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane) {
   return v;
 }
 
+// Two channels of a row of out: those of m-tile i of O^T, which lane group g holds (codes
+// 2 (i & 1) .. of its word of the block).
+template <typename QT, int D>
+__device__ __forceinline__ void store_pair(const PagedArgs& a, const Seq& sq, int kvh, int row, int i, int g, float y0,
+                                           float y1) {
+  const bool odd = i & 2;
+  int c = 64 * (i / 4) + (odd ? 32 : 2) + 4 * g + 2 * (i & 1);
+  if (!odd && g == 7 && (i & 1)) c -= 32;   // the word made of a row's first and ninth words
+  const int tok = row / a.group;
+  QT* op = static_cast<QT*>(a.out) + ((sq.q0 + tok) * a.heads + kvh * a.group + row - tok * a.group) * D + c;
+  if (std::is_same<QT, __half>::value) {
+    *reinterpret_cast<uint32_t*>(op) = pack_half2(y0, y1);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(y0, y1);
+    *reinterpret_cast<uint32_t*>(op) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
 template <typename QT, int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT * D <= 256 ? 2 : 1)
 paged_few_kernel(const PagedArgs a) {
   using Sh = Shape<D>;
   using Pt = Part<D, NT>;
   constexpr int S = Sh::S, KT = Sh::KT, RW = Sh::RW, P = Sh::P, R = Pt::R, NREG = Pt::NREG;
-  static_assert(kWarps / 2 * (NREG + 4 * NT) * 128 <= Sh::RING, "the join of a CTA's warps reuses the ring");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps * kStages];
-  __shared__ int64_t sums[kWarps], found[2];
+  __shared__ int64_t sums[kWarps], found[kWarps][2];
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0)
@@ -187,23 +207,24 @@ paged_few_kernel(const PagedArgs a) {
   fence_mbar_init();
   pdl_wait();
 
-  // ---- this CTA's share of all key tiles
+  // ---- this warp's share of all key tiles
   int64_t mine = 0;
   for (int b = tid; b < a.batch; b += kThreads) mine += units_of<D, NT>(a, read_seq(a, b)).all;
   const int64_t inc = warp_inclusive(mine, lane);
   if (lane == 31) sums[warp] = inc;
-  if (tid == 0) found[0] = -1;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += sums[w];
-  const int64_t share = i64max(kWarps, (total + gridDim.x - 1) / gridDim.x);
-  int32_t* desc = reinterpret_cast<int32_t*>(a.part) + static_cast<int64_t>(blockIdx.x) * kDescInts;
-  float* parts = a.part + kMaxCtas * kDescInts;
-  if (tid == 0) desc[0] = -1;   // nothing to join at this boundary, until found otherwise
-  int64_t pos = blockIdx.x * share;
-  const int64_t end = i64min(total, pos + share);
-  if (pos >= end) return;
+  const int64_t shares = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t share = i64max(kMinShare, (total + shares - 1) / shares);
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  int32_t* desc = reinterpret_cast<int32_t*>(a.part) + gw * kDescInts;
+  float* parts = a.part + kMaxWarps * kDescInts;
+  if (lane == 0) desc[0] = -1;   // nothing to join at this boundary, until found otherwise
+  const int64_t pos0 = blockIdx.x * (kWarps * share);
+  if (pos0 >= total) return;     // uniform over the CTA
+  // the sequence that holds each warp's first tile
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     __syncthreads();
@@ -212,18 +233,33 @@ paged_few_kernel(const PagedArgs a) {
     const int64_t i = warp_inclusive(v, lane);
     if (lane == 31) sums[warp] = i;
     __syncthreads();
-    int64_t before = base;
+    int64_t before = base + i - v;
     for (int w = 0; w < warp; ++w) before += sums[w];
-    if (pos >= before + i - v && pos < before + i) {
-      found[0] = b;
-      found[1] = before + i - v;
+    for (int w = 0; w < kWarps; ++w) {
+      const int64_t p = pos0 + w * share;
+      if (p >= before && p < before + v) {
+        found[w][0] = b;
+        found[w][1] = before;
+      }
     }
     for (int w = 0; w < kWarps; ++w) base += sums[w];
-    __syncthreads();
-    if (found[0] >= 0) break;
+    if (base > pos0 + (kWarps - 1) * share) break;   // uniform: every warp's tile is found
   }
-  int b = static_cast<int>(found[0]);
-  base = found[1];
+  __syncthreads();
+  int64_t pos = pos0 + warp * share;
+  const int64_t end = i64min(total, pos + share);
+  const int64_t cta_end = i64min(total, pos0 + kWarps * share);
+  // one unit holds all of the CTA's tiles?
+  bool inner;
+  {
+    const int b0 = static_cast<int>(found[0][0]);
+    const int64_t tiles = units_of<D, NT>(a, read_seq(a, b0)).tiles;
+    const int64_t last = (cta_end - 1 - pos0) / share;
+    inner = found[last][0] == b0 && (pos0 - found[0][1]) / tiles == (cta_end - 1 - found[0][1]) / tiles;
+  }
+  if (!inner && pos >= end) return;   // no barrier from here on, unless inner
+  int b = static_cast<int>(found[inner ? 0 : warp][0]);
+  base = found[inner ? 0 : warp][1];
 
   uint8_t* ring = smem + warp * (kStages * Sh::STAGE);
   const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp * kStages]);
@@ -236,36 +272,34 @@ paged_few_kernel(const PagedArgs a) {
   const uint32_t piece_bytes = static_cast<uint32_t>(RW * 4) << piece_shift;
   const int64_t start = pos;
 
-  while (pos < end) {
+  while (inner || pos < end) {
     const Seq sq = read_seq(a, b);
     const auto un = units_of<D, NT>(a, sq);
-    if (pos >= base + un.all) {
+    if (!inner && pos >= base + un.all) {
       base += un.all;
       ++b;
       continue;
     }
-    const int64_t local = pos - base;
-    const int64_t unit = local / un.tiles;
-    const int tile0 = static_cast<int>(local - unit * un.tiles);
+    const int64_t unit = ((inner ? pos0 : pos) - base) / un.tiles;
+    const int tile0 = static_cast<int>(pos - base - unit * un.tiles);
     const int kvh = static_cast<int>(unit / un.row_tiles);
     const int rt = static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
-    const int n = static_cast<int>(i64min(un.tiles - tile0, end - pos));
+    const int n = static_cast<int>(inner ? i64max(0, end - pos) : i64min(un.tiles - tile0, end - pos));
     const int n_rows = sq.n_q * a.group;
-    const int nw = (n - warp + kWarps - 1) / kWarps;   // this warp's tiles
 
     // ---- copies of this warp's tiles
     const int32_t* table = a.table + b * a.table_stride;
     const int64_t head_off = (static_cast<int64_t>(kvh) << a.page_shift) * (RW * 4);
     auto fetch = [&](int j) -> int {   // page of this lane's piece of tile j
-      const int key = (tile0 + warp + kWarps * j) * KT + (lane << piece_shift);
-      return (lane < pieces && j < nw && key < sq.kv) ? table[key >> a.page_shift] : 0;
+      const int key = (tile0 + j) * KT + (lane << piece_shift);
+      return (lane < pieces && j < n && key < sq.kv) ? table[key >> a.page_shift] : 0;
     };
     int issued = 0;
     auto issue = [&](int j, int page) {
-      if (j >= nw || waiter.bad) return;
+      if (j >= n || waiter.bad) return;
       issued = j + 1;
       const uint32_t c = it + j, s = c % kStages;
-      const int key0 = (tile0 + warp + kWarps * j) * KT;
+      const int key0 = (tile0 + j) * KT;
       const int have = max(0, min(pieces, (sq.kv - key0 + (1 << piece_shift) - 1) >> piece_shift));
       if (lane == 0) mbar_arrive_expect_tx(bar_u + 8 * s, 2 * have * piece_bytes);
       __syncwarp();
@@ -370,13 +404,13 @@ paged_few_kernel(const PagedArgs a) {
     int v_exp = 0;   // largest exponent (fp16, biased) of V's scales so far; weights carry 2^(21 - v_exp)
 
 #pragma unroll 1
-    for (int j = 0; j < nw; ++j) {
+    for (int j = 0; j < n; ++j) {
       const uint32_t c = it + j, st = c % kStages;
       if (j >= issued) break;   // an earlier wait ran out
       waiter.wait(bar_u + 8 * st, (c / kStages) & 1);
       const uint32_t* kw = reinterpret_cast<const uint32_t*>(ring + st * Sh::STAGE);
       const uint32_t* vw = kw + Sh::TILE / 4;
-      const int key0 = (tile0 + warp + kWarps * j) * KT;
+      const int key0 = (tile0 + j) * KT;
 
       // ---- scores: s[mt][nt][e], key S g + 2 mt (e < 2) or the next, column 2 t + (e & 1)
       float s[S / 2][NT][4];
@@ -546,9 +580,9 @@ paged_few_kernel(const PagedArgs a) {
       issue(j + kStages, next_page);
       next_page = fetch(j + kStages + 1);
     }
-    it += nw;
+    it += n;
 
-    // ---- join the warps, in a fixed order
+    // ---- the unit's rows, or this share's part of them
     const float v_down = __int_as_float((127 - 21 + v_exp) << 23);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -562,83 +596,66 @@ paged_few_kernel(const PagedArgs a) {
       for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[nt][cc] += __shfl_xor_sync(kFull, l[nt][cc], x);
-    float* xch = reinterpret_cast<float*>(smem);
-    constexpr int kXch = (NREG + 4 * NT) * 32;
-    __syncthreads();   // every warp's tiles are consumed: the ring is free
+    if (inner) {   // join the warps, in a fixed order
+      constexpr int kXch = (NREG + 4 * NT) * 32;
+      static_assert(kWarps / 2 * kXch * 4 <= Sh::RING, "the exchange reuses the ring");
+      float* xch = reinterpret_cast<float*>(smem);
+      __syncthreads();   // every warp's tiles are consumed: the ring is free
 #pragma unroll 1
-    for (int half = kWarps / 2; half > 0; half /= 2) {
-      if (warp >= half && warp < 2 * half) {
-        float* dst = xch + (warp - half) * kXch + lane;
+      for (int half = kWarps / 2; half > 0; half /= 2) {
+        if (warp >= half && warp < 2 * half) {
+          float* dst = xch + (warp - half) * kXch + lane;
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) dst[32 * i] = o[i / (4 * NT)][i / 4 % NT][i & 3];
+          for (int i = 0; i < NREG; ++i) dst[32 * i] = o[i / (4 * NT)][i / 4 % NT][i & 3];
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-          dst[32 * (NREG + i)] = m[i / 2][i & 1];
-          dst[32 * (NREG + 2 * NT + i)] = l[i / 2][i & 1];
-        }
-        fence_proxy_async_smem();   // these writes come before the next unit's copies
-      }
-      __syncthreads();
-      if (warp < half) {
-        const float* src = xch + warp * kXch + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float wa[2], wb[2];
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const float mb = src[32 * (NREG + 2 * nt + cc)], lb = src[32 * (NREG + 2 * NT + 2 * nt + cc)];
-            const float top = fmaxf(m[nt][cc], mb);
-            wa[cc] = join_weight(m[nt][cc], top);
-            wb[cc] = join_weight(mb, top);
-            m[nt][cc] = top;
-            l[nt][cc] = fmaf(wa[cc], l[nt][cc], wb[cc] * lb);
+          for (int i = 0; i < 2 * NT; ++i) {
+            dst[32 * (NREG + i)] = m[i / 2][i & 1];
+            dst[32 * (NREG + 2 * NT + i)] = l[i / 2][i & 1];
           }
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[i][nt][e] = fmaf(wa[e & 1], o[i][nt][e], wb[e & 1] * src[32 * ((i * NT + nt) * 4 + e)]);
         }
+        __syncthreads();
+        if (warp < half) {
+          const float* src = xch + warp * kXch + lane;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float wa[2], wb[2];
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const float mb = src[32 * (NREG + 2 * nt + cc)], lb = src[32 * (NREG + 2 * NT + 2 * nt + cc)];
+              const float top = fmaxf(m[nt][cc], mb);
+              wa[cc] = join_weight(m[nt][cc], top);
+              wb[cc] = join_weight(mb, top);
+              m[nt][cc] = top;
+              l[nt][cc] = fmaf(wa[cc], l[nt][cc], wb[cc] * lb);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[i][nt][e] = fmaf(wa[e & 1], o[i][nt][e], wb[e & 1] * src[32 * ((i * NT + nt) * 4 + e)]);
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
+      if (warp > 0) return;
     }
-    if (warp == 0) {
-      if (n == un.tiles) {   // the whole unit: the rows of out
+    {
+      const bool whole = inner ? tile0 == 0 && cta_end - pos0 == un.tiles : n == un.tiles;
+      if (whole) {   // the whole unit: the rows of out
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int row = rt * R + 8 * nt + 2 * t + cc;
             if (row >= n_rows) continue;
-            const int tok = row / a.group;
-            QT* op = static_cast<QT*>(a.out) +
-                     ((sq.q0 + tok) * a.heads + kvh * a.group + row - tok * a.group) * D;
             const float inv = l[nt][cc] == 0.0f ? 0.0f : 1.0f / l[nt][cc];
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-              for (int odd = 0; odd < 2; ++odd) {
-                const int i = 4 * p + 2 * odd;
-                const float y0 = o[i][nt][cc] * inv, y1 = o[i][nt][2 + cc] * inv;
-                const float y2 = o[i + 1][nt][cc] * inv, y3 = o[i + 1][nt][2 + cc] * inv;
-                const int c = 64 * p + (odd ? 32 : 2) + 4 * g;
-                const int c2 = !odd && g == 7 ? 64 * p : c + 2;
-                uint32_t lo, hi;
-                if (std::is_same<QT, __half>::value) {
-                  lo = pack_half2(y0, y1);
-                  hi = pack_half2(y2, y3);
-                } else {
-                  const __nv_bfloat162 x0 = __floats2bfloat162_rn(y0, y1), x1 = __floats2bfloat162_rn(y2, y3);
-                  lo = *reinterpret_cast<const uint32_t*>(&x0);
-                  hi = *reinterpret_cast<const uint32_t*>(&x1);
-                }
-                *reinterpret_cast<uint32_t*>(op + c) = lo;
-                *reinterpret_cast<uint32_t*>(op + c2) = hi;
-              }
+            for (int i = 0; i < D / 16; ++i)
+              store_pair<QT, D>(a, sq, kvh, row, i, g, o[i][nt][cc] * inv, o[i][nt][2 + cc] * inv);
           }
       } else {
         const bool first = pos == start;
-        float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1)) * Pt::FLOATS;
+        float* part = parts + (2 * gw + (first ? 0 : 1)) * Pt::FLOATS;
 #pragma unroll
         for (int i = 0; i < NREG; ++i) part[32 * i + lane] = o[i / (4 * NT)][i / 4 % NT][i & 3];
         if (g == 0) {
@@ -650,89 +667,182 @@ paged_few_kernel(const PagedArgs a) {
               part[32 * NREG + R + 8 * nt + 2 * t + cc] = l[nt][cc];
             }
         }
-        // the first boundary inside a unit names the unit's partial states:
-        // CTA c - 1 (its last) and the first of c, c + 1, ...
+        // The first boundary inside a unit names the unit's parts, from share c - 1 on
+        // (its first part where the unit starts the share, else its second) to the
+        // unit's last share.  An inner CTA is one part, of its first share; the
+        // unit's first boundary is its own second share's when the unit starts it.
         const int64_t u0 = pos - tile0;
-        if (first && tile0 > 0 && u0 >= start - share && lane == 0) {
-          desc[1] = kvh;
-          desc[2] = rt;
-          desc[3] = u0 == start - share ? 0 : 1;
-          desc[4] = static_cast<int32_t>((u0 + un.tiles - 1) / share) - static_cast<int32_t>(blockIdx.x) + 2;
-          desc[0] = b;
+        const bool starts = inner && tile0 == 0;
+        if (lane == 0 && (starts || (first && tile0 > 0 && u0 >= start - share))) {
+          int32_t* at = desc + (starts ? kDescInts : 0);
+          const int64_t c = gw + (starts ? 1 : 0), u1 = u0 + un.tiles, wide = kWarps * share;
+          const int64_t k0 = (u0 + wide - 1) / wide;                                // inner CTAs k0 ..
+          const int64_t k1 = u1 == total ? (u1 + wide - 1) / wide : u1 / wide;      // .. k1 - 1
+          const int64_t last = (u1 - 1) / share;
+          at[1] = kvh;
+          at[2] = rt;
+          at[3] = u0 == (c - 1) * share ? 0 : 1;
+          const int64_t n_a = k0 < k1 ? k0 * kWarps - (c - 1) : last - (c - 1) + 1;  // parts before them
+          const int64_t n_b = i64max(0, k1 - k0);
+          at[4] = static_cast<int32_t>(n_a + n_b + (n_b ? i64max(0, last - k1 * kWarps + 1) : 0));
+          at[5] = static_cast<int32_t>(n_a);
+          at[6] = static_cast<int32_t>(n_b);
+          at[0] = b;
         }
       }
     }
+    if (inner) return;
     pos += n;
   }
 }
 
-// Joins the partial states of a unit that several CTAs hold parts of: block
-// (c, y) a slice of the unit first cut at the start of CTA c + 1.
+// Joins the partial states of the units that several shares hold parts of.  Warp w of
+// block (x, y) looks at boundary 8 x + w and takes quarter y of its unit's channels: alone
+// where the unit has few parts; the parts of one with more are dealt to the block's warps.
+constexpr int kJoinY = 4;
+constexpr int kAlone = 8;   // parts that one warp joins alone
+
 template <typename QT, int D, int NT>
-__global__ void __launch_bounds__(256) paged_few_join_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads) paged_few_join_kernel(const PagedArgs a) {
   using Pt = Part<D, NT>;
-  constexpr int R = Pt::R, NREG = Pt::NREG, E = NREG * 32 / kMergeY;   // elements of this block
-  static_assert(E % 64 == 0, "slices of 64 elements");
-  __shared__ float w[kMaxCtas + 1][R];
-  __shared__ float inv[R];
-  __shared__ float sum[4][64];
+  constexpr int R = Pt::R, NREG = Pt::NREG, MT = D / 16 / kJoinY;   // m-tiles of a quarter
+  __shared__ int32_t big[kWarps][8];
+  __shared__ float red[kWarps][4 * MT + 2][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int32_t* desc = reinterpret_cast<const int32_t*>(a.part) + (static_cast<int64_t>(blockIdx.x) + 1) * kDescInts;
-  const int b = desc[0];
-  if (b < 0) return;
-  const int kvh = desc[1], rt = desc[2], n = min(desc[4], kMaxCtas + 1);
-  const float* parts = a.part + kMaxCtas * kDescInts;
-  const int64_t c = blockIdx.x;
-  // partial p of the unit: slot desc[3] of CTA c, then slot 0 of the CTAs after it
-  auto part = [&](int p) { return parts + (p == 0 ? 2 * c + desc[3] : 2 * (c + p)) * Pt::FLOATS; };
-  const Seq sq = read_seq(a, b);
-  for (int i = threadIdx.x; i < n * R; i += 256) w[i / R][i % R] = part(i / R)[32 * NREG + i % R];
-  __syncthreads();
-  {
-    constexpr int kPer = 256 / R;   // threads of a row (neighbours)
-    const int row = threadIdx.x / kPer, k = threadIdx.x % kPer;
-    float top = -INFINITY;
-    for (int p = k; p < n; p += kPer) top = fmaxf(top, w[p][row]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const float* parts = a.part + kMaxWarps * kDescInts;
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int32_t field = lane < 8 ? reinterpret_cast<const int32_t*>(a.part)[mine * kDescInts + lane] : 0;
+  const int b0 = __shfl_sync(kFull, field, 0), n0 = __shfl_sync(kFull, field, 4);
+  if (lane < 8) big[warp][lane] = lane == 0 && n0 <= kAlone ? -1 : field;
+  if (b0 >= 0 && n0 <= kAlone) {
+    const int kvh = __shfl_sync(kFull, field, 1), rt = __shfl_sync(kFull, field, 2);
+    const int slot = __shfl_sync(kFull, field, 3), n_a = __shfl_sync(kFull, field, 5), n_b = __shfl_sync(kFull, field, 6);
+    const Seq sq = read_seq(a, b0);
+    const float* part[kAlone];
 #pragma unroll
-    for (int x = 1; x < kPer; x *= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-    float l = 0.0f;
-    for (int p = k; p < n; p += kPer) {
-      const float f = join_weight(w[p][row], top);
-      w[p][row] = f;
-      l = fmaf(f, part(p)[32 * NREG + R + row], l);
+    for (int p = 0; p < kAlone; ++p) {
+      // beyond the last, the first again with weight 0, so that the loads need no branch
+      const int q = p < n0 ? p : 0;
+      const int s = q < n_a ? q : (q < n_a + n_b ? n_a + kWarps * (q - n_a) : q + (kWarps - 1) * n_b);
+      part[p] = parts + (2 * (mine - 1 + s) + (s == 0 ? slot : 0)) * Pt::FLOATS;
     }
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[kAlone][2], inv[2];
 #pragma unroll
-    for (int x = 1; x < kPer; x *= 2) l += __shfl_xor_sync(kFull, l, x);
-    if (k == 0) inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
+      for (int cc = 0; cc < 2; ++cc) {
+        const int at = 32 * NREG + 8 * nt + 2 * t + cc;
+        float top = -INFINITY, l = 0.0f, lp[kAlone];
+#pragma unroll
+        for (int p = 0; p < kAlone; ++p) {
+          w[p][cc] = part[p][at];
+          lp[p] = part[p][at + R];
+        }
+#pragma unroll
+        for (int p = 0; p < kAlone; ++p) {
+          if (p >= n0) w[p][cc] = -INFINITY;
+          top = fmaxf(top, w[p][cc]);
+        }
+#pragma unroll
+        for (int p = 0; p < kAlone; ++p) {
+          w[p][cc] = join_weight(w[p][cc], top);
+          l = p < n0 ? fmaf(w[p][cc], lp[p], l) : l;
+        }
+        inv[cc] = l == 0.0f ? 0.0f : 1.0f / l;
+      }
+      const int row = rt * R + 8 * nt + 2 * t;
+      const bool have0 = row < sq.n_q * a.group, have1 = row + 1 < sq.n_q * a.group;
+#pragma unroll
+      for (int q = 0; q < MT; ++q) {
+        const int i = blockIdx.y * MT + q;
+        float v[kAlone][4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int p = 0; p < kAlone; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[p][e] = part[p][32 * ((i * NT + nt) * 4 + e) + lane];
+#pragma unroll
+        for (int p = 0; p < kAlone; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = p < n0 ? fmaf(w[p][e & 1], v[p][e], y[e]) : y[e];
+        if (have0) store_pair<QT, D>(a, sq, kvh, row, i, g, y[0] * inv[0], y[2] * inv[0]);
+        if (have1) store_pair<QT, D>(a, sq, kvh, row + 1, i, g, y[1] * inv[1], y[3] * inv[1]);
+      }
+    }
   }
   __syncthreads();
-  const int e64 = threadIdx.x & 63, pg = threadIdx.x >> 6;
-  const int n_rows = sq.n_q * a.group;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = blockIdx.y * E + e0 + e64;
-    const int reg = e / 32, lane = e % 32, g = lane >> 2, t = lane & 3;
-    const int i = reg / (4 * NT), nt = reg / 4 % NT, k = reg & 3;
-    const int row = 8 * nt + 2 * t + (k & 1);
-    float y = 0.0f;
-#pragma unroll 8
-    for (int p = pg; p < n; p += 4) y = fmaf(w[p][row], part(p)[e], y);
-    sum[pg][e64] = y;
-    __syncthreads();
-    const int r = rt * R + row;
-    if (pg == 0 && r < n_rows) {
-      y = ((sum[0][e64] + sum[1][e64]) + (sum[2][e64] + sum[3][e64])) * inv[row];
-      const int word = i & 1, odd = (i >> 1) & 1, ch = 2 * word + (k >> 1);   // code of the lane's word
-      int chan = 64 * (i / 4) + (odd ? 32 : 2) + 4 * g + ch;
-      if (!odd && g == 7 && ch >= 2) chan -= 32;   // the word of a row's first and ninth words
-      const int tok = r / a.group;
-      QT* op = static_cast<QT*>(a.out) + ((sq.q0 + tok) * a.heads + kvh * a.group + r - tok * a.group) * D + chan;
-      if (std::is_same<QT, __half>::value)
-        *reinterpret_cast<__half*>(op) = __float2half_rn(y);
-      else
-        *reinterpret_cast<__nv_bfloat16*>(op) = __float2bfloat16_rn(y);
+  for (int j = 0; j < kWarps; ++j) {
+    const int b = big[j][0];
+    if (b < 0) continue;   // uniform over the block
+    const int kvh = big[j][1], rt = big[j][2], slot = big[j][3], n = big[j][4], n_a = big[j][5], n_b = big[j][6];
+    const int64_t c1 = static_cast<int64_t>(blockIdx.x) * kWarps + j - 1;
+    // part p: share c - 1's, then the first slot of the shares after it, of the
+    // inner CTAs' eight shares only the first
+    auto part = [&](int p) {
+      const int s = p < n_a ? p : (p < n_a + n_b ? n_a + kWarps * (p - n_a) : p + (kWarps - 1) * n_b);
+      return parts + (2 * (c1 + s) + (s == 0 ? slot : 0)) * Pt::FLOATS;
+    };
+    const Seq sq = read_seq(a, b);
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      const int at = 32 * NREG + 8 * nt + 2 * t;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 4
+      for (int p = warp; p < n; p += kWarps) {
+        top[0] = fmaxf(top[0], part(p)[at]);
+        top[1] = fmaxf(top[1], part(p)[at + 1]);
+      }
+      red[warp][0][lane] = top[0];
+      red[warp][1][lane] = top[1];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        top[0] = fmaxf(top[0], red[k][0][lane]);
+        top[1] = fmaxf(top[1], red[k][1][lane]);
+      }
+      __syncthreads();
+      float l[2] = {0.0f, 0.0f}, y[MT][4] = {};
+#pragma unroll 4
+      for (int p = warp; p < n; p += kWarps) {
+        const float* s = part(p);
+        const float w[2] = {join_weight(s[at], top[0]), join_weight(s[at + 1], top[1])};
+        l[0] = fmaf(w[0], s[at + R], l[0]);
+        l[1] = fmaf(w[1], s[at + R + 1], l[1]);
+#pragma unroll
+        for (int q = 0; q < MT; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[q][e] = fmaf(w[e & 1], s[32 * (((blockIdx.y * MT + q) * NT + nt) * 4 + e) + lane], y[q][e]);
+      }
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[warp][4 * q + e][lane] = y[q][e];
+      red[warp][4 * MT][lane] = l[0];
+      red[warp][4 * MT + 1][lane] = l[1];
+      __syncthreads();
+      if (warp == 0) {
+        float sum[4 * MT + 2];
+#pragma unroll
+        for (int q = 0; q < 4 * MT + 2; ++q) {
+          sum[q] = red[0][q][lane];
+#pragma unroll
+          for (int k = 1; k < kWarps; ++k) sum[q] += red[k][q][lane];
+        }
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int row = rt * R + 8 * nt + 2 * t + cc;
+          const float inv = sum[4 * MT + cc] == 0.0f ? 0.0f : 1.0f / sum[4 * MT + cc];
+          if (row < sq.n_q * a.group)
+#pragma unroll
+            for (int q = 0; q < MT; ++q)
+              store_pair<QT, D>(a, sq, kvh, row, blockIdx.y * MT + q, g, sum[4 * q + cc] * inv,
+                                sum[4 * q + 2 + cc] * inv);
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -750,8 +860,9 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
     configured_device = dev;
   }
   e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
-  if (e != cudaSuccess || ctas < 2) return e;
-  return launch_kernel(paged_few_join_kernel<QT, D, NT>, dim3(ctas - 1, kMergeY), dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  PdlScope early;   // the join is scheduled while the last warps run, and waits for them
+  return launch_kernel(paged_few_join_kernel<QT, D, NT>, dim3(ctas, kJoinY), dim3(kThreads), 0, stream, a);
 }
 
 template <typename QT, int D>
@@ -772,7 +883,7 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, cudaStream_t stream) 
 
 int64_t paged_few_floats(int32_t head_dim, int64_t rows) {
   const int64_t r = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-  return kMaxCtas * (kDescInts + 2 * (r * head_dim + 2 * r));
+  return kMaxWarps * (kDescInts + 2 * (r * head_dim + 2 * r));
 }
 
 cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows, cudaStream_t stream) {
