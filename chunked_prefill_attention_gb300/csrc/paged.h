@@ -89,6 +89,7 @@ int64_t paged_few_floats(int32_t head_dim, int64_t rows);
 // Many query rows per K/V head.  The plan of a call from its bounds: blocks
 // (row units of 256 rows times K/V heads), shares of the key tiles, workspace.
 struct TilesPlan {
+  bool pair;        // no sequence of more than 128 rows
   int64_t slots;
   int32_t splits;
   int64_t part_ml;
@@ -96,7 +97,7 @@ struct TilesPlan {
 };
 TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_kv,
                            int32_t head_dim);
-cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t slots,
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, bool pair, int64_t slots,
                                cudaStream_t stream);
 
 }  // namespace q8a

@@ -177,9 +177,12 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
 
 namespace {
 
-// Sequences of at most so many rows (tokens * group) go to the few-row kernel:
-// TUNE
-constexpr int64_t kFewRows = 64;
+// Sequences of at most so many rows (tokens * group) go to the few-row kernel.  Both
+// kernels at 16 rows, 16 sequences of 32,768 keys, 8 K/V heads: 142 us against 328 (64
+// channels), 334 against 552 (128); a few-row kernel made for 32 rows took 310 and 430
+// there, but 50 and 61 against 36 and 50 for 2,048 keys and 587 and 820 against 329 and
+// 554 at 64 rows (in two passes), so from 17 rows on the tile kernel takes them.
+constexpr int64_t kFewRows = 16;
 
 // The launches of a call, from its bounds alone.
 struct Plan {
@@ -284,7 +287,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
     b.splits = plan.t.splits;
     b.part = workspace + plan.few_floats;
     b.part_ml = plan.t.part_ml;
-    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t.slots, st);
+    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t.pair, plan.t.slots, st);
   }
   if (plan.few && e == cudaSuccess) {
     a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;

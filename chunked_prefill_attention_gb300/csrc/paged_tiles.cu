@@ -52,12 +52,11 @@ namespace {
 
 constexpr int BM = 128;
 constexpr int ND = 2;            // dequantised K and V rings
-constexpr int kRows = 2 * BM;    // rows of a CTA
 constexpr float kLazy = 8.0f;    // the reference moves when exceeded by more than 2^8
 constexpr float kLift = 7.0f;    // weights carry 2^7, so they reach 2^15 and keep fp16's 11 bits down to 2^-21
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-template <int D>
+template <int D, bool kPair>
 struct Geo {
   static constexpr int BN = D == 64 ? 96 : 64;          // keys of a tile
   static constexpr int RB = D / 32 * 34;                // bytes of a row
@@ -67,14 +66,13 @@ struct Geo {
   static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
   static constexpr int NR = D == 64 ? 4 : 3;            // raw ring
   static constexpr int NS = D == 64 ? 3 : 2;            // score buffers
-  static constexpr int kThreads = D == 64 ? 640 : 512;
+  static constexpr int kThreads = D == 64 || kPair ? 640 : 512;
   static constexpr int kDq = kThreads / 32 - 11;        // dequantising warps
-  static constexpr bool QB_SMEM = false;             // tile B's Q in shared memory
+  static constexpr int ROWS = kPair ? BM : 2 * BM;      // query rows of a CTA
   // shared memory
   static constexpr int OFF_K = 0;                       // [ND][hi | lo]
   static constexpr int OFF_V = OFF_K + ND * 2 * TILE;   // [ND][hi | lo]
-  static constexpr int OFF_QB = OFF_V + ND * 2 * TILE;
-  static constexpr int OFF_RAW = OFF_QB + (QB_SMEM ? BM * D * 2 : 0);
+  static constexpr int OFF_RAW = OFF_V + ND * 2 * TILE;
   static constexpr int OFF_BAR = OFF_RAW + NR * 2 * RAWB;
   static constexpr int B_Q = 0, B_RAWFULL = 1, B_RAWEMPTY = B_RAWFULL + NR, B_KFULL = B_RAWEMPTY + NR,
                        B_KEMPTY = B_KFULL + ND, B_VFULL = B_KEMPTY + ND, B_VEMPTY = B_VFULL + ND,
@@ -84,10 +82,10 @@ struct Geo {
   static constexpr int SMEM = OFF_CTL + 32 + 1024;      // + alignment slack
   static_assert(SMEM <= 227 * 1024 && TILE % 1024 == 0 && OFF_RAW % 16 == 0 && RAWB % 16 == 0, "shared memory");
   // TMEM columns
-  static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + (QB_SMEM ? 1 : 2) * (D / 2);
+  static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + D;
   static_assert(T_END <= 512, "TMEM");
   // registers of the softmax warpgroups and of the others, out of the launch's REG_L a thread
-  static constexpr int REG_S = D == 64 ? 144 : 136, REG_O = D == 64 ? 64 : 120, REG_L = D == 64 ? 96 : 128;
+  static constexpr int REG_S = kThreads == 640 ? 144 : 136, REG_O = kThreads == 640 ? 64 : 120, REG_L = kThreads == 640 ? 96 : 128;
   static_assert(2 * 128 * REG_S + (kThreads - 256) * REG_O <= kThreads * REG_L, "register split");
 };
 
@@ -167,32 +165,38 @@ struct Unit {
 };
 
 // Key tiles that rows r .. r + 127 of a sequence see.
-template <int D>
+template <int D, bool kPair>
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, const Seq& sq, int r, int n_rows) {
   if (r >= n_rows) return 0;
   const int last = min(r + BM - 1, n_rows - 1) / a.group;   // token of the last row
   const int vis = a.causal ? min(sq.kv, sq.kv - sq.n_q + last + 1) : sq.kv;
-  return vis > 0 ? (vis + Geo<D>::BN - 1) / Geo<D>::BN : 0;
+  return vis > 0 ? (vis + Geo<D, kPair>::BN - 1) / Geo<D, kPair>::BN : 0;
 }
 
-template <int D>
+template <int D, bool kPair>
 __device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, int kvh, int split) {
   Unit u;
   u.sq = read_seq(a, ctl->b);
   u.kvh = kvh;
   u.n_rows = u.sq.n_q * a.group;
   // the unit with the most visible keys first
-  u.r0 = ((u.n_rows + kRows - 1) / kRows - 1 - ctl->unit) * kRows;
-  const int ta = tiles_of<D>(a, u.sq, u.r0, u.n_rows), tb = tiles_of<D>(a, u.sq, u.r0 + BM, u.n_rows);
+  u.r0 = ((u.n_rows + Geo<D, kPair>::ROWS - 1) / Geo<D, kPair>::ROWS - 1 - ctl->unit) * Geo<D, kPair>::ROWS;
+  const int ta = tiles_of<D, kPair>(a, u.sq, u.r0, u.n_rows);
+  const int tb = kPair ? 0 : tiles_of<D, kPair>(a, u.sq, u.r0 + BM, u.n_rows);
   u.per = max(1, (max(ta, tb) + a.splits - 1) / a.splits);
   u.t0 = split * u.per;
   u.T[0] = max(0, min(u.per, ta - u.t0));
   u.T[1] = max(0, min(u.per, tb - u.t0));
+  if (kPair) {   // the key tiles in turn
+    u.T[1] = u.T[0] / 2;
+    u.T[0] -= u.T[1];
+  }
   return u;
 }
 
 // Block x of the grid -> (sequence, row unit), by warp 0: the sequences' units
 // laid end to end, those of the few-row kernel left out.
+template <int kRows>
 __device__ __forceinline__ void locate(const PagedArgs& a, int64_t slot, Ctl* ctl, int lane) {
   int64_t base = 0;
   int found = -1, unit = 0;
@@ -224,21 +228,42 @@ __device__ __forceinline__ void locate(const PagedArgs& a, int64_t slot, Ctl* ct
   }
 }
 
-// Step n <-> (key tile t, tile x): A and B in turn, then the longer one alone.
-__device__ __forceinline__ int step_of(const Unit& u, int t, int x) {
+// Step n <-> (key tile t, tile x), the key tiles counted from t0: A and B in turn, then the
+// longer one alone; in pairs, step n is key tile n.  j: tile x's j-th step.
+template <bool kPair>
+__device__ __forceinline__ int step_of(const Unit& u, int j, int x) {
   const int m = min(u.T[0], u.T[1]);
-  return t < m ? 2 * t + x : m + t;
+  return kPair || j < m ? 2 * j + x : m + j;
+}
+template <bool kPair>
+__device__ __forceinline__ int step_key(const Unit& u, int n) {
+  const int m = min(u.T[0], u.T[1]);
+  return kPair ? n : (n < 2 * m ? n >> 1 : n - m);
+}
+template <bool kPair>
+__device__ __forceinline__ int step_tile(const Unit& u, int n) {
+  return kPair || n < 2 * min(u.T[0], u.T[1]) ? n & 1 : (u.T[1] > u.T[0] ? 1 : 0);
+}
+// Whether tile x's step is the one that reads key tile t last: B's, or A's where B has none.
+template <bool kPair>
+__device__ __forceinline__ bool last_reader(const Unit& u, int t, int x) {
+  return kPair || x == 1 || t >= u.T[1];
+}
+// Key tiles that go through the CTA.
+template <bool kPair>
+__device__ __forceinline__ int key_tiles(const Unit& u) {
+  return kPair ? u.T[0] + u.T[1] : max(u.T[0], u.T[1]);
 }
 
 // ------------------------------------------------------------------ roles --
 
-template <int D>
+template <int D, bool kPair>
 __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int b, uint32_t sbase, Ctl* ctl) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   const uint64_t budget = 2 * a.timeout_ns;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-  const int T = max(u.T[0], u.T[1]);
+  const int T = key_tiles<kPair>(u);
   const int shift = min(a.page_shift, 5);   // pieces of 32 rows, or of a page of 16
   const int pieces = G::BN >> shift;
   const uint32_t bytes = static_cast<uint32_t>(G::RB) << shift;
@@ -302,9 +327,9 @@ __device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], bool odd, 
 
 // One (32 rows, block) group of a tile: the lanes read consecutive rows, 17 words apart
 // (32 banks; 34 apart at D = 128: two lanes a bank).
-template <int D, bool kLo>
+template <int D, bool kPair, bool kLo>
 __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile, int group, int n_valid, int lane) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   const int row = (group % (G::BN / 32)) * 32 + lane, blk = group / (G::BN / 32);
   const bool odd = blk & 1;
   uint8_t* hi = tile + (blk >> 1) * G::ATOM + row * 128;
@@ -330,15 +355,15 @@ __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile,
 // K of key tile i + 1, then V of key tile i: V's place in the ring is free only after
 // O's update of key tile i - 2, and K must not wait behind it.  The groups go
 // round the warps from tile to tile, so five warps share twelve (sixteen) evenly.
-template <int D, bool kExactV>
+template <int D, bool kPair, bool kExactV>
 __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w, uint8_t* smem, uint32_t sbase,
                                         Ctl* ctl) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   constexpr int kGroups = G::BN / 32 * (D / 32);   // groups of a tensor's tile: 6 or 8
   const uint64_t budget = 2 * a.timeout_ns;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-  const int T = max(u.T[0], u.T[1]);
+  const int T = key_tiles<kPair>(u);
   int mine = w;   // this warp's next group of the iteration: K's, then V's behind them
   for (int i = -1; i < T; ++i) {
     const int k = i + 1;
@@ -349,7 +374,7 @@ __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w
       const int n_valid = u.sq.kv - (u.t0 + k) * G::BN;
 #pragma unroll 1
       for (; mine < kGroups; mine += G::kDq)
-        dequant_group<D, true>(smem + G::OFF_RAW + k % G::NR * 2 * G::RAWB, smem + G::OFF_K + sd * 2 * G::TILE, mine,
+        dequant_group<D, kPair, true>(smem + G::OFF_RAW + k % G::NR * 2 * G::RAWB, smem + G::OFF_K + sd * 2 * G::TILE, mine,
                                n_valid, lane);
       fence_proxy_async_smem();
       mbar_arrive(bar(G::B_KFULL + sd));
@@ -361,7 +386,7 @@ __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w
       const int n_valid = u.sq.kv - (u.t0 + i) * G::BN;
 #pragma unroll 1
       for (; mine < kGroups; mine += G::kDq)
-        dequant_group<D, kExactV>(smem + G::OFF_RAW + i % G::NR * 2 * G::RAWB + G::RAWB,
+        dequant_group<D, kPair, kExactV>(smem + G::OFF_RAW + i % G::NR * 2 * G::RAWB + G::RAWB,
                                   smem + G::OFF_V + sd * 2 * G::TILE, mine, n_valid, lane);
       fence_proxy_async_smem();
       mbar_arrive(bar(G::B_VFULL + sd));
@@ -381,32 +406,20 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
-// Step n's key tile and tile.
-__device__ __forceinline__ int step_key(const Unit& u, int n) {
-  const int m = min(u.T[0], u.T[1]);
-  return n < 2 * m ? n >> 1 : n - m;
-}
-__device__ __forceinline__ int step_tile(const Unit& u, int n) {
-  return n < 2 * min(u.T[0], u.T[1]) ? n & 1 : (u.T[1] > u.T[0] ? 1 : 0);
-}
-// Whether tile x's step is the one that reads key tile t last: B's, or A's where B has none.
-__device__ __forceinline__ bool last_reader(const Unit& u, int t, int x) { return x == 1 || t >= u.T[1]; }
-
 // Scores.  K tiles K-major in 64-channel swizzle columns, a k-step 16 channels (32
 // bytes of the swizzled rows); Q's channels 16 k .. in TMEM columns 8 k .. of Q.
-template <int D>
+template <int D, bool kPair>
 __device__ __forceinline__ void score_mma(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   const uint64_t budget = 2 * a.timeout_ns;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
   constexpr uint32_t kIdesc = idesc_f16_f32(128, G::BN, 0, 0);
   const bool leader = elect_one();
   const uint64_t kdesc = smem_desc(sbase + G::OFF_K, 1024, 1024, kSwizzle128);
-  const uint64_t qdesc = smem_desc(sbase + G::OFF_QB, 1024, 1024, kSwizzle128);
   const int N = u.T[0] + u.T[1];
   bool ok = wait_bar(bar(G::B_Q), 0, ctl, budget, a.status);
   for (int n = 0; ok && n < N; ++n) {
-    const int t = step_key(u, n), x = step_tile(u, n), sd = t % ND, buf = n % G::NS;
+    const int t = step_key<kPair>(u, n), x = step_tile<kPair>(u, n), sd = t % ND, buf = n % G::NS;
     if (!wait_bar(bar(G::B_KFULL + sd), (t / ND) & 1, ctl, budget, a.status)) break;
     // the buffer's weights have been used by O's update of step n - G::NS
     if (n >= G::NS && !wait_bar(bar(G::B_PV + buf), (n / G::NS - 1) & 1, ctl, budget, a.status)) break;
@@ -419,14 +432,10 @@ __device__ __forceinline__ void score_mma(const PagedArgs& a, const Unit& u, uin
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t kb = kd + static_cast<uint64_t>((part * G::TILE + (k >> 2) * G::ATOM + (k & 3) * 32) >> 4);
-          if (G::QB_SMEM && x == 1)
-            mma_ss(d, qdesc + static_cast<uint64_t>(((k >> 2) * BM * 128 + (k & 3) * 32) >> 4), kb, kIdesc,
-                   (part | k) != 0 ? 1u : 0u);
-          else
-            mma_ts(d, tmem + G::T_Q + (D / 2) * x + 8 * k, kb, kIdesc, (part | k) != 0 ? 1u : 0u);
+          mma_ts(d, tmem + G::T_Q + (D / 2) * x + 8 * k, kb, kIdesc, (part | k) != 0 ? 1u : 0u);
         }
       mma_commit(bar(G::B_SFULL + buf));
-      if (last_reader(u, t, x)) mma_commit(bar(G::B_KEMPTY + sd));
+      if (last_reader<kPair>(u, t, x)) mma_commit(bar(G::B_KEMPTY + sd));
     }
     __syncwarp();
   }
@@ -439,9 +448,9 @@ __device__ __forceinline__ void score_mma(const PagedArgs& a, const Unit& u, uin
 // O's updates.  V tiles MN-major: the 64-channel halves of N one column apart (leading
 // offset), a k-step 16 keys = 2 KB.  P of keys 16 k .. sits in columns 8 k .. of its S
 // buffer.
-template <int D, bool kExactV>
+template <int D, bool kPair, bool kExactV>
 __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uint32_t sbase, uint32_t tmem, Ctl* ctl) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   const uint64_t budget = 2 * a.timeout_ns;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
   constexpr uint32_t kIdesc = idesc_f16_f32(128, D, 0, 1);
@@ -449,7 +458,7 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
   const uint64_t vdesc = smem_desc(sbase + G::OFF_V, G::ATOM, 1024, kSwizzle128);
   const int N = u.T[0] + u.T[1];
   for (int n = 0; n < N; ++n) {
-    const int t = step_key(u, n), x = step_tile(u, n), sd = t % ND, buf = n % G::NS;
+    const int t = step_key<kPair>(u, n), x = step_tile<kPair>(u, n), sd = t % ND, buf = n % G::NS;
     if (!wait_bar(bar(G::B_VFULL + sd), (t / ND) & 1, ctl, budget, a.status) ||
         !wait_bar(bar(G::B_PFULL + buf), (n / G::NS) & 1, ctl, budget, a.status))
       break;
@@ -463,8 +472,8 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
         for (int k = 0; k < G::BN / 16; ++k)
           mma_ts(o, p + 8 * k, vd + static_cast<uint64_t>((part * G::TILE + k * 2048) >> 4), kIdesc, 1u);
       mma_commit(bar(G::B_PV + buf));
-      if (t == u.T[x] - 1) mma_commit(bar(G::B_ODONE + x));
-      if (last_reader(u, t, x)) mma_commit(bar(G::B_VEMPTY + sd));
+      if ((kPair ? n >> 1 : t) == u.T[x] - 1) mma_commit(bar(G::B_ODONE + x));
+      if (last_reader<kPair>(u, t, x)) mma_commit(bar(G::B_VEMPTY + sd));
     }
     __syncwarp();
   }
@@ -473,23 +482,23 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
   wait_bar(bar(G::B_DRAIN + 1), 0, ctl, budget, a.status, false);
 }
 
-template <typename QT, int D>
+template <typename QT, int D, bool kPair>
 __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, int64_t slot, uint8_t* smem,
                                         uint32_t sbase, uint32_t tmem, Ctl* ctl) {
-  using G = Geo<D>;
+  using G = Geo<D, kPair>;
   constexpr int BN = G::BN;
   const uint64_t budget = 2 * a.timeout_ns;
   const int lane_row = threadIdx.x & 127;
   const uint32_t lane_off = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-  const int row = u.r0 + x * BM + lane_row;
+  const int row = u.r0 + (kPair ? 0 : x * BM) + lane_row;
   const bool active = row < u.n_rows;
   const int tok = row / a.group;
   const int head = u.kvh * a.group + row - tok * a.group;
   const uint32_t t_o = tmem + lane_off + G::T_O + D * x;
   const int T = u.T[x];
 
-  // ---- Q's row, as fp16 (bf16 scaled by a power of two), into TMEM or shared memory
+  // ---- Q's row, as fp16 (bf16 scaled by a power of two), into TMEM
   float sl2 = a.scale_log2;
   {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + (u.sq.q0 + tok) * a.q_stride +
@@ -528,15 +537,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
         for (int i = 0; i < 32; ++i)
           q[i] = pack_half2(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xFFFF0000u) * up);
       }
-      if (G::QB_SMEM && x == 1) {
-        uint8_t* dst = smem + G::OFF_QB + h * BM * 128 + lane_row * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(dst + ((c ^ (lane_row & 7)) * 16)) =
-              make_uint4(q[4 * c], q[4 * c + 1], q[4 * c + 2], q[4 * c + 3]);
-      } else {
-        tmem_st32(tmem + lane_off + G::T_Q + (D / 2) * x + 32 * h, q);
-      }
+      tmem_st32(tmem + lane_off + G::T_Q + (D / 2) * x + 32 * h, q);
     }
 #pragma unroll 1
     for (int h = 0; h < D / 32; ++h) {   // O = 0
@@ -555,10 +556,10 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   const float2 sl22 = make_float2(sl2, sl2);
   // keys that this row, and that every row of the tile, sees
   const int lim = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + tok + 1) : u.sq.kv;
-  const int clear = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + (u.r0 + x * BM) / a.group + 1) : u.sq.kv;
+  const int clear = a.causal ? min(u.sq.kv, u.sq.kv - u.sq.n_q + (u.r0 + (kPair ? 0 : x * BM)) / a.group + 1) : u.sq.kv;
 #pragma unroll 1
   for (int t = 0; t < T; ++t) {
-    const int n = step_of(u, t, x), buf = n % G::NS;
+    const int n = step_of<kPair>(u, t, x), buf = n % G::NS;
     const uint32_t t_s = tmem + lane_off + G::T_S + BN * buf;
     if (!wait_bar(bar(G::B_SFULL + buf), (n / G::NS) & 1, ctl, budget, a.status)) return;
     tc_fence_after();
@@ -567,7 +568,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     for (int i = 0; i < BN / 32; ++i) tmem_ld32(t_s + 32 * i, s[i]);
 #pragma unroll
     for (int i = 0; i < BN / 32; ++i) tmem_wait_ld(s[i]);
-    const int key0 = (u.t0 + t) * BN;
+    const int key0 = (u.t0 + (kPair ? 2 * t + x : t)) * BN;
     if (__builtin_expect(key0 + BN > clear, 0)) {
       const int li = lim - key0;
 #pragma unroll
@@ -607,7 +608,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
       // O is free once this tile's update before, of step p, has completed.  p is n - 2
       // (or n - 1), the buffer's earlier use p - G::NS has completed (scores n were
       // issued behind it) and its next one waits for this step, so the phase is p's.
-      const int p = step_of(u, t - 1, x);
+      const int p = step_of<kPair>(u, t - 1, x);
       if (!wait_bar(bar(G::B_PV + p % G::NS), (p / G::NS) & 1, ctl, budget, a.status)) return;
       tc_fence_after();
 #pragma unroll 1
@@ -637,10 +638,11 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     if (!wait_bar(bar(G::B_ODONE + x), 0, ctl, budget, a.status)) return;
     tc_fence_after();
   }
-  if (a.splits > 1) {
-    // the share's partial state; shares without key tiles are not read
+  if (kPair || a.splits > 1) {
+    // the share's partial state (in pairs, the tile's); shares without key tiles are not read
     if (T == 0) return;
-    const int64_t at = (slot * a.splits + blockIdx.y) * kRows + x * BM + lane_row;
+    const int64_t at = kPair ? ((slot * a.splits + blockIdx.y) * 2 + x) * BM + lane_row
+                             : (slot * a.splits + blockIdx.y) * G::ROWS + x * BM + lane_row;
     if (active) {
       float2* ml = reinterpret_cast<float2*>(a.part + a.part_ml);
       ml[at] = make_float2(m_run, l_run);
@@ -686,9 +688,9 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   }
 }
 
-template <typename QT, int D>
-__global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
-  using G = Geo<D>;
+template <typename QT, int D, bool kPair>
+__global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
+  using G = Geo<D, kPair>;
   constexpr bool kExactV = std::is_same<QT, __half>::value;
   extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const 
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + G::OFF_CTL);
   const int warp = threadIdx.x >> 5, wg = warp >> 2;
   const int64_t slot = blockIdx.x;   // row unit * kv_heads + K/V head
-  if (warp == 0) locate(a, slot / a.kv_heads, ctl, threadIdx.x & 31);
+  if (warp == 0) locate<G::ROWS>(a, slot / a.kv_heads, ctl, threadIdx.x & 31);
   if (threadIdx.x == 32) {
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t count = 1;
@@ -716,8 +718,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const 
   __syncthreads();
   if (ctl->b < 0) return;   // uniform over the CTA: more blocks than row units
   const int b = ctl->b;
-  const Unit u = make_unit<D>(a, ctl, static_cast<int>(slot % a.kv_heads), blockIdx.y);
-  if (a.splits > 1 && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
+  const Unit u = make_unit<D, kPair>(a, ctl, static_cast<int>(slot % a.kv_heads), blockIdx.y);
+  if ((kPair || a.splits > 1) && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
   if (warp == 13) {
     tmem_alloc(sbase + G::OFF_CTL, 512);
     tmem_relinquish();
@@ -728,17 +730,17 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const 
   const uint32_t tmem = ctl->tmem;
   if (wg < 2) {
     reg_alloc<G::REG_S>();
-    softmax<QT, D>(a, u, wg, slot, smem, sbase, tmem, ctl);
+    softmax<QT, D, kPair>(a, u, wg, slot, smem, sbase, tmem, ctl);
   } else {
     reg_dealloc<G::REG_O>();
     if (warp == 12) {
-      producer<D>(a, u, b, sbase, ctl);
+      producer<D, kPair>(a, u, b, sbase, ctl);
     } else if (warp == 13) {
-      score_mma<D>(a, u, sbase, tmem, ctl);
+      score_mma<D, kPair>(a, u, sbase, tmem, ctl);
     } else if (warp == 14) {
-      value_mma<D, kExactV>(a, u, sbase, tmem, ctl);
+      value_mma<D, kPair, kExactV>(a, u, sbase, tmem, ctl);
     } else {
-      dequant<D, kExactV>(a, u, warp < 12 ? warp - 8 : warp - 11, smem, sbase, ctl);
+      dequant<D, kPair, kExactV>(a, u, warp < 12 ? warp - 8 : warp - 11, smem, sbase, ctl);
     }
   }
   tc_fence_before();
@@ -750,30 +752,38 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) paged_tiles_kernel(const 
 }
 
 // Joins the shares of a unit's rows, a warp per row, in order.
-template <typename QT, int D>
+template <typename QT, int D, bool kPair>
 __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a) {
   __shared__ Ctl ctl;
   pdl_launch_dependents();
   pdl_wait();
   const int64_t slot = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) locate(a, slot / a.kv_heads, &ctl, lane);
+  if (warp == 0) locate<Geo<D, kPair>::ROWS>(a, slot / a.kv_heads, &ctl, lane);
   __syncthreads();
   if (ctl.b < 0) return;
   const int kvh = static_cast<int>(slot % a.kv_heads);
-  const Unit u = make_unit<D>(a, &ctl, kvh, 0);
+  const Unit u = make_unit<D, kPair>(a, &ctl, kvh, 0);
   const int in_unit = blockIdx.y * 8 + warp;
   const int row = u.r0 + in_unit;
   if (row >= u.n_rows) return;
-  const int tiles = tiles_of<D>(a, u.sq, u.r0 + in_unit / BM * BM, u.n_rows);
-  const int n = (tiles + u.per - 1) / u.per;   // shares with key tiles of this row's tile
+  const int tiles = tiles_of<D, kPair>(a, u.sq, u.r0 + in_unit / BM * BM, u.n_rows);
+  // shares with key tiles of this row's tile; in pairs two for each, but one for a last
+  // share of a single key tile
+  int n = (tiles + u.per - 1) / u.per;
+  if (kPair && n > 0) n = 2 * n - ((tiles - (n - 1) * u.per) < 2 ? 1 : 0);
+  constexpr int kStep = Geo<D, kPair>::ROWS;
   const float2* ml = reinterpret_cast<const float2*>(a.part + a.part_ml);
-  const int64_t at0 = slot * a.splits * kRows + in_unit;
+  const int64_t at0 = slot * a.splits * (kPair ? 2 : 1) * kStep + in_unit;
+  // with one key tile a share, the second tile's states do not exist
+  const int skip = kPair && u.per == 1 ? 2 : 1;
+  if (skip == 2) n = tiles;
   float top = -INFINITY;
-  for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + static_cast<int64_t>(z) * kRows].x);
+  for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + static_cast<int64_t>(z) * skip * kStep].x);
   float l = 0.0f, y[D / 32] = {};
+#pragma unroll 4
   for (int z = 0; z < n; ++z) {
-    const int64_t at = at0 + static_cast<int64_t>(z) * kRows;
+    const int64_t at = at0 + static_cast<int64_t>(z) * skip * kStep;
     const float2 v = ml[at];
     const float w = v.x == -INFINITY ? 0.0f : (v.x == top ? 1.0f : ex2_approx(v.x - top));
     l = fmaf(w, v.y, l);
@@ -792,10 +802,10 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   }
 }
 
-template <typename QT, int D>
+template <typename QT, int D, bool kPair>
 cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream) {
-  using G = Geo<D>;
-  auto kernel = paged_tiles_kernel<QT, D>;
+  using G = Geo<D, kPair>;
+  auto kernel = paged_tiles_kernel<QT, D, kPair>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -814,8 +824,9 @@ cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream)
   }
   const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(a.splits));
   e = launch_kernel(kernel, grid, dim3(G::kThreads), G::SMEM, stream, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  return launch_kernel(paged_tiles_join_kernel<QT, D>, dim3(grid.x, kRows / 8), dim3(256), 0, stream, a);
+  if (e != cudaSuccess || (!kPair && a.splits == 1)) return e;
+  PdlScope early;   // the join is scheduled while the last CTAs run, and waits for them
+  return launch_kernel(paged_tiles_join_kernel<QT, D, kPair>, dim3(grid.x, G::ROWS / 8), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -823,28 +834,44 @@ cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream)
 TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_kv,
                            int32_t head_dim) {
   TilesPlan p;
-  int64_t units = batch * ((max_rows + kRows - 1) / kRows);
-  if (units > total_rows / kRows + batch) units = total_rows / kRows + batch;
+  p.pair = max_rows <= BM;
+  const int64_t per = p.pair ? BM : 2 * BM;
+  int64_t units = batch * ((max_rows + per - 1) / per);
+  if (units > total_rows / per + batch) units = total_rows / per + batch;
   p.slots = units * kv_heads;
-  // One CTA runs on an SM at a time.  Fewer units than SMs share their key tiles among
-  // as many CTAs as fit into one wave, of at least eight key tiles each.
-  constexpr int64_t kSms = 152;
-  const int64_t bn = head_dim == 64 ? Geo<64>::BN : Geo<128>::BN;
-  int64_t n = p.slots > 0 ? kSms / p.slots : 1;
-  if (n > max_kv / (8 * bn)) n = max_kv / (8 * bn);
-  p.splits = static_cast<int32_t>(n < 1 ? 1 : n);
-  p.part_ml = p.splits > 1 ? p.slots * p.splits * kRows * head_dim : 0;
-  p.floats = p.splits > 1 ? p.part_ml + p.slots * p.splits * kRows * 2 : 0;
+  // One CTA runs on an SM at a time.  Shares of the key tiles: the number that makes waves x
+  // (key tiles of a share + the start and end of a CTA, worth about six) least.
+  constexpr int64_t kSms = 152, kEnds = 6;
+  const int64_t bn = head_dim == 64 ? Geo<64, false>::BN : Geo<128, false>::BN;
+  const int64_t tiles = (max_kv + bn - 1) / bn;
+  int64_t best = 1, cost = INT64_MAX;
+  for (int64_t n = 1; n <= 64 && n * 4 <= tiles + 3; ++n) {
+    if (n > 1 && p.slots * n > 4 * kSms) break;
+    const int64_t c = (p.slots * n + kSms - 1) / kSms * ((tiles + n - 1) / n + kEnds);
+    if (c < cost) {
+      cost = c;
+      best = n;
+    }
+  }
+  p.splits = static_cast<int32_t>(best);
+  const bool parts = p.pair || p.splits > 1;
+  p.part_ml = parts ? p.slots * p.splits * 2 * BM * head_dim : 0;
+  p.floats = parts ? p.part_ml + p.slots * p.splits * 2 * BM * 2 : 0;
   return p;
 }
 
-cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t slots,
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, bool pair, int64_t slots,
                                cudaStream_t stream) {
   if (slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (dtype == kF16)
-    return head_dim == 64 ? launch_tiles<__half, 64>(a, slots, stream) : launch_tiles<__half, 128>(a, slots, stream);
-  return head_dim == 64 ? launch_tiles<__nv_bfloat16, 64>(a, slots, stream)
-                        : launch_tiles<__nv_bfloat16, 128>(a, slots, stream);
+  auto go = [&](auto type, auto dim) {
+    using QT = decltype(type);
+    constexpr int kD = decltype(dim)::value;
+    return pair ? launch_tiles<QT, kD, true>(a, slots, stream) : launch_tiles<QT, kD, false>(a, slots, stream);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == kF16) return head_dim == 64 ? go(__half{}, D64{}) : go(__half{}, D128{});
+  return head_dim == 64 ? go(__nv_bfloat16{}, D64{}) : go(__nv_bfloat16{}, D128{});
 }
 
 }  // namespace q8a
