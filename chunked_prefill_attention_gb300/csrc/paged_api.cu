@@ -1,6 +1,11 @@
 // paged_api.cu -- the extern "C" entry points of the paged Q8_0 cache and of the
 // rotary positions (declared in include/q8attn.h): host-side argument validation
 // and the launches.  Every argument is checked before the first CUDA call.
+//
+// All kernels of these calls are launched with programmatic stream serialization: a
+// step of a server is a chain of short kernels, and each may be scheduled while its
+// predecessor's last CTAs run.  Each waits for the predecessor's completion before it
+// touches memory (pdl_wait), so nothing else changes.
 
 #include <cmath>
 #include <cstdarg>
@@ -32,7 +37,7 @@ constexpr int64_t kMaxTokens = int64_t{1} << 31;
 constexpr int64_t kMaxStride = int64_t{1} << 32;   // elements between tokens
 
 int check_heads(const char* fn, int32_t heads, int32_t head_dim, int32_t dtype, bool f32) {
-  if (heads <= 0 || heads > 65536) return refuse(Q8A_ERR_INVALID_ARG, fn, "heads must be 1..65536 (got %d)", heads);
+  if (heads <= 0 || heads > 65535) return refuse(Q8A_ERR_INVALID_ARG, fn, "heads must be 1..65535 (got %d)", heads);
   if (head_dim != 64 && head_dim != 128)
     return refuse(Q8A_ERR_UNSUPPORTED, fn, "head_dim must be 64 or 128 (got %d)", head_dim);
   if (dtype != Q8A_F16 && dtype != Q8A_BF16 && !(f32 && dtype == Q8A_F32))
@@ -99,6 +104,7 @@ int attn_rope(const void* x, void* out, int32_t dtype, int64_t n_tokens, int32_t
               int64_t x_token_stride, int64_t out_token_stride, const int64_t* positions, const double* inv_freq,
               int32_t rot_dim, int32_t layout, float mscale, int32_t inverse, void* stream) {
   q8a::NvtxRange nvtx_range("attn_rope");
+  q8a::PdlScope early;   // see the top of this file
   const char* fn = "attn_rope";
   if (int rc = check_heads(fn, heads, head_dim, dtype, true)) return rc;
   if (n_tokens < 0 || n_tokens > kMaxTokens)
@@ -125,6 +131,7 @@ int q8kv_append_paged(const void* k, const void* v, int32_t dtype, int64_t n_tok
                       const int64_t* positions, const double* inv_freq, int32_t rot_dim, int32_t layout, float mscale,
                       void* stream) {
   q8a::NvtxRange nvtx_range("q8kv_append_paged");
+  q8a::PdlScope early;   // see the top of this file
   const char* fn = "q8kv_append_paged";
   if (int rc = check_heads(fn, kv_heads, head_dim, dtype, true)) return rc;
   if (n_tokens < 0 || n_tokens > kMaxTokens)
@@ -155,6 +162,7 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
                     int64_t page_stride_bytes, const int64_t* slots, int64_t n_tokens, int32_t kv_heads,
                     int32_t head_dim, void* k_out, void* v_out, int32_t dtype, void* stream) {
   q8a::NvtxRange nvtx_range("q8kv_read_paged");
+  q8a::PdlScope early;   // see the top of this file
   const char* fn = "q8kv_read_paged";
   if (int rc = check_heads(fn, kv_heads, head_dim, dtype, true)) return rc;
   if (n_tokens < 0 || n_tokens > kMaxTokens)
@@ -224,6 +232,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
                const int32_t* cu_q, int64_t batch, int64_t max_q, int64_t max_kv, float scale, int32_t causal,
                void* out, float* workspace, int64_t workspace_floats, void* stream) {
   q8a::NvtxRange nvtx_range("attn_paged");
+  q8a::PdlScope early;   // see the top of this file
   const char* fn = "attn_paged";
   if (int rc = check_heads(fn, heads, head_dim, dtype, false)) return rc;
   if (kv_heads <= 0 || heads % kv_heads)

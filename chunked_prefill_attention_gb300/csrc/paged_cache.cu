@@ -26,15 +26,24 @@
 namespace q8a {
 namespace {
 
-// (cos, sin) of position * f radians, f in fp64.
-__device__ __forceinline__ float2 rotation(int64_t position, double f, float mscale, float sign) {
-  double t = f * 0.15915494309189535;   // turns per position
+// Turns per position of f radians, as a fraction of 2^64.
+__device__ __forceinline__ uint64_t turn_step(double f) {
+  double t = f * 0.15915494309189535;   // 1 / (2 pi)
   t -= floor(t);                        // [0, 1)
-  const uint64_t step = __double2ull_rn(t * 18446744073709551616.0);
+  return __double2ull_rn(t * 18446744073709551616.0);
+}
+// (cos, sin) of position * f radians.
+__device__ __forceinline__ float2 rotation(int64_t position, uint64_t step, float mscale, float sign) {
   const int64_t turns = static_cast<int64_t>(static_cast<uint64_t>(position) * step);
   float s, c;
   sincospif(static_cast<float>(turns) * 1.0842021724855044e-19f, &s, &c);   // 2^-63
   return make_float2(c * mscale, s * mscale * sign);
+}
+
+// (a cos - b sin, a sin + b cos).  Packed pairs (fma.f32x2) took the appending kernel from
+// 64 registers to 102 and from 60 to 91 us.
+__device__ __forceinline__ float2 turn_pair(float a, float b, float2 q) {
+  return make_float2(fmaf(a, q.x, -b * q.y), fmaf(a, q.y, b * q.x));
 }
 
 template <typename T>
@@ -64,94 +73,94 @@ struct alignas(N * sizeof(T)) Vec {
 // One item of a head row: a pair of vectors, one vector of whole pairs
 // (interleaved), or one vector that passes through.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;    // most tokens of a block
 constexpr int kMaxPairs = 64;
 
 // N: elements of one access.  kInter: pairs (2i, 2i + 1), else (i, i + rot / 2).
-// Block: threadIdx.x is the item of a head row, threadIdx.y steps over the
-// block's (token, head) rows, kU of them in flight.
+// A thread has one item (threadIdx.x) of one token and turns it in heads_per_thread
+// heads, so its angles are formed once, in registers; the fp64 part of them, which does
+// not depend on the token, once per block.
 template <typename T, int N, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const T* x, T* out, int64_t n_tokens, int32_t heads, int32_t head_dim, int64_t x_stride,
-            int64_t out_stride, const RopeArgs r, int32_t tokens_per_block) {
-  constexpr bool kTwo = !(kInter && N > 1);   // a rotating item is two vectors
-  constexpr int kU = 4;
-  __shared__ float2 cs[kRopeTokens * kMaxPairs];
+            int64_t out_stride, const RopeArgs r, int32_t heads_per_thread) {
+  constexpr bool kTwo = !(kInter && N > 1);         // a rotating item is two vectors
+  constexpr int kAngles = kTwo ? N : N / 2;
+  constexpr int kU = kTwo && N > 1 ? 2 : 4;         // heads in flight
+  __shared__ uint64_t steps[kMaxPairs];
   pdl_launch_dependents();
   pdl_wait();
   using V = Vec<T, N>;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_block;
-  const int n_tok = static_cast<int>(i64min(tokens_per_block, n_tokens - t0));
   const int pairs = r.rot / 2;
   const int turning = kTwo ? pairs / N : r.rot / N;   // items that rotate
   const int item = threadIdx.x;
   const bool turns = item < turning;
-  int c0, c1 = 0, pair0;
+  int c0, c1 = 0, pair0 = 0;
   if (turns) {
-    if (kTwo) {
-      c0 = kInter ? 2 * item : item * N;
-      c1 = kInter ? c0 + 1 : c0 + pairs;
-      pair0 = item * N;
-    } else {
-      c0 = item * N;
-      pair0 = c0 / 2;
-    }
+    c0 = kTwo ? (kInter ? 2 * item : item * N) : item * N;
+    c1 = kInter ? c0 + 1 : c0 + pairs;
+    pair0 = kTwo ? item * N : c0 / 2;
   } else {
     c0 = r.rot + (item - turning) * N;
-    pair0 = 0;
   }
-  const int rows = n_tok * heads;
-  const int step = blockDim.y;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int h0 = blockIdx.y * heads_per_thread;
+  const int h1 = min(heads, h0 + heads_per_thread);
+  const bool live = t < n_tokens && (turns || x != out);   // in place, the rest stays
+  const T* px = x + t * x_stride + static_cast<int64_t>(h0) * head_dim;
+  T* po = out + t * out_stride + static_cast<int64_t>(h0) * head_dim;
   V a[kU], b[kU];
-  auto load = [&](int row0) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int row = row0 + u * step;
-      if (row < rows) {
-        const T* p = x + (t0 + row / heads) * x_stride + static_cast<int64_t>(row % heads) * head_dim;
-        a[u] = *reinterpret_cast<const V*>(p + c0);
-        if (kTwo && turns) b[u] = *reinterpret_cast<const V*>(p + c1);
-      }
+  for (int u = 0; u < kU; ++u)
+    if (live && h0 + u < h1) {
+      a[u] = *reinterpret_cast<const V*>(px + u * head_dim + c0);
+      if (kTwo && turns) b[u] = *reinterpret_cast<const V*>(px + u * head_dim + c1);
     }
-  };
-  load(threadIdx.y);
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-  for (int i = tid; i < n_tok * pairs; i += blockDim.x * blockDim.y) {
-    const int t = i / pairs;
-    cs[i] = rotation(r.positions[t0 + t], r.inv_freq[i - t * pairs], r.mscale, r.sign);
-  }
+  const int64_t position = live ? r.positions[t] : 0;
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < pairs; i += blockDim.x * blockDim.y)
+    steps[i] = turn_step(r.inv_freq[i]);
   __syncthreads();
-  for (int row0 = threadIdx.y; row0 < rows; row0 += kU * step) {
-    if (row0 != threadIdx.y) load(row0);
+  if (!live) return;
+  float2 cs[kAngles];
+  if (turns) {
+#pragma unroll
+    for (int e = 0; e < kAngles; ++e) cs[e] = rotation(position, steps[pair0 + e], r.mscale, r.sign);
+  }
+  for (int h = h0;;) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int row = row0 + u * step;
-      if (row >= rows) break;
-      const int t = row / heads;
-      T* p = out + (t0 + t) * out_stride + static_cast<int64_t>(row - t * heads) * head_dim;
+      if (h + u >= h1) break;
       if (turns) {
-        const float2* k = cs + t * pairs + pair0;
         if (kTwo) {
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            const float2 q = k[e];
             const float va = Elem<T>::get(a[u].e[e]), vb = Elem<T>::get(b[u].e[e]);
-            a[u].e[e] = Elem<T>::put(fmaf(va, q.x, -vb * q.y));
-            b[u].e[e] = Elem<T>::put(fmaf(va, q.y, vb * q.x));
+            const float2 y = turn_pair(va, vb, cs[e]);
+            a[u].e[e] = Elem<T>::put(y.x);
+            b[u].e[e] = Elem<T>::put(y.y);
           }
-          *reinterpret_cast<V*>(p + c1) = b[u];
+          *reinterpret_cast<V*>(po + u * head_dim + c1) = b[u];
         } else {
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) {
-            const float2 q = k[e];
             const float va = Elem<T>::get(a[u].e[2 * e]), vb = Elem<T>::get(a[u].e[2 * e + 1]);
-            a[u].e[2 * e] = Elem<T>::put(fmaf(va, q.x, -vb * q.y));
-            a[u].e[2 * e + 1] = Elem<T>::put(fmaf(va, q.y, vb * q.x));
+            const float2 y = turn_pair(va, vb, cs[e]);
+            a[u].e[2 * e] = Elem<T>::put(y.x);
+            a[u].e[2 * e + 1] = Elem<T>::put(y.y);
           }
         }
       }
-      *reinterpret_cast<V*>(p + c0) = a[u];
+      *reinterpret_cast<V*>(po + u * head_dim + c0) = a[u];
     }
+    h += kU;
+    if (h >= h1) break;
+    px += kU * head_dim;
+    po += kU * head_dim;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (h + u < h1) {
+        a[u] = *reinterpret_cast<const V*>(px + u * head_dim + c0);
+        if (kTwo && turns) b[u] = *reinterpret_cast<const V*>(px + u * head_dim + c1);
+      }
   }
 }
 
@@ -160,15 +169,17 @@ cudaError_t launch_rope_n(const T* x, T* out, int64_t n_tokens, int32_t heads, i
                           int64_t x_stride, int64_t out_stride, const RopeArgs& r, cudaStream_t stream) {
   const bool two = !(r.interleaved && N > 1);
   const int items = (two ? r.rot / 2 / N : r.rot / N) + (head_dim - r.rot) / N;
-  const int steps = kRopeThreads / items;
-  // enough rows for four accesses a thread, but a block per token while there are few tokens
-  int64_t tpb = n_tokens < 1024 ? 1 : (4 * steps + heads - 1) / heads;
-  if (tpb > kRopeTokens) tpb = kRopeTokens;
-  const int64_t blocks = (n_tokens + tpb - 1) / tpb;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int tokens = kRopeThreads / items;
+  // as many heads a thread as leave every SM its threads
+  constexpr int64_t kFill = 152 * 2048;
+  int hpt = 8;
+  while (hpt > 1 && n_tokens * items * ((heads + hpt - 1) / hpt) < kFill) hpt /= 2;
+  const int64_t blocks = (n_tokens + tokens - 1) / tokens;
+  const int64_t groups = (heads + hpt - 1) / hpt;
+  if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
   auto kernel = r.interleaved ? rope_kernel<T, N, true> : rope_kernel<T, N, false>;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(items, steps), 0, stream, x, out, n_tokens,
-                       heads, head_dim, x_stride, out_stride, r, static_cast<int32_t>(tpb));
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(items, tokens), 0,
+                       stream, x, out, n_tokens, heads, head_dim, x_stride, out_stride, r, hpt);
 }
 
 template <typename T>
@@ -219,7 +230,10 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
   constexpr int kTok = 32 / kBlk;
   static_assert(kTok * kRow == kStageBytes, "one warp's rows");
   __shared__ __align__(16) uint8_t stage[kAppHeads][kStageBytes];
-  __shared__ float2 cs[kRope ? kTok * (kD / 2) : 1];
+  // (cos, sin) of (token, pair); a row of pairs + 1, so that the lanes of different tokens
+  // read different banks
+  __shared__ float2 cs[kRope ? kTok * (kD / 2 + 1) : 1];
+  __shared__ uint64_t steps[kRope ? kD / 2 : 1];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,26 +241,38 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
   const int first = static_cast<int>(blockIdx.x % row_tiles) * kAppHeads;   // of the block's 2 * kv_heads rows
   const int n_tok = static_cast<int>(i64min(kTok, n_tokens - t0));
   const int pairs = r.rot / 2;
-  if (kRope && first < pool.kv_heads) {   // the block has key heads
-    for (int i = threadIdx.x; i < n_tok * pairs; i += kAppThreads) {
-      const int t = i / pairs;
-      cs[i] = rotation(r.positions[t0 + t], r.inv_freq[i - t * pairs], r.mscale, r.sign);
-    }
-  }
-  if (kRope) __syncthreads();
   const int row = first + warp;
-  if (row >= 2 * pool.kv_heads) return;
+  const bool have = row < 2 * pool.kv_heads;
   const bool is_v = row >= pool.kv_heads;
   const int head = is_v ? row - pool.kv_heads : row;
   const int tok = lane / kBlk, bb = lane % kBlk;
-  const bool valid = tok < n_tok;
+  const bool valid = have && tok < n_tok;
+  // the block's values are on their way while the angles are formed
+  const T* src = nullptr;
   float x[32];
   if (valid) {
-    const T* src = (is_v ? v + (t0 + tok) * v_stride : k + (t0 + tok) * k_stride) + static_cast<int64_t>(head) * kD;
+    src = (is_v ? v + (t0 + tok) * v_stride : k + (t0 + tok) * k_stride) + static_cast<int64_t>(head) * kD;
 #pragma unroll
     for (int i = 0; i < 4; ++i) load8(src + 32 * bb + 8 * i, x + 8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+  }
+  int64_t slot = -1;   // lane t < n_tok: token t's
+  if (have && lane < n_tok) slot = slots[t0 + lane];
+  if (kRope && first < pool.kv_heads) {   // uniform: the block has key heads
+    for (int i = threadIdx.x; i < pairs; i += kAppThreads) steps[i] = turn_step(r.inv_freq[i]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_tok * pairs; i += kAppThreads) {
+      const int t = i / pairs;
+      cs[i + t] = rotation(r.positions[t0 + t], steps[i - t * pairs], r.mscale, r.sign);
+    }
+    __syncthreads();
+  }
+  if (!have) return;
+  if (valid) {
     if (kRope && !is_v) {
-      const float2* turn = cs + tok * pairs;
+      const float2* turn = cs + tok * (pairs + 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = 32 * bb + 8 * i;   // first of eight channels
@@ -255,9 +281,9 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
           for (int e = 0; e < 8; e += 2) {
             if (c + e < r.rot) {
               const float2 q = turn[(c + e) / 2];
-              const float a = x[8 * i + e], b = x[8 * i + e + 1];
-              x[8 * i + e] = fmaf(a, q.x, -b * q.y);
-              x[8 * i + e + 1] = fmaf(a, q.y, b * q.x);
+              const float2 y = turn_pair(x[8 * i + e], x[8 * i + e + 1], q);
+              x[8 * i + e] = y.x;
+              x[8 * i + e + 1] = y.y;
             }
           }
         } else if (c < r.rot) {
@@ -283,22 +309,18 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
   }
   uint32_t w[8];
   const uint32_t d = q8_block(x, w);
   if (valid) q8_put_block(&stage[warp][tok * kRow], bb, d, w);
   // lane t < kTok knows where token t's row goes (-1: nowhere)
   int64_t at = -1;
-  if (lane < n_tok) {
-    const int64_t slot = slots[t0 + lane];
+  if (slot >= 0) {
     const int64_t page = slot >> pool.page_shift;
-    if (slot >= 0 && page < pool.n_pages) {
+    if (page < pool.n_pages) {
       const int64_t off = slot & ((1ll << pool.page_shift) - 1);
       at = page * pool.page_stride + ((static_cast<int64_t>(head) << pool.page_shift) + off) * kRow;
-    } else if (slot >= 0) {
+    } else {
       *reinterpret_cast<volatile uint32_t*>(status) = kStatusIndex;
     }
   }
@@ -306,6 +328,20 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
   uint8_t* base = is_v ? pool.v : pool.k;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(stage[warp]);
   constexpr int kWords = kRow / 4;
+  // A prompt's tokens mostly fill consecutive rows of a page: then the warp's rows are
+  // one run of bytes (they end 16-byte aligned where they start so).
+  const int64_t at0 = __shfl_sync(0xFFFFFFFFu, at, 0);
+  if (__all_sync(0xFFFFFFFFu, lane >= n_tok || at == at0 + lane * kRow) && at0 >= 0) {
+    uint8_t* dst = base + at0;
+    const int n_words = n_tok * kWords;
+    if ((at0 & 15) == 0 && n_tok == kTok) {
+      for (int i = lane; i < kStageBytes / 16; i += 32)
+        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(words)[i];
+    } else {
+      for (int i = lane; i < n_words; i += 32) reinterpret_cast<uint32_t*>(dst)[i] = words[i];
+    }
+    return;
+  }
 #pragma unroll
   for (int i0 = 0; i0 < kTok * kWords; i0 += 32) {
     const int i = i0 + lane;
@@ -342,11 +378,11 @@ cudaError_t launch_append_t(const void* k, const void* v, int64_t n_tokens, int3
 // ------------------------------------------------------------------ read --
 
 constexpr int kReadThreads = 256;
+constexpr int kReadRows = 4;   // rows of a thread, in flight together
 
 // A thread takes eight channels of a head row: eight codes (two words, or
 // three where an even block's codes straddle words) and the block's scale, all
-// from one or two 32-byte sectors that its neighbours read as well.  Two
-// rows a thread are in flight.
+// from one or two 32-byte sectors that its neighbours read as well.
 template <typename T, int kD>
 __global__ void __launch_bounds__(kReadThreads)
 read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t* __restrict__ slots,
@@ -354,7 +390,7 @@ read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t*
   constexpr int kRow = kD / 32 * 34;
   constexpr int kPer = kD / 8;                     // threads of a row
   constexpr int kPass = kReadThreads / kPer;       // rows of a block and pass
-  constexpr int kU = 2;
+  constexpr int kU = kReadRows;
   pdl_launch_dependents();
   pdl_wait();
   const int j = threadIdx.x % kPer;
@@ -362,22 +398,39 @@ read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t*
   const int code0 = 34 * bb + 2 + 8 * (j % 4);     // first code's byte of the row
   const uint8_t* base = blockIdx.y ? pool.v : pool.k;
   T* out = blockIdx.y ? v : k;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (kPass * kU) + threadIdx.x / kPer;
+  // row = token * kv_heads + head: one division for the thread's first row, the others
+  // kPass further each
+  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * (kPass * kU);
+  const int64_t row0 = block0 + threadIdx.x / kPer;
+  const uint32_t heads = static_cast<uint32_t>(pool.kv_heads);
+  int64_t t = block0 / pool.kv_heads;   // uniform
+  uint32_t h = static_cast<uint32_t>(block0 - t * pool.kv_heads) + threadIdx.x / kPer;
+  t += h / heads;
+  h %= heads;
+  const uint32_t dt = kPass / heads, dh = kPass % heads;
+  int64_t slot[kU];
+  uint32_t head[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    slot[u] = row0 + u * kPass < n_rows ? __ldg(slots + t) : -1;
+    head[u] = h;
+    t += dt;
+    h += dh;
+    if (h >= heads) {
+      h -= heads;
+      ++t;
+    }
+  }
   const uint8_t* at[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
-    const int64_t row = row0 + u * kPass;
     at[u] = nullptr;
-    if (row < n_rows) {
-      const int64_t t = row / pool.kv_heads;
-      const int64_t slot = slots[t];
-      const int64_t page = slot >> pool.page_shift;
-      if (slot >= 0 && page < pool.n_pages) {
-        const int64_t off = slot & ((1ll << pool.page_shift) - 1);
-        at[u] = base + page * pool.page_stride + (((row - t * pool.kv_heads) << pool.page_shift) + off) * kRow;
-      } else if (slot >= 0) {
-        *reinterpret_cast<volatile uint32_t*>(status) = kStatusIndex;
-      }
+    const int64_t page = slot[u] >> pool.page_shift;
+    if (slot[u] >= 0 && page < pool.n_pages) {
+      const uint32_t off = static_cast<uint32_t>(slot[u]) & ((1u << pool.page_shift) - 1);
+      at[u] = base + page * pool.page_stride + ((static_cast<int64_t>(head[u]) << pool.page_shift) + off) * kRow;
+    } else if (slot[u] >= 0) {
+      *reinterpret_cast<volatile uint32_t*>(status) = kStatusIndex;
     }
   }
   uint32_t w[kU][3], d[kU];
@@ -419,7 +472,7 @@ template <typename T>
 cudaError_t launch_read_t(void* k, void* v, int64_t n_tokens, int32_t head_dim, const int64_t* slots,
                           const PagePool& pool, uint32_t* status, cudaStream_t stream) {
   const int64_t rows = n_tokens * pool.kv_heads;
-  const int64_t per = 2 * (kReadThreads / (head_dim / 8));
+  const int64_t per = kReadRows * (kReadThreads / (head_dim / 8));
   const int64_t blocks = (rows + per - 1) / per;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   auto kernel = head_dim == 64 ? read_kernel<T, 64> : read_kernel<T, 128>;

@@ -861,7 +861,6 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
   }
   e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess) return e;
-  PdlScope early;   // the join is scheduled while the last warps run, and waits for them
   return launch_kernel(paged_few_join_kernel<QT, D, NT>, dim3(ctas, kJoinY), dim3(kThreads), 0, stream, a);
 }
 

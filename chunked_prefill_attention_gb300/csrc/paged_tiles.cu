@@ -825,7 +825,6 @@ cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream)
   const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(a.splits));
   e = launch_kernel(kernel, grid, dim3(G::kThreads), G::SMEM, stream, a);
   if (e != cudaSuccess || (!kPair && a.splits == 1)) return e;
-  PdlScope early;   // the join is scheduled while the last CTAs run, and waits for them
   return launch_kernel(paged_tiles_join_kernel<QT, D, kPair>, dim3(grid.x, G::ROWS / 8), dim3(256), 0, stream, a);
 }
 

@@ -35,9 +35,13 @@ __device__ __forceinline__ uint2 code_pair(float2 x, float2 nd2, float2 y2) {
 // codes as eight little-endian words.  A zero scale, or one that overflows
 // fp16, gives codes 0.
 __device__ __forceinline__ uint32_t q8_block(const float (&v)[32], uint32_t (&w)[8]) {
-  float a = 0.0f;
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) a = fmaxf(a, fabsf(v[i]));
+  for (int i = 0; i < 32; i += 2) {   // three-input maxima
+    float& a = m[i / 2 & 3];
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(a), "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
+  }
+  const float a = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
   const __half d16 = __float2half_rn(__fdiv_rn(a, 127.0f));
   const float d = __half2float(d16);
   const bool finite_nonzero = d > 0.0f && d <= 65504.0f;

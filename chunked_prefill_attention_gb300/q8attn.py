@@ -552,7 +552,8 @@ def q8kv_read_paged(k_pages, v_pages, slots, dtype=torch.float16, out=None):
         _refuse(f"dtype {dtype} is not supported")
     shape = (T, kv_heads, head_dim)
     if out is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=slots.device).unbind(0)
+        k = torch.empty(shape, dtype=dtype, device=slots.device)
+        v = torch.empty(shape, dtype=dtype, device=slots.device)
         out = (k, v)
     else:
         k, v = out

@@ -20,7 +20,7 @@ def test_rope_refusals(lib):
         return lib.attn_rope(x, out, dtype, n, heads, D, xs, os, pos, f, rot, layout, ms, 0, N)
 
     bad = Q.Q8A_ERR_INVALID_ARG
-    for kw in (dict(n=-1), dict(n=(1 << 31) + 1), dict(heads=0), dict(heads=65537, xs=1 << 30, os=1 << 30),
+    for kw in (dict(n=-1), dict(n=(1 << 31) + 1), dict(heads=0), dict(heads=65536, xs=1 << 30, os=1 << 30),
                dict(xs=127), dict(os=64), dict(xs=(1 << 32) + 2), dict(x=N), dict(out=N), dict(pos=N), dict(f=N),
                dict(rot=0), dict(rot=33), dict(rot=66), dict(rot=-2), dict(layout=2), dict(ms=float("nan")),
                dict(ms=0.0), dict(xs=256)):   # the last: in place with two strides
