@@ -81,9 +81,11 @@ struct PagedArgs {
 
 // Few query rows per K/V head: one launch over key tiles plus the merge.
 // `rows`: the largest tokens * group of the sequences it takes (a bound).
-cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows,
+// `direct`: a CTA per (sequence, K/V head), no workspace.
+cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows, bool direct,
                              cudaStream_t stream);
-// Floats of PagedArgs::part that launch_paged_few needs.
+bool paged_few_direct(int64_t batch, int32_t kv_heads, int64_t max_kv, int32_t head_dim);
+// Floats of PagedArgs::part that launch_paged_few needs when not direct.
 int64_t paged_few_floats(int32_t head_dim, int64_t rows);
 
 // Many query rows per K/V head.  The plan of a call from its bounds: blocks

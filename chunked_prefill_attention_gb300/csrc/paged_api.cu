@@ -194,7 +194,7 @@ constexpr int64_t kFewRows = 16;
 
 // The launches of a call, from its bounds alone.
 struct Plan {
-  bool few, tiles;
+  bool few, direct, tiles;
   q8a::TilesPlan t;
   int64_t few_floats, floats;
 };
@@ -208,7 +208,8 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   p.few = !p.tiles || (total_q - (batch - 1) * max_q) * group <= kFewRows;
   if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
   const int64_t few_rows = p.tiles ? kFewRows : max_q * group;
-  p.few_floats = p.few ? q8a::paged_few_floats(head_dim, few_rows) : 0;
+  p.direct = q8a::paged_few_direct(batch, kv_heads, max_kv, head_dim);
+  p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
 }
@@ -300,7 +301,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   }
   if (plan.few && e == cudaSuccess) {
     a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;
-    e = q8a::launch_paged_few(a, dtype, head_dim, plan.tiles ? kFewRows : max_q * a.group, st);
+    e = q8a::launch_paged_few(a, dtype, head_dim, plan.tiles ? kFewRows : max_q * a.group, plan.direct, st);
   }
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
 }

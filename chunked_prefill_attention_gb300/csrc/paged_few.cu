@@ -191,7 +191,8 @@ __device__ __forceinline__ void store_pair(const PagedArgs& a, const Seq& sq, in
   }
 }
 
-template <typename QT, int D, int NT>
+// kDirect: a CTA per unit, its tiles dealt to the eight warps, nothing left to join.
+template <typename QT, int D, int NT, bool kDirect>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_few_kernel(const PagedArgs a) {
   using Sh = Shape<D>;
@@ -199,7 +200,7 @@ paged_few_kernel(const PagedArgs a) {
   constexpr int S = Sh::S, KT = Sh::KT, RW = Sh::RW, P = Sh::P, R = Pt::R, NREG = Pt::NREG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps * kStages];
-  __shared__ int64_t sums[kWarps], found[kWarps][2];
+  __shared__ int64_t sums[kDirect ? 1 : kWarps], found[kDirect ? 1 : kWarps][2];
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0)
@@ -207,59 +208,73 @@ paged_few_kernel(const PagedArgs a) {
   fence_mbar_init();
   pdl_wait();
 
-  // ---- this warp's share of all key tiles
-  int64_t mine = 0;
-  for (int b = tid; b < a.batch; b += kThreads) mine += units_of<D, NT>(a, read_seq(a, b)).all;
-  const int64_t inc = warp_inclusive(mine, lane);
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sums[w];
-  const int64_t shares = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t share = i64max(kMinShare, (total + shares - 1) / shares);
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  int32_t* desc = reinterpret_cast<int32_t*>(a.part) + gw * kDescInts;
+  // ---- this warp's share of all key tiles: [pos, end) of the tiles laid end to end
+  int64_t total, share, gw, pos0, pos, end, cta_end, base = 0;
+  int b;
+  bool inner;   // one unit holds all of the CTA's tiles
+  int32_t* desc = nullptr;
   float* parts = a.part + kMaxWarps * kDescInts;
-  if (lane == 0) desc[0] = -1;   // nothing to join at this boundary, until found otherwise
-  const int64_t pos0 = blockIdx.x * (kWarps * share);
-  if (pos0 >= total) return;     // uniform over the CTA
-  // the sequence that holds each warp's first tile
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+  if (kDirect) {
+    // tiles of this unit alone; a sequence has one row tile
+    b = blockIdx.x / a.kv_heads;
+    const auto un = units_of<D, NT>(a, read_seq(a, b));
+    if (un.row_tiles == 0) return;   // uniform
+    total = cta_end = un.tiles;
+    share = (un.tiles + kWarps - 1) / kWarps;
+    gw = pos0 = 0;
+    pos = warp * share;
+    end = i64min(total, pos + share);
+    inner = true;
+  } else {
+    int64_t mine = 0;
+    for (int b = tid; b < a.batch; b += kThreads) mine += units_of<D, NT>(a, read_seq(a, b)).all;
+    const int64_t inc = warp_inclusive(mine, lane);
+    if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    const int b = b0 + tid;
-    const int64_t v = b < a.batch ? units_of<D, NT>(a, read_seq(a, b)).all : 0;
-    const int64_t i = warp_inclusive(v, lane);
-    if (lane == 31) sums[warp] = i;
-    __syncthreads();
-    int64_t before = base + i - v;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    for (int w = 0; w < kWarps; ++w) {
-      const int64_t p = pos0 + w * share;
-      if (p >= before && p < before + v) {
-        found[w][0] = b;
-        found[w][1] = before;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += sums[w];
+    const int64_t shares = static_cast<int64_t>(gridDim.x) * kWarps;
+    share = i64max(kMinShare, (total + shares - 1) / shares);
+    gw = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    desc = reinterpret_cast<int32_t*>(a.part) + gw * kDescInts;
+    if (lane == 0) desc[0] = -1;   // nothing to join at this boundary, until found otherwise
+    pos0 = blockIdx.x * (kWarps * share);
+    if (pos0 >= total) return;     // uniform over the CTA
+    // the sequence that holds each warp's first tile
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      __syncthreads();
+      const int b = b0 + tid;
+      const int64_t v = b < a.batch ? units_of<D, NT>(a, read_seq(a, b)).all : 0;
+      const int64_t i = warp_inclusive(v, lane);
+      if (lane == 31) sums[warp] = i;
+      __syncthreads();
+      int64_t before = base + i - v;
+      for (int w = 0; w < warp; ++w) before += sums[w];
+      for (int w = 0; w < kWarps; ++w) {
+        const int64_t p = pos0 + w * share;
+        if (p >= before && p < before + v) {
+          found[w][0] = b;
+          found[w][1] = before;
+        }
       }
+      for (int w = 0; w < kWarps; ++w) base += sums[w];
+      if (base > pos0 + (kWarps - 1) * share) break;   // uniform: every warp's tile is found
     }
-    for (int w = 0; w < kWarps; ++w) base += sums[w];
-    if (base > pos0 + (kWarps - 1) * share) break;   // uniform: every warp's tile is found
+    __syncthreads();
+    pos = pos0 + warp * share;
+    end = i64min(total, pos + share);
+    cta_end = i64min(total, pos0 + kWarps * share);
+    {
+      const int b0 = static_cast<int>(found[0][0]);
+      const int64_t tiles = units_of<D, NT>(a, read_seq(a, b0)).tiles;
+      const int64_t last = (cta_end - 1 - pos0) / share;
+      inner = found[last][0] == b0 && (pos0 - found[0][1]) / tiles == (cta_end - 1 - found[0][1]) / tiles;
+    }
+    if (!inner && pos >= end) return;   // no barrier from here on, unless inner
+    b = static_cast<int>(found[inner ? 0 : warp][0]);
+    base = found[inner ? 0 : warp][1];
   }
-  __syncthreads();
-  int64_t pos = pos0 + warp * share;
-  const int64_t end = i64min(total, pos + share);
-  const int64_t cta_end = i64min(total, pos0 + kWarps * share);
-  // one unit holds all of the CTA's tiles?
-  bool inner;
-  {
-    const int b0 = static_cast<int>(found[0][0]);
-    const int64_t tiles = units_of<D, NT>(a, read_seq(a, b0)).tiles;
-    const int64_t last = (cta_end - 1 - pos0) / share;
-    inner = found[last][0] == b0 && (pos0 - found[0][1]) / tiles == (cta_end - 1 - found[0][1]) / tiles;
-  }
-  if (!inner && pos >= end) return;   // no barrier from here on, unless inner
-  int b = static_cast<int>(found[inner ? 0 : warp][0]);
-  base = found[inner ? 0 : warp][1];
 
   uint8_t* ring = smem + warp * (kStages * Sh::STAGE);
   const uint32_t ring_u = smem_u32(ring), bar_u = smem_u32(&bars[warp * kStages]);
@@ -282,8 +297,8 @@ paged_few_kernel(const PagedArgs a) {
     }
     const int64_t unit = ((inner ? pos0 : pos) - base) / un.tiles;
     const int tile0 = static_cast<int>(pos - base - unit * un.tiles);
-    const int kvh = static_cast<int>(unit / un.row_tiles);
-    const int rt = static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
+    const int kvh = kDirect ? static_cast<int>(blockIdx.x % a.kv_heads) : static_cast<int>(unit / un.row_tiles);
+    const int rt = kDirect ? 0 : static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
     const int n = static_cast<int>(inner ? i64max(0, end - pos) : i64min(un.tiles - tile0, end - pos));
     const int n_rows = sq.n_q * a.group;
 
@@ -641,7 +656,7 @@ paged_few_kernel(const PagedArgs a) {
     }
     {
       const bool whole = inner ? tile0 == 0 && cta_end - pos0 == un.tiles : n == un.tiles;
-      if (whole) {   // the whole unit: the rows of out
+      if (kDirect || whole) {   // the whole unit: the rows of out
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -846,9 +861,9 @@ __global__ void __launch_bounds__(kThreads) paged_few_join_kernel(const PagedArg
   }
 }
 
-template <typename QT, int D, int NT>
+template <typename QT, int D, int NT, bool kDirect>
 cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
-  auto kernel = paged_few_kernel<QT, D, NT>;
+  auto kernel = paged_few_kernel<QT, D, NT, kDirect>;
   constexpr int smem = Shape<D>::RING;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -860,34 +875,47 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
     configured_device = dev;
   }
   e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || kDirect) return e;
   return launch_kernel(paged_few_join_kernel<QT, D, NT>, dim3(ctas, kJoinY), dim3(kThreads), 0, stream, a);
 }
 
 template <typename QT, int D>
-cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, cudaStream_t stream) {
+cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStream_t stream) {
+  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
+  // of 108 at 64 channels, 334 instead of 194 at 128
+  if (direct) {
+    const int ctas = a.batch * a.kv_heads;
+    return rows <= 8 ? launch_few<QT, D, 1, true>(a, ctas, stream) : launch_few<QT, D, 2, true>(a, ctas, stream);
+  }
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
-  // of 108 at 64 channels, 334 instead of 194 at 128
-  return rows <= 8 ? launch_few<QT, D, 1>(a, ctas, stream) : launch_few<QT, D, 2>(a, ctas, stream);
+  return rows <= 8 ? launch_few<QT, D, 1, false>(a, ctas, stream) : launch_few<QT, D, 2, false>(a, ctas, stream);
 }
 
 }  // namespace
+
+// Whether every unit is one CTA's: no unit has more than four tiles a warp.  The shares
+// and their join would spread so few tiles further, but cost a second launch.
+bool paged_few_direct(int64_t batch, int32_t kv_heads, int64_t max_kv, int32_t head_dim) {
+  const int64_t tile = head_dim == 64 ? Shape<64>::KT : Shape<128>::KT;
+  return max_kv <= 4 * kWarps * tile && batch * kv_heads <= 0x7FFFFFFF;
+}
 
 int64_t paged_few_floats(int32_t head_dim, int64_t rows) {
   const int64_t r = rows <= 8 ? 8 : 16;
   return kMaxWarps * (kDescInts + 2 * (r * head_dim + 2 * r));
 }
 
-cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows, cudaStream_t stream) {
+cudaError_t launch_paged_few(const PagedArgs& a, int32_t dtype, int32_t head_dim, int64_t rows, bool direct,
+                             cudaStream_t stream) {
   if (dtype == kF16)
-    return head_dim == 64 ? launch_few_d<__half, 64>(a, rows, stream) : launch_few_d<__half, 128>(a, rows, stream);
-  return head_dim == 64 ? launch_few_d<__nv_bfloat16, 64>(a, rows, stream)
-                        : launch_few_d<__nv_bfloat16, 128>(a, rows, stream);
+    return head_dim == 64 ? launch_few_d<__half, 64>(a, rows, direct, stream)
+                          : launch_few_d<__half, 128>(a, rows, direct, stream);
+  return head_dim == 64 ? launch_few_d<__nv_bfloat16, 64>(a, rows, direct, stream)
+                        : launch_few_d<__nv_bfloat16, 128>(a, rows, direct, stream);
 }
 
 }  // namespace q8a

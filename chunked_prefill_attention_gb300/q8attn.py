@@ -598,16 +598,21 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
     elif not (isinstance(out, torch.Tensor) and out.dtype == q.dtype and out.get_device() == device and
               out.shape == q.shape and out.is_contiguous()):
         _refuse(f"out: a contiguous tensor {(T, H, D)} of {q.dtype} on cuda:{device} is needed")
+    ws = floats = 0
     if workspace is None:
-        workspace = torch.empty(paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D), dtype=torch.float32,
-                                device=q.device)
+        floats = paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D)
+        if floats:
+            workspace = torch.empty(floats, dtype=torch.float32, device=q.device)
+            ws = workspace.data_ptr()
     elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32 and
               workspace.get_device() == device and workspace.is_contiguous()):
         _refuse(f"workspace: a contiguous fp32 tensor on cuda:{device} is needed")
+    else:
+        ws, floats = workspace.data_ptr(), workspace.numel()
     _call(load().attn_paged, device, q.data_ptr(), code, stride, T, H, kv_heads, D, k_pages.data_ptr(),
           v_pages.data_ptr(), n_pages, page_tokens, page_stride, block_table.data_ptr(), width, lens, cu, B, max_q,
           max_kv, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+          ws, floats)
     return out
 
 

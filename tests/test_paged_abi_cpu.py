@@ -77,8 +77,9 @@ def test_attention_refusals(lib):
     bad, mis, uns = Q.Q8A_ERR_INVALID_ARG, Q.Q8A_ERR_MISALIGNED, Q.Q8A_ERR_UNSUPPORTED
     for kw in (dict(heads=0), dict(kv=0), dict(kv=3), dict(batch=-1), dict(batch=(1 << 20) + 1), dict(total=-1),
                dict(total=1 << 31), dict(mq=-1), dict(mkv=-1), dict(scale=0.0), dict(scale=float("inf")),
-               dict(qs=511), dict(pages=0), dict(pt=17), dict(q=N), dict(out=N), dict(lens=N), dict(cu=N), dict(ws=N),
-               dict(table=N), dict(ts=-1), dict(mkv=65), dict(floats=10), dict(kp=N)):
+               dict(qs=511), dict(pages=0), dict(pt=17), dict(q=N), dict(out=N), dict(lens=N), dict(cu=N), dict(table=N),
+               dict(ts=-1), dict(mkv=65), dict(kp=N), dict(ts=4096, mkv=65536, ws=N),
+               dict(ts=4096, mkv=65536, floats=10)):
         assert call(**kw) == bad, kw
     for kw in (dict(q=A8), dict(out=A8), dict(ws=A8), dict(qs=516), dict(kp=A8), dict(lens=P(0x100002))):
         assert call(**kw) == mis, kw
@@ -89,7 +90,8 @@ def test_attention_refusals(lib):
     assert lib.q8a_paged_workspace_floats(1, 1, 8, 3, 1, 1, 64) == -1
     assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1, 96) == -1
     assert lib.q8a_paged_workspace_floats(0, 1, 8, 2, 1, 1, 64) == 0
-    assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1, 64) > 0
+    assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1, 64) == 0        # a CTA per unit
+    assert lib.q8a_paged_workspace_floats(1, 1, 8, 2, 1, 1 << 20, 64) > 0
 
 
 def test_rope_frequencies():
