@@ -74,8 +74,10 @@ struct PagedArgs {
   float scale_log2;           // scale * log2(e)
   int32_t row_limit;          // sequences of at most so many rows (tokens * group) are the few-row
                               // kernel's, the others the tile kernel's
-  int32_t splits;             // tile kernel: shares of a unit's key tiles (grid rows)
+  int32_t shares;             // tile kernel: units are cut into shares of their key tiles
+  int32_t share_tiles;        // key tiles of a share; 0: from the lengths, on the device
   int64_t part_ml;            // tile kernel: floats of `part` before the shares' (m, l)
+  int64_t ctas;               // tile kernel: its grid
   uint64_t timeout_ns;
 };
 
@@ -88,18 +90,19 @@ bool paged_few_direct(int64_t batch, int32_t kv_heads, int64_t max_kv, int32_t h
 // Floats of PagedArgs::part that launch_paged_few needs when not direct.
 int64_t paged_few_floats(int32_t head_dim, int64_t rows);
 
-// Many query rows per K/V head.  The plan of a call from its bounds: blocks
-// (row units of 256 rows times K/V heads), shares of the key tiles, workspace.
+// Many query rows per K/V head.  The plan of a call from its bounds.
 struct TilesPlan {
   bool pair;        // no sequence of more than 128 rows
-  int64_t slots;
-  int32_t splits;
+  bool shares;
+  int32_t share_tiles;
+  int64_t slots;    // (row unit, K/V head) pairs, at most
+  int64_t ctas;
   int64_t part_ml;
   int64_t floats;
 };
 TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_kv,
                            int32_t head_dim);
-cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, bool pair, int64_t slots,
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
                                cudaStream_t stream);
 
 }  // namespace q8a

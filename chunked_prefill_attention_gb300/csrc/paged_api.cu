@@ -294,10 +294,12 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   if (plan.tiles) {
     q8a::PagedArgs b = a;
     b.row_limit = plan.few ? static_cast<int32_t>(kFewRows) : 0;
-    b.splits = plan.t.splits;
+    b.shares = plan.t.shares;
+    b.share_tiles = plan.t.share_tiles;
+    b.ctas = plan.t.ctas;
     b.part = workspace + plan.few_floats;
     b.part_ml = plan.t.part_ml;
-    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t.pair, plan.t.slots, st);
+    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t, st);
   }
   if (plan.few && e == cudaSuccess) {
     a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;

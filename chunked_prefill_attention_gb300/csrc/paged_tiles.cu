@@ -64,9 +64,12 @@ struct Geo {
   static constexpr int ATOMS = D / 64;                  // 64-channel swizzle columns of a tile
   static constexpr int ATOM = BN * 128;                 // bytes of one such column
   static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
-  static constexpr int NR = D == 64 ? 4 : 3;            // raw ring
+  // Raw ring.  In pairs a key tile serves 128 rows, so the copies' latency counts more: at
+  // D = 64 (16 sequences of 32,768 keys, 128 rows) 3 stages 357 us, 4 333, 6 and more the
+  // same; at D = 128 3 stages 566, 4 551.
+  static constexpr int NR = D == 64 || kPair ? 4 : 3;
   static constexpr int NS = D == 64 ? 3 : 2;            // score buffers
-  static constexpr int kThreads = D == 64 || kPair ? 640 : 512;
+  static constexpr int kThreads = kPair ? 768 : (D == 64 ? 640 : 512);
   static constexpr int kDq = kThreads / 32 - 11;        // dequantising warps
   static constexpr int ROWS = kPair ? BM : 2 * BM;      // query rows of a CTA
   // shared memory
@@ -79,13 +82,14 @@ struct Geo {
                        B_SFULL = B_VEMPTY + ND, B_PFULL = B_SFULL + NS, B_PV = B_PFULL + NS, B_ODONE = B_PV + NS, B_DRAIN = B_ODONE + 2,
                        NBAR = B_DRAIN + 2;
   static constexpr int OFF_CTL = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_CTL + 32 + 1024;      // + alignment slack
+  static constexpr int SMEM = OFF_CTL + 48 + 1024;      // + alignment slack
   static_assert(SMEM <= 227 * 1024 && TILE % 1024 == 0 && OFF_RAW % 16 == 0 && RAWB % 16 == 0, "shared memory");
   // TMEM columns
   static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + D;
   static_assert(T_END <= 512, "TMEM");
   // registers of the softmax warpgroups and of the others, out of the launch's REG_L a thread
-  static constexpr int REG_S = kThreads == 640 ? 144 : 136, REG_O = kThreads == 640 ? 64 : 120, REG_L = kThreads == 640 ? 96 : 128;
+  static constexpr int REG_S = kPair ? 128 : (D == 64 ? 144 : 136), REG_O = kPair ? 56 : (D == 64 ? 64 : 120),
+                       REG_L = kPair ? 80 : (D == 64 ? 96 : 128);
   static_assert(2 * 128 * REG_S + (kThreads - 256) * REG_O <= kThreads * REG_L, "register split");
 };
 
@@ -94,6 +98,10 @@ struct Ctl {
   uint32_t abort;
   int32_t b;      // sequence of this CTA, or -1
   int32_t unit;   // its row unit
+  int32_t kvh;    // K/V head
+  int32_t share;  // which share of the key tiles
+  int32_t per;    // key tiles of a share
+  int32_t first;  // CTA of the unit's first share
 };
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl* ctl, uint64_t budget, uint32_t* status,
@@ -174,16 +182,16 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, const Seq& sq, int r
 }
 
 template <int D, bool kPair>
-__device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, int kvh, int split) {
+__device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, int split) {
   Unit u;
   u.sq = read_seq(a, ctl->b);
-  u.kvh = kvh;
+  u.kvh = ctl->kvh;
   u.n_rows = u.sq.n_q * a.group;
   // the unit with the most visible keys first
   u.r0 = ((u.n_rows + Geo<D, kPair>::ROWS - 1) / Geo<D, kPair>::ROWS - 1 - ctl->unit) * Geo<D, kPair>::ROWS;
   const int ta = tiles_of<D, kPair>(a, u.sq, u.r0, u.n_rows);
   const int tb = kPair ? 0 : tiles_of<D, kPair>(a, u.sq, u.r0 + BM, u.n_rows);
-  u.per = max(1, (max(ta, tb) + a.splits - 1) / a.splits);
+  u.per = ctl->per;
   u.t0 = split * u.per;
   u.T[0] = max(0, min(u.per, ta - u.t0));
   u.T[1] = max(0, min(u.per, tb - u.t0));
@@ -194,37 +202,96 @@ __device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, in
   return u;
 }
 
-// Block x of the grid -> (sequence, row unit), by warp 0: the sequences' units
-// laid end to end, those of the few-row kernel left out.
-template <int kRows>
-__device__ __forceinline__ void locate(const PagedArgs& a, int64_t slot, Ctl* ctl, int lane) {
-  int64_t base = 0;
-  int found = -1, unit = 0;
-  for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t n = 0;
-    if (b < a.batch) {
-      const int64_t rows = static_cast<int64_t>(read_seq(a, b).n_q) * a.group;
-      n = rows > a.row_limit && rows <= 0x7FFFFF00 ? (rows + kRows - 1) / kRows : 0;
+// What a sequence brings: row units (0 where the few-row kernel takes it) and key tiles.
+struct Load {
+  int32_t units, tiles;
+};
+template <int D, bool kPair>
+__device__ __forceinline__ Load load_of(const PagedArgs& a, int b) {
+  using G = Geo<D, kPair>;
+  if (b >= a.batch) return Load{0, 0};
+  const Seq sq = read_seq(a, b);
+  const int64_t rows = static_cast<int64_t>(sq.n_q) * a.group;
+  return Load{rows > a.row_limit ? static_cast<int32_t>((rows + G::ROWS - 1) / G::ROWS) : 0, (sq.kv + G::BN - 1) / G::BN};
+}
+
+constexpr int kSms = 152;   // CTAs of a wave: one per SM
+constexpr int kEnds = 6;    // a CTA's start and end, in key tiles
+constexpr int kPlanned = 64;   // most sequences of a call whose shares are planned here
+
+// Key tiles of a share, by one warp: of the longest sequence's tiles cut into 1 .. 32 parts,
+// the length that makes waves x (length + a CTA's ends) least.  Lane k - 1 tries k parts.
+template <int D, bool kPair>
+__device__ __forceinline__ int plan_shares(const PagedArgs& a, int lane) {
+  if (a.share_tiles > 0) return a.share_tiles;
+  Load mine[kPlanned / 32];
+  int top = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanned / 32; ++i) {
+    mine[i] = load_of<D, kPair>(a, 32 * i + lane);
+    if (mine[i].units > 0) top = max(top, mine[i].tiles);
+  }
+  top = max(1, __reduce_max_sync(kFull, top));
+  const int len = (top + lane) / (lane + 1);
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanned / 32; ++i)
+    for (int j = 0; j < min(32, a.batch - 32 * i); ++j) {
+      const int units = __shfl_sync(kFull, mine[i].units, j), tiles = __shfl_sync(kFull, mine[i].tiles, j);
+      count += units * static_cast<int>(static_cast<unsigned>(tiles + len - 1) / static_cast<unsigned>(len));
     }
-    int64_t inc = n;
+  count *= a.kv_heads;
+  // the least cost, of equal ones the fewest parts (one part always fits the grid)
+  const bool fits = lane == 0 || (len >= 4 && count <= a.ctas);
+  const unsigned cost = static_cast<unsigned>((count + kSms - 1) / kSms) * static_cast<unsigned>(len + kEnds);
+  const unsigned best = __reduce_min_sync(kFull, fits ? min(cost, 0x03FFFFFFu) * 32u + lane : 0xFFFFFFFFu);
+  return __shfl_sync(kFull, len, best & 31u);
+}
+
+// Finds, by one warp, what block x of the grid works on: the sequences' (row unit, K/V
+// head) pairs laid end to end, each with its shares (kShares), or without (x is the pair).
+template <int D, bool kPair, bool kShares>
+__device__ __forceinline__ void locate(const PagedArgs& a, int64_t x, int per, Ctl* ctl, int lane) {
+  int64_t base = 0, ctas = 0;   // of what x counts; CTAs before the sequence
+  int found = -1, unit = 0, kvh = 0, share = 0;
+  int64_t first = 0;
+  for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
+    const Load ld = load_of<D, kPair>(a, b0 + lane);
+    const int s = (ld.tiles + per - 1) / per;
+    const int64_t pairs = static_cast<int64_t>(ld.units) * a.kv_heads;
+    const int64_t n = kShares ? pairs * s : pairs;
+    int64_t inc = n, inc_c = pairs * s;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int64_t v = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += v;
+      const int64_t v = __shfl_up_sync(kFull, inc, o), w = __shfl_up_sync(kFull, inc_c, o);
+      if (lane >= o) {
+        inc += v;
+        inc_c += w;
+      }
     }
-    const bool here = slot >= base + inc - n && slot < base + inc;
+    const bool here = x >= base + inc - n && x < base + inc;
     const unsigned who = __ballot_sync(kFull, here);
     if (who) {
       const int src = __ffs(who) - 1;
       found = b0 + src;
-      unit = static_cast<int>(__shfl_sync(kFull, slot - (base + inc - n), src));
+      const int64_t at = __shfl_sync(kFull, x - (base + inc - n), src);
+      const int shares = __shfl_sync(kFull, s, src);
+      const int64_t pair = kShares ? at / shares : at;
+      share = kShares ? static_cast<int>(at - pair * shares) : 0;
+      unit = static_cast<int>(pair / a.kv_heads);
+      kvh = static_cast<int>(pair - static_cast<int64_t>(unit) * a.kv_heads);
+      first = __shfl_sync(kFull, ctas + inc_c - pairs * s, src) + pair * shares;
     }
     base += __shfl_sync(kFull, inc, 31);
+    ctas += __shfl_sync(kFull, inc_c, 31);
   }
   if (lane == 0) {
     ctl->b = found;
     ctl->unit = unit;
+    ctl->kvh = kvh;
+    ctl->share = share;
+    ctl->per = per;
+    ctl->first = static_cast<int32_t>(first);
   }
 }
 
@@ -483,7 +550,7 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
 }
 
 template <typename QT, int D, bool kPair>
-__device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, int64_t slot, uint8_t* smem,
+__device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, uint8_t* smem,
                                         uint32_t sbase, uint32_t tmem, Ctl* ctl) {
   using G = Geo<D, kPair>;
   constexpr int BN = G::BN;
@@ -638,11 +705,10 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     if (!wait_bar(bar(G::B_ODONE + x), 0, ctl, budget, a.status)) return;
     tc_fence_after();
   }
-  if (kPair || a.splits > 1) {
-    // the share's partial state (in pairs, the tile's); shares without key tiles are not read
+  if (kPair || a.shares) {
+    // the share's partial state of the tile; one without key tiles is not read
     if (T == 0) return;
-    const int64_t at = kPair ? ((slot * a.splits + blockIdx.y) * 2 + x) * BM + lane_row
-                             : (slot * a.splits + blockIdx.y) * G::ROWS + x * BM + lane_row;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + x) * BM + lane_row;
     if (active) {
       float2* ml = reinterpret_cast<float2*>(a.part + a.part_ml);
       ml[at] = make_float2(m_run, l_run);
@@ -700,8 +766,13 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
   const uint32_t sbase = smem_u32(smem);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + G::OFF_CTL);
   const int warp = threadIdx.x >> 5, wg = warp >> 2;
-  const int64_t slot = blockIdx.x;   // row unit * kv_heads + K/V head
-  if (warp == 0) locate<G::ROWS>(a, slot / a.kv_heads, ctl, threadIdx.x & 31);
+  if (warp == 0) {
+    const int lane = threadIdx.x & 31;
+    if (kPair || a.shares)
+      locate<D, kPair, true>(a, blockIdx.x, plan_shares<D, kPair>(a, lane), ctl, lane);
+    else
+      locate<D, kPair, false>(a, blockIdx.x, 0x3FFFFFFF, ctl, lane);
+  }
   if (threadIdx.x == 32) {
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t count = 1;
@@ -716,10 +787,10 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
     fence_mbar_init();
   }
   __syncthreads();
-  if (ctl->b < 0) return;   // uniform over the CTA: more blocks than row units
+  if (ctl->b < 0) return;   // uniform over the CTA: more blocks than work
   const int b = ctl->b;
-  const Unit u = make_unit<D, kPair>(a, ctl, static_cast<int>(slot % a.kv_heads), blockIdx.y);
-  if ((kPair || a.splits > 1) && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
+  const Unit u = make_unit<D, kPair>(a, ctl, ctl->share);
+  if ((kPair || a.shares) && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
   if (warp == 13) {
     tmem_alloc(sbase + G::OFF_CTL, 512);
     tmem_relinquish();
@@ -730,7 +801,7 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
   const uint32_t tmem = ctl->tmem;
   if (wg < 2) {
     reg_alloc<G::REG_S>();
-    softmax<QT, D, kPair>(a, u, wg, slot, smem, sbase, tmem, ctl);
+    softmax<QT, D, kPair>(a, u, wg, smem, sbase, tmem, ctl);
   } else {
     reg_dealloc<G::REG_O>();
     if (warp == 12) {
@@ -757,33 +828,33 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   __shared__ Ctl ctl;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t slot = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) locate<Geo<D, kPair>::ROWS>(a, slot / a.kv_heads, &ctl, lane);
+  if (warp == 0) locate<D, kPair, false>(a, blockIdx.x, plan_shares<D, kPair>(a, lane), &ctl, lane);
   __syncthreads();
   if (ctl.b < 0) return;
-  const int kvh = static_cast<int>(slot % a.kv_heads);
-  const Unit u = make_unit<D, kPair>(a, &ctl, kvh, 0);
+  const Unit u = make_unit<D, kPair>(a, &ctl, 0);
   const int in_unit = blockIdx.y * 8 + warp;
   const int row = u.r0 + in_unit;
   if (row >= u.n_rows) return;
   const int tiles = tiles_of<D, kPair>(a, u.sq, u.r0 + in_unit / BM * BM, u.n_rows);
-  // shares with key tiles of this row's tile; in pairs two for each, but one for a last
-  // share of a single key tile
-  int n = (tiles + u.per - 1) / u.per;
-  if (kPair && n > 0) n = 2 * n - ((tiles - (n - 1) * u.per) < 2 ? 1 : 0);
-  constexpr int kStep = Geo<D, kPair>::ROWS;
+  // states of this row's tile: one for each share with key tiles of it (tile in_unit / 128 of
+  // the CTA's two); in pairs two, but one for a share of a single key tile
+  const int full = (tiles + u.per - 1) / u.per;
+  if (static_cast<int64_t>(ctl.first) + full > a.ctas) {   // lengths beyond the call's bounds
+    *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+    return;
+  }
+  const bool two = kPair && u.per > 1;
+  const int n = two && full > 0 ? 2 * full - (tiles - (full - 1) * u.per < 2 ? 1 : 0) : full;
+  const int64_t step = two ? BM : 2 * BM;
+  const int64_t at0 = static_cast<int64_t>(ctl.first) * 2 * BM + in_unit;
   const float2* ml = reinterpret_cast<const float2*>(a.part + a.part_ml);
-  const int64_t at0 = slot * a.splits * (kPair ? 2 : 1) * kStep + in_unit;
-  // with one key tile a share, the second tile's states do not exist
-  const int skip = kPair && u.per == 1 ? 2 : 1;
-  if (skip == 2) n = tiles;
   float top = -INFINITY;
-  for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + static_cast<int64_t>(z) * skip * kStep].x);
+  for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + z * step].x);
   float l = 0.0f, y[D / 32] = {};
 #pragma unroll 4
   for (int z = 0; z < n; ++z) {
-    const int64_t at = at0 + static_cast<int64_t>(z) * skip * kStep;
+    const int64_t at = at0 + z * step;
     const float2 v = ml[at];
     const float w = v.x == -INFINITY ? 0.0f : (v.x == top ? 1.0f : ex2_approx(v.x - top));
     l = fmaf(w, v.y, l);
@@ -792,7 +863,7 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int tok = row / a.group;
-  QT* dst = static_cast<QT*>(a.out) + ((u.sq.q0 + tok) * a.heads + kvh * a.group + row - tok * a.group) * D;
+  QT* dst = static_cast<QT*>(a.out) + ((u.sq.q0 + tok) * a.heads + u.kvh * a.group + row - tok * a.group) * D;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     if (std::is_same<QT, __half>::value)
@@ -803,7 +874,7 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
 }
 
 template <typename QT, int D, bool kPair>
-cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream) {
+cudaError_t launch_tiles(const PagedArgs& a, const TilesPlan& plan, cudaStream_t stream) {
   using G = Geo<D, kPair>;
   auto kernel = paged_tiles_kernel<QT, D, kPair>;
   static thread_local int configured_device = -1;
@@ -822,10 +893,9 @@ cudaError_t launch_tiles(const PagedArgs& a, int64_t slots, cudaStream_t stream)
       return cudaErrorInvalidConfiguration;
     configured_device = dev;
   }
-  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(a.splits));
-  e = launch_kernel(kernel, grid, dim3(G::kThreads), G::SMEM, stream, a);
-  if (e != cudaSuccess || (!kPair && a.splits == 1)) return e;
-  return launch_kernel(paged_tiles_join_kernel<QT, D, kPair>, dim3(grid.x, G::ROWS / 8), dim3(256), 0, stream, a);
+  e = launch_kernel(kernel, dim3(static_cast<unsigned>(plan.ctas)), dim3(G::kThreads), G::SMEM, stream, a);
+  if (e != cudaSuccess || !(kPair || a.shares)) return e;
+  return launch_kernel(paged_tiles_join_kernel<QT, D, kPair>, dim3(static_cast<unsigned>(plan.slots), G::ROWS / 8), dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -838,34 +908,35 @@ TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, 
   int64_t units = batch * ((max_rows + per - 1) / per);
   if (units > total_rows / per + batch) units = total_rows / per + batch;
   p.slots = units * kv_heads;
-  // One CTA runs on an SM at a time.  Shares of the key tiles: the number that makes waves x
-  // (key tiles of a share + the start and end of a CTA, worth about six) least.
-  constexpr int64_t kSms = 152, kEnds = 6;
+  // Few pairs of row unit and K/V head are cut into shares of their key tiles: by the lengths
+  // themselves, on the device, or for many sequences by the bounds.  Up to 76 pairs fill
+  // one wave of SMs with at least two shares each; 77 to 101 two waves with three; from there
+  // on only lengths that differ give anything to share.  4 sequences of 8,192 to 32,768
+  // keys, 64 rows, 8 K/V heads: 95 us with nine shares each, 64 so (64 channels), 152
+  // and 97 (128 channels).
   const int64_t bn = head_dim == 64 ? Geo<64, false>::BN : Geo<128, false>::BN;
   const int64_t tiles = (max_kv + bn - 1) / bn;
-  int64_t best = 1, cost = INT64_MAX;
-  for (int64_t n = 1; n <= 64 && n * 4 <= tiles + 3; ++n) {
-    if (n > 1 && p.slots * n > 4 * kSms) break;
-    const int64_t c = (p.slots * n + kSms - 1) / kSms * ((tiles + n - 1) / n + kEnds);
-    if (c < cost) {
-      cost = c;
-      best = n;
-    }
+  p.shares = tiles >= 8 && (p.slots <= kSms * 2 / 3 || (batch > 1 && p.slots <= kSms));
+  p.share_tiles = p.pair ? 0x3FFFFFFF : 0;
+  p.ctas = p.slots;
+  if (p.shares) {
+    p.ctas = p.slots > kSms / 2 && p.slots <= kSms * 2 / 3 ? 2 * kSms : kSms;
+    const int64_t n = p.ctas / p.slots;
+    p.share_tiles = batch <= kPlanned ? 0 : static_cast<int32_t>((tiles + n - 1) / n);
   }
-  p.splits = static_cast<int32_t>(best);
-  const bool parts = p.pair || p.splits > 1;
-  p.part_ml = parts ? p.slots * p.splits * 2 * BM * head_dim : 0;
-  p.floats = parts ? p.part_ml + p.slots * p.splits * 2 * BM * 2 : 0;
+  const int64_t states = p.shares || p.pair ? p.ctas * 2 * BM : 0;
+  p.part_ml = states * head_dim;
+  p.floats = states * (head_dim + 2);
   return p;
 }
 
-cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, bool pair, int64_t slots,
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
                                cudaStream_t stream) {
-  if (slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (plan.ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   auto go = [&](auto type, auto dim) {
     using QT = decltype(type);
     constexpr int kD = decltype(dim)::value;
-    return pair ? launch_tiles<QT, kD, true>(a, slots, stream) : launch_tiles<QT, kD, false>(a, slots, stream);
+    return plan.pair ? launch_tiles<QT, kD, true>(a, plan, stream) : launch_tiles<QT, kD, false>(a, plan, stream);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
