@@ -249,6 +249,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
     return rc;
   if (!q || !out || !kv_lens || !cu_q || (table_stride > 0 && !block_table))
     return refuse(Q8A_ERR_INVALID_ARG, fn, "null pointer");
+  if (out == q) return refuse(Q8A_ERR_INVALID_ARG, fn, "out must not be q");
   if (table_stride < 0 || table_stride > 0x7FFFFFFFll)
     return refuse(Q8A_ERR_INVALID_ARG, fn, "table stride must be 0..2^31-1 (got %lld)", (long long)table_stride);
   if (max_kv > table_stride * page_tokens)

@@ -60,7 +60,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
 constexpr int kMaxCtas = 320;      // two per SM of 160 SMs
 constexpr int kMaxWarps = kMaxCtas * kWarps;
 constexpr int kMinShare = 2;       // tiles of a warp's share
@@ -68,7 +67,7 @@ constexpr int kDescInts = 8;       // join record of a share boundary
 constexpr float kLazy = 8.0f;      // the reference moves when exceeded by more than 2^8
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-template <int D>
+template <int D, int NT>
 struct Shape {
   static constexpr int S = 256 / D;              // keys of a lane group and tile
   static constexpr int KT = 8 * S;               // keys of a tile: 32 or 16
@@ -76,7 +75,13 @@ struct Shape {
   static constexpr int RW = 17 * P;              // words of a row
   static constexpr int TILE = KT * RW * 4;       // bytes of a tensor's tile: 2176
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int RING = kWarps * kStages * STAGE;
+  // 16 rows of 128 channels: Q^T's fragments stay in shared memory (in registers they spill
+  // 324 bytes a thread) and take a stage of the ring
+  static constexpr bool QS = NT * D >= 256;
+  static constexpr int STAGES = QS ? 2 : 3;
+  static constexpr int RING = kWarps * STAGES * STAGE;
+  static constexpr int QBYTES = QS ? P * 4 * NT * 32 * 8 : 0;   // of a warp
+  static constexpr int SMEM = RING + kWarps * QBYTES;
 };
 
 template <int D, int NT>
@@ -158,7 +163,7 @@ template <int D, int NT>
 __device__ __forceinline__ Units<D, NT> units_of(const PagedArgs& a, const Seq& s) {
   Units<D, NT> u;
   const int64_t rows = static_cast<int64_t>(s.n_q) * a.group;
-  u.tiles = max(1, (s.kv + Shape<D>::KT - 1) / Shape<D>::KT);
+  u.tiles = max(1, (s.kv + Shape<D, NT>::KT - 1) / Shape<D, NT>::KT);
   u.row_tiles = rows > a.row_limit ? 0 : static_cast<int32_t>((rows + 8 * NT - 1) / (8 * NT));
   u.all = static_cast<int64_t>(u.tiles) * u.row_tiles * a.kv_heads;
   return u;
@@ -195,8 +200,9 @@ __device__ __forceinline__ void store_pair(const PagedArgs& a, const Seq& sq, in
 template <typename QT, int D, int NT, bool kDirect>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_few_kernel(const PagedArgs a) {
-  using Sh = Shape<D>;
+  using Sh = Shape<D, NT>;
   using Pt = Part<D, NT>;
+  constexpr int kStages = Sh::STAGES;
   constexpr int S = Sh::S, KT = Sh::KT, RW = Sh::RW, P = Sh::P, R = Pt::R, NREG = Pt::NREG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps * kStages];
@@ -340,7 +346,8 @@ paged_few_kernel(const PagedArgs a) {
     int next_page = fetch(kStages);
 
     // ---- Q^T fragments: lane (g, t) holds row 8 nt + g, the channels of its words
-    uint32_t qf[NT][P][4][2];
+    uint32_t qf[Sh::QS ? 1 : NT][P][4][2];
+    uint2* qs = reinterpret_cast<uint2*>(smem + Sh::RING + warp * Sh::QBYTES) + lane;
     float sl2[NT][2];
     int lim[NT][2];   // keys that the row of column 2 t (+ 1) sees
 #pragma unroll
@@ -389,8 +396,15 @@ paged_few_kernel(const PagedArgs a) {
             uint32_t x = raw[p][st][h];
             if (!std::is_same<QT, __half>::value)
               x = pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up);
-            qf[nt][p][st][h] = x;
+            qf[Sh::QS ? 0 : nt][p][st][h] = x;
           }
+      if (Sh::QS) {   // each lane keeps its own
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+            qs[((p * 4 + st) * NT + nt) * 32] = make_uint2(qf[0][p][st][0], qf[0][p][st][1]);
+      }
       const float sc = a.scale_log2 * down;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -450,10 +464,15 @@ paged_few_kernel(const PagedArgs a) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(x, f[0], qf[nt][p][0][0], qf[nt][p][0][1]);
-            mma16816(y, f[2], qf[nt][p][2][0], qf[nt][p][2][1]);
-            mma16816(x, f[1], qf[nt][p][1][0], qf[nt][p][1][1]);
-            mma16816(y, f[3], qf[nt][p][3][0], qf[nt][p][3][1]);
+            uint2 q[4];
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              q[st] = Sh::QS ? qs[((p * 4 + st) * NT + nt) * 32]
+                             : make_uint2(qf[Sh::QS ? 0 : nt][p][st][0], qf[Sh::QS ? 0 : nt][p][st][1]);
+            mma16816(x, f[0], q[0].x, q[0].y);
+            mma16816(y, f[2], q[2].x, q[2].y);
+            mma16816(x, f[1], q[1].x, q[1].y);
+            mma16816(y, f[3], q[3].x, q[3].y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float d0 = e < 2 ? da0 : db0, d1 = e < 2 ? da1 : db1;
@@ -864,7 +883,7 @@ __global__ void __launch_bounds__(kThreads) paged_few_join_kernel(const PagedArg
 template <typename QT, int D, int NT, bool kDirect>
 cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
   auto kernel = paged_few_kernel<QT, D, NT, kDirect>;
-  constexpr int smem = Shape<D>::RING;
+  constexpr int smem = Shape<D, NT>::SMEM;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -900,7 +919,7 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStre
 // Whether every unit is one CTA's: no unit has more than four tiles a warp.  The shares
 // and their join would spread so few tiles further, but cost a second launch.
 bool paged_few_direct(int64_t batch, int32_t kv_heads, int64_t max_kv, int32_t head_dim) {
-  const int64_t tile = head_dim == 64 ? Shape<64>::KT : Shape<128>::KT;
+  const int64_t tile = head_dim == 64 ? Shape<64, 1>::KT : Shape<128, 1>::KT;
   return max_kv <= 4 * kWarps * tile && batch * kv_heads <= 0x7FFFFFFF;
 }
 

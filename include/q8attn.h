@@ -492,8 +492,8 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *   cu_q         int32 [batch + 1] on the device: sequence b's rows are
  *                cu_q[b] .. cu_q[b + 1] - 1 of q (none is allowed); not decreasing,
  *                at most total_q.  Rows from cu_q[batch] on are left as they were.
- *   max_q, max_kv  upper bounds of the sequences' rows and kv_lens (they size the
- *                launches; rows beyond max_q may be left as they were).
+ *   max_q, max_kv  upper bounds of the sequences' rows and kv_lens.  They size the
+ *                launches: of a sequence beyond them some rows may be left as they were.
  *   out          [total_q][heads][D] of q's type, contiguous, 16-byte aligned; not q.
  *   workspace    fp32 scratch, 16-byte aligned, of at least
  *                q8a_paged_workspace_floats(batch, total_q, heads, kv_heads,

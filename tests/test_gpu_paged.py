@@ -577,3 +577,186 @@ def test_captured_step_replays_with_new_lengths(Q):
         assert torch.equal(kp, mirror[0]) and torch.equal(vp, mirror[1])
         assert torch.equal(got, Q.attn_paged(q, kp, vp, table, lens, cu, 1, width * page))
         assert (got[3] == 0).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([300, 1, 60], [300, 700, 900]), ([100, 20], [5000, 300]), ([9], [70])])
+def test_captured_prompts_replay(Q, q_lens, kv_lens):
+    """A captured call over prompts, replayed after the lengths shrink; two graphs of one stream share a workspace."""
+    x = Batch(q_lens, kv_lens, 8, 2, 64, 32, F16, seed=21)
+    y = Batch(q_lens[::-1], kv_lens[::-1], 8, 2, 64, 32, F16, seed=22)
+    n = Q.paged_workspace_floats(len(q_lens), x.n_rows, 8, 2, max(q_lens), max(kv_lens), 64)
+    ws = torch.empty(max(n, 1), device="cuda")
+    outs, graphs = [torch.zeros_like(b.q) for b in (x, y)], []
+    for b, out in zip((x, y), outs):
+        Q.attn_paged(*b.args(), out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            Q.attn_paged(*b.args(), out=out, workspace=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(5.0)
+        graphs[0].replay()
+        graphs[1].replay()
+        x.check(outs[0])
+        y.check(outs[1])
+    # shorter sequences within the captured bounds: the first keeps its first rows' keys only
+    drop = q_lens[0] // 2
+    x.kv_lens[0] -= drop
+    x.cu_q[1:] -= drop
+    outs[0].fill_(5.0)
+    graphs[0].replay()
+    short = Q.attn_paged(x.q, x.k_pages, x.v_pages, x.table, x.kv_lens, x.cu_q, max(q_lens), max(kv_lens),
+                         out=torch.full_like(x.q, 5.0))
+    assert torch.equal(outs[0], short)
+    assert (outs[0][x.n_rows - drop:] == 5.0).all()
+
+
+def test_two_streams_at_once(Q):
+    """Independent calls on two streams, each with its own workspace."""
+    a = Batch([1, 1], [40000, 3000], 8, 2, 128, 64, BF16, seed=31)
+    b = Batch([400], [2000], 4, 2, 64, 16, F16, seed=32)
+    want = [Q.attn_paged(*x.args()) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        for s, x in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(Q.attn_paged(*x.args()))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])
+    a.check(want[0])
+    b.check(want[1])
+
+
+def guarded(shape, dtype, fill=0x5A):
+    """A tensor with 256 guard bytes on both sides."""
+    n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+    raw = torch.full((n + 512,), fill, dtype=torch.uint8, device="cuda")
+    return raw[256:256 + n].view(dtype).view(shape), raw, fill
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 2100]), ([5, 3], [40, 3000]), ([40, 17], [700, 90]),
+                                            ([200, 30], [500, 1000]), ([300], [300])])
+def test_nothing_is_written_beside_the_buffers(Q, q_lens, kv_lens, D, page):
+    x = Batch(q_lens, kv_lens, 8, 2, D, page, F16, seed=41)
+    args = x.args()
+    pools = (x.k_pages.clone(), x.v_pages.clone())
+    out, out_raw, _ = guarded(x.q.shape, F16)
+    n = Q.paged_workspace_floats(len(q_lens), x.n_rows, 8, 2, max(q_lens), max(kv_lens), D)
+    ws, ws_raw, _ = guarded((max(n, 4),), F32)
+    Q.attn_paged(*args, out=out, workspace=ws)
+    x.check(out)
+    for raw in (out_raw, ws_raw):
+        assert (raw[:256] == 0x5A).all() and (raw[-256:] == 0x5A).all()
+    assert torch.equal(x.k_pages, pools[0]) and torch.equal(x.v_pages, pools[1])
+    # append and rope into guarded buffers
+    T = 37
+    k = torch.randn((T, 2, D), device="cuda", generator=gen(2))
+    pages, raw_k, _ = guarded((3, 2, page, D // 32 * 34), torch.uint8)
+    pages_v, raw_v, _ = guarded((3, 2, page, D // 32 * 34), torch.uint8)
+    slots = torch.arange(3 * page - T, 3 * page, device="cuda")
+    Q.q8kv_append_paged(k, k, pages, pages_v, slots)
+    rot, rot_raw, _ = guarded((T, 2, D), F32)
+    Q.attn_rope(k, torch.arange(T, device="cuda"), Q.rope_inv_freq(D, device="cuda"), out=rot)
+    rd, rd_raw, _ = guarded((T, 2, D), BF16)
+    rd2, rd2_raw, _ = guarded((T, 2, D), BF16)
+    Q.q8kv_read_paged(pages, pages_v, slots, BF16, out=(rd, rd2))
+    for raw in (raw_k, raw_v, rot_raw, rd_raw, rd2_raw):
+        assert (raw[:256] == 0x5A).all() and (raw[-256:] == 0x5A).all()
+    used = torch.zeros((3, page), dtype=torch.bool, device="cuda")
+    used.view(-1)[slots] = True
+    assert (pages.transpose(1, 2)[~used] == 0x5A).all() and (pages_v.transpose(1, 2)[~used] == 0x5A).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(Q, seed):
+    rng = np.random.default_rng(seed)
+    D, page = int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128, 256, 1024]))
+    kv_heads = int(rng.integers(1, 4))
+    group = int(rng.choice([1, 2, 3, 4, 5, 8]))
+    B = int(rng.integers(1, 7))
+    top = int(rng.choice([1, 4, 30, 130, 500]))
+    q_lens = [int(rng.integers(0, top + 1)) for _ in range(B)]
+    if sum(q_lens) == 0:
+        q_lens[0] = 1
+    kv_lens = [int(n + rng.integers(0, int(rng.choice([2, 100, 4000])))) for n in q_lens]
+    if seed % 5 == 0:
+        kv_lens[0] = max(0, q_lens[0] - 1)
+    kv_lens[-1] = max(kv_lens[-1], 1)
+    causal, dtype = bool(rng.random() < 0.7), [F16, BF16][seed % 2]
+    x = Batch(q_lens, kv_lens, kv_heads * group, kv_heads, D, page, dtype, seed=seed, interleave_pools=seed % 3 == 0)
+    x.check(Q.attn_paged(*x.args(), causal=causal), causal)
+
+
+def test_offsets_beyond_32_bits(Q):
+    """Pages and rows whose byte offsets pass 2^32 (the pools are 5.7 GB each)."""
+    D, HK, page, n_pages = 128, 8, 256, 20500
+    kp = torch.zeros((n_pages, HK, page, 136), dtype=torch.uint8, device="cuda")
+    vp = torch.zeros_like(kp)
+    g = gen(51)
+    at = torch.tensor([n_pages - 1, 3, n_pages - 2], dtype=torch.int32, device="cuda")
+    n = 700
+    k, v = (torch.randn((n, HK, D), generator=g, device="cuda").half() for _ in range(2))
+    pos = torch.arange(n, device="cuda")
+    slots = at[pos // page].long() * page + pos % page
+    Q.q8kv_append_paged(k, v, kp, vp, slots)
+    assert torch.equal(at_slots(kp, slots).cpu(), rows_of(k)) and torch.equal(at_slots(vp, slots).cpu(), rows_of(v))
+    k2, v2 = Q.q8kv_read_paged(kp, vp, slots, F32)
+    for q_len in (1, 30, 300):
+        x = Batch.__new__(Batch)
+        x.group, x.D, x.page, x.q_lens, x.kv_lens_host = 2, D, page, [q_len], [n]
+        x.q = torch.randn((q_len, 2 * HK, D), generator=g, device="cuda").half()
+        x.k, x.v = [k2.double()], [v2.double()]
+        out = Q.attn_paged(x.q, kp, vp, at[None], torch.tensor([n], dtype=torch.int32, device="cuda"),
+                           torch.tensor([0, q_len], dtype=torch.int32, device="cuda"), q_len, n)
+        x.check(out)
+    assert kp[:3].count_nonzero() == 0 and vp[4:n_pages - 2].count_nonzero() == 0
+
+
+def test_binding_refusals(Q):
+    """What shapes, types, strides and devices tell is refused before the call."""
+    x = Batch([2], [40], 4, 2, 64, 16, F16)
+    q, kp, vp, table, lens, cu, mq, mkv = x.args()
+    bad = [
+        dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)), dict(q=q.cpu()), dict(kp=kp.int()),
+        dict(kp=kp[:, :, ::2]), dict(kp=kp[:1]), dict(vp=vp[:, :1]), dict(table=table.long()), dict(table=table[0]),
+        dict(table=table.t()), dict(lens=lens.long()), dict(lens=lens[:0]), dict(cu=cu[:1]), dict(cu=cu.float()),
+        dict(mkv=10 ** 9), dict(mq=-1), dict(scale=0.0), dict(out=q), dict(out=torch.empty_like(q)[:1]),
+        dict(out=torch.empty_like(q).float()), dict(workspace=torch.empty(4, device="cuda").half()),
+    ]
+    for kw in bad:
+        a = dict(q=q, kp=kp, vp=vp, table=table, lens=lens, cu=cu, mq=mq, mkv=mkv, scale=None, out=None, workspace=None)
+        a.update(kw)
+        with pytest.raises(Q.Q8AttnError):
+            Q.attn_paged(a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["cu"], a["mq"], a["mkv"], scale=a["scale"],
+                         out=a["out"], workspace=a["workspace"])
+    f, pos, slots = Q.rope_inv_freq(64, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda"), \
+        torch.zeros(2, dtype=torch.int64, device="cuda")
+    for args in [(q.int(), pos, f), (q, pos.int(), f), (q, pos[:1], f), (q, pos, f.float()), (q, pos, f[:0]),
+                 (q, pos, torch.cat([f, f])), (q, pos.cpu(), f), (q[..., :32], pos, f)]:
+        with pytest.raises(Q.Q8AttnError):
+            Q.attn_rope(*args)
+    with pytest.raises(Q.Q8AttnError):
+        Q.attn_rope(q, pos, f, out=q[:1])
+    k = q[:, :2].contiguous()
+    for args in [(k, k.float(), kp, vp, slots), (k, k[:1], kp, vp, slots), (q, q, kp, vp, slots),
+                 (k, k, kp, vp, slots.int()), (k, k, kp, vp, slots[:1]), (k, k, kp, vp, slots, pos),
+                 (k, k, kp, vp, slots, None, f), (k.double(), k.double(), kp, vp, slots)]:
+        with pytest.raises(Q.Q8AttnError):
+            Q.q8kv_append_paged(*args)
+    for args in [(kp, vp, slots.int()), (kp, vp, slots.cpu()), (kp, vp, slots, torch.float64),
+                 (kp, vp, slots, F16, (k[:1], k)), (kp, vp[:1], slots)]:
+        with pytest.raises(Q.Q8AttnError):
+            Q.q8kv_read_paged(*args)
+    for kw in (dict(factor=2.0, scaling="base"), dict(factor=2.0, scaling="bands", original_len=100)):
+        assert Q.rope_inv_freq(32, device="cuda", **kw).is_cuda
+    # empty calls
+    assert Q.attn_rope(q[:0], pos[:0], f).shape == (0, 4, 64)
+    Q.q8kv_append_paged(k[:0], k[:0], kp, vp, slots[:0])
+    assert Q.q8kv_read_paged(kp, vp, slots[:0])[0].shape == (0, 2, 64)
+    assert Q.attn_paged(q[:0], kp, vp, table, lens, cu * 0, 0, mkv).shape == (0, 4, 64)

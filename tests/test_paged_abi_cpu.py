@@ -68,7 +68,7 @@ def test_append_and_read_refusals(lib):
 def test_attention_refusals(lib):
     from chunked_prefill_attention_gb300 import q8attn as Q
 
-    def call(q=A16, dtype=0, qs=512, total=10, heads=8, kv=2, D=64, kp=A16, vp=A16, pages=3, pt=16,
+    def call(q=P(0x200000), dtype=0, qs=512, total=10, heads=8, kv=2, D=64, kp=A16, vp=A16, pages=3, pt=16,
              stride=2 * 16 * 68, table=A4, ts=4, lens=A4, cu=A4, batch=2, mq=5, mkv=64, scale=0.125, out=A16, ws=A16,
              floats=1 << 30):
         return lib.attn_paged(q, dtype, qs, total, heads, kv, D, kp, vp, pages, pt, stride, table, ts, lens, cu, batch,
@@ -77,7 +77,7 @@ def test_attention_refusals(lib):
     bad, mis, uns = Q.Q8A_ERR_INVALID_ARG, Q.Q8A_ERR_MISALIGNED, Q.Q8A_ERR_UNSUPPORTED
     for kw in (dict(heads=0), dict(kv=0), dict(kv=3), dict(batch=-1), dict(batch=(1 << 20) + 1), dict(total=-1),
                dict(total=1 << 31), dict(mq=-1), dict(mkv=-1), dict(scale=0.0), dict(scale=float("inf")),
-               dict(qs=511), dict(pages=0), dict(pt=17), dict(q=N), dict(out=N), dict(lens=N), dict(cu=N), dict(table=N),
+               dict(qs=511), dict(pages=0), dict(pt=17), dict(q=N), dict(out=N), dict(lens=N), dict(cu=N), dict(table=N), dict(q=A16),
                dict(ts=-1), dict(mkv=65), dict(kp=N), dict(ts=4096, mkv=65536, ws=N),
                dict(ts=4096, mkv=65536, floats=10)):
         assert call(**kw) == bad, kw
