@@ -82,7 +82,7 @@ struct Geo {
                        B_SFULL = B_VEMPTY + ND, B_PFULL = B_SFULL + NS, B_PV = B_PFULL + NS, B_ODONE = B_PV + NS, B_DRAIN = B_ODONE + 2,
                        NBAR = B_DRAIN + 2;
   static constexpr int OFF_CTL = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_CTL + 48 + 1024;      // + alignment slack
+  static constexpr int SMEM = OFF_CTL + 64 + 1024;      // + alignment slack
   static_assert(SMEM <= 227 * 1024 && TILE % 1024 == 0 && OFF_RAW % 16 == 0 && RAWB % 16 == 0, "shared memory");
   // TMEM columns
   static constexpr uint32_t T_S = 0, T_O = NS * BN, T_Q = T_O + 2 * D, T_END = T_Q + D;
@@ -102,6 +102,7 @@ struct Ctl {
   int32_t share;  // which share of the key tiles
   int32_t per;    // key tiles of a share
   int32_t first;  // CTA of the unit's first share
+  Seq sq;
 };
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl* ctl, uint64_t budget, uint32_t* status,
@@ -184,7 +185,7 @@ __device__ __forceinline__ int tiles_of(const PagedArgs& a, const Seq& sq, int r
 template <int D, bool kPair>
 __device__ __forceinline__ Unit make_unit(const PagedArgs& a, const Ctl* ctl, int split) {
   Unit u;
-  u.sq = read_seq(a, ctl->b);
+  u.sq = ctl->sq;
   u.kvh = ctl->kvh;
   u.n_rows = u.sq.n_q * a.group;
   // the unit with the most visible keys first
@@ -292,6 +293,7 @@ __device__ __forceinline__ void locate(const PagedArgs& a, int64_t x, int per, C
     ctl->share = share;
     ctl->per = per;
     ctl->first = static_cast<int32_t>(first);
+    if (found >= 0) ctl->sq = read_seq(a, found);
   }
 }
 
@@ -550,7 +552,7 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
 }
 
 template <typename QT, int D, bool kPair>
-__device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, uint8_t* smem,
+__device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x, uint32_t (&q)[D / 64][32],
                                         uint32_t sbase, uint32_t tmem, Ctl* ctl) {
   using G = Geo<D, kPair>;
   constexpr int BN = G::BN;
@@ -568,44 +570,22 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   // ---- Q's row, as fp16 (bf16 scaled by a power of two), into TMEM
   float sl2 = a.scale_log2;
   {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + (u.sq.q0 + tok) * a.q_stride +
-                                                      static_cast<int64_t>(head) * D);
-    float up = 1.0f;
     if (!std::is_same<QT, __half>::value) {
       uint32_t top = 0;
-      if (active) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = __ldg(src + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        }
-      }
+      for (int i = 0; i < D / 2; ++i) top = max(top, max(q[i / 32][i % 32] & 0x7FFFu, (q[i / 32][i % 32] >> 16) & 0x7FFFu));
       const int e = static_cast<int>(top >> 7);
       const int f = (e == 0 || e == 255) ? 0 : min(141 - e, 100);
-      up = __int_as_float((127 + f) << 23);
+      const float up = __int_as_float((127 + f) << 23);
       sl2 *= __int_as_float((127 - f) << 23);
-    }
-#pragma unroll 1
-    for (int h = 0; h < D / 64; ++h) {   // 64 channels at a time
-      uint32_t q[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (active) v = __ldg(src + 8 * h + i);
-        q[4 * i] = v.x;
-        q[4 * i + 1] = v.y;
-        q[4 * i + 2] = v.z;
-        q[4 * i + 3] = v.w;
+      for (int i = 0; i < D / 2; ++i) {
+        const uint32_t v = q[i / 32][i % 32];
+        q[i / 32][i % 32] = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
       }
-      if (!std::is_same<QT, __half>::value) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          q[i] = pack_half2(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xFFFF0000u) * up);
-      }
-      tmem_st32(tmem + lane_off + G::T_Q + (D / 2) * x + 32 * h, q);
     }
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) tmem_st32(tmem + lane_off + G::T_Q + (D / 2) * x + 32 * h, q[h]);
 #pragma unroll 1
     for (int h = 0; h < D / 32; ++h) {   // O = 0
       uint32_t z[32];
@@ -614,7 +594,6 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
       tmem_st32(t_o + 32 * h, z);
     }
     tmem_wait_st();
-    fence_proxy_async_smem();
     tc_fence_before();
     mbar_arrive(bar(G::B_Q));
   }
@@ -754,6 +733,25 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   }
 }
 
+// The whole row of Q of a softmax thread, all loads in flight together, before anything else
+// of the CTA's start has to be waited for.
+template <typename QT, int D, bool kPair>
+__device__ __forceinline__ void load_q(const PagedArgs& a, const Unit& u, int x, uint32_t (&q)[D / 64][32]) {
+  const int row = u.r0 + (kPair ? 0 : x * BM) + (threadIdx.x & 127);
+  const int tok = row / a.group;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + (u.sq.q0 + tok) * a.q_stride +
+                                                    static_cast<int64_t>(u.kvh * a.group + row - tok * a.group) * D);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row < u.n_rows) v = __ldg(src + i);
+    q[i / 8][4 * i % 32] = v.x;
+    q[i / 8][4 * i % 32 + 1] = v.y;
+    q[i / 8][4 * i % 32 + 2] = v.z;
+    q[i / 8][4 * i % 32 + 3] = v.w;
+  }
+}
+
 template <typename QT, int D, bool kPair>
 __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel(const PagedArgs a) {
   using G = Geo<D, kPair>;
@@ -786,11 +784,6 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
     ctl->abort = 0u;
     fence_mbar_init();
   }
-  __syncthreads();
-  if (ctl->b < 0) return;   // uniform over the CTA: more blocks than work
-  const int b = ctl->b;
-  const Unit u = make_unit<D, kPair>(a, ctl, ctl->share);
-  if ((kPair || a.shares) && u.T[0] + u.T[1] == 0) return;   // uniform: an empty share
   if (warp == 13) {
     tmem_alloc(sbase + G::OFF_CTL, 512);
     tmem_relinquish();
@@ -799,9 +792,19 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  const int b = ctl->b;
+  Unit u;
+  if (b >= 0) u = make_unit<D, kPair>(a, ctl, ctl->share);
+  // uniform over the CTA: more blocks than work, or an empty share
+  if (b < 0 || ((kPair || a.shares) && u.T[0] + u.T[1] == 0)) {
+    if (warp == 13) tmem_dealloc(tmem, 512);
+    return;
+  }
   if (wg < 2) {
+    uint32_t q[D / 64][32];
+    load_q<QT, D, kPair>(a, u, wg, q);
     reg_alloc<G::REG_S>();
-    softmax<QT, D, kPair>(a, u, wg, smem, sbase, tmem, ctl);
+    softmax<QT, D, kPair>(a, u, wg, q, sbase, tmem, ctl);
   } else {
     reg_dealloc<G::REG_O>();
     if (warp == 12) {
