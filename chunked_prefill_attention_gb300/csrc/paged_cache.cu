@@ -219,9 +219,13 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
 // the block's partners of the half layout (another part of the same row, in L1
 // or L2 by then), rotates in registers, quantises, and the warp's rows go
 // through shared memory so that each row leaves as consecutive words.
+// Instruction issue bounds it, not memory.  The half layout in whole runs of eight took 36 us,
+// with a test per channel 40 (16,384 tokens, 8 x 128 bf16, all channels turned).  Resident
+// blocks an SM: five without rotation (65,536 tokens, 8 x 128 bf16: 79 us; with four 88), four
+// with it.
 // kRope: 0 none, 1 half, 2 interleaved.
 template <typename T, int kD, int kRope>
-__global__ void __launch_bounds__(kAppThreads)
+__global__ void __launch_bounds__(kAppThreads, kRope ? 4 : 5)
 append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens, int64_t k_stride,
               int64_t v_stride, const int64_t* __restrict__ slots, const RopeArgs r, const PagePool pool,
               uint32_t* status, int32_t row_tiles) {
@@ -286,24 +290,25 @@ append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens
               x[8 * i + e + 1] = y.y;
             }
           }
-        } else if (c < r.rot) {
-          // the eight channels' partners: one 16-byte aligned run when rot / 2
-          // is a multiple of 8 (then the eight are on one side), else singly
+        } else if (c < r.rot && pairs % 8 == 0) {
+          // the eight channels lie on one side and their partners are one 16-byte aligned run
+          const bool low = c < pairs;
           float y[8];
-          if (pairs % 8 == 0) {
-            load8(src + (c < pairs ? c + pairs : c - pairs), y);
-          } else {
+          load8(src + (low ? c + pairs : c - pairs), y);
+          const float2* q = turn + (low ? c : c - pairs);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              y[e] = c + e < r.rot ? Elem<T>::get(src[c + e < pairs ? c + e + pairs : c + e - pairs]) : 0.0f;
+          for (int e = 0; e < 8; ++e) {
+            // low: a cos - b sin; high: b cos + a sin, the same rounding as attn_rope's
+            x[8 * i + e] = low ? fmaf(x[8 * i + e], q[e].x, -y[e] * q[e].y) : fmaf(y[e], q[e].y, x[8 * i + e] * q[e].x);
           }
+        } else if (c < r.rot) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (c + e < r.rot) {
               const bool low = c + e < pairs;
               const float2 q = turn[low ? c + e : c + e - pairs];
-              // low: a cos - b sin; high: b cos + a sin, the same rounding as attn_rope's
-              x[8 * i + e] = low ? fmaf(x[8 * i + e], q.x, -y[e] * q.y) : fmaf(y[e], q.y, x[8 * i + e] * q.x);
+              const float y = Elem<T>::get(src[low ? c + e + pairs : c + e - pairs]);
+              x[8 * i + e] = low ? fmaf(x[8 * i + e], q.x, -y * q.y) : fmaf(y, q.y, x[8 * i + e] * q.x);
             }
           }
         }
