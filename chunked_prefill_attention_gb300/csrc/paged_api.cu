@@ -203,10 +203,12 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   Plan p{};
   if (max_q > total_q) max_q = total_q;
   p.tiles = max_q * group > kFewRows;
-  // a batch whose bounds leave no room for a short sequence is the tile kernel's
-  // alone (which then takes sequences of any length)
-  p.few = !p.tiles || (total_q - (batch - 1) * max_q) * group <= kFewRows;
   if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
+  // The tile kernel takes every sequence of a call of at most 128 rows each (one of few
+  // rows costs it no more than one of many, the other kernel's launches 8 us), and of a
+  // call whose bounds leave no room for a short one.  Single tokens beside prompts keep their
+  // own kernel: there a long cache would be one CTA's.
+  p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   const int64_t few_rows = p.tiles ? kFewRows : max_q * group;
   p.direct = q8a::paged_few_direct(batch, kv_heads, max_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, few_rows) : 0;
