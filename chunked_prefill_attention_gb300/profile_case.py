@@ -43,6 +43,15 @@ warm-up call and then --reps calls.  --burst 131072 holds 0.57 GB of Q8_0 KV.
 
   ncu --set full --clock-control none -k regex:chunk_step_kernel -s 1 -c 1 \\
       python -m chunked_prefill_attention_gb300.profile_case --burst 131072
+
+With --paged few or tiles it runs attn_paged: single tokens of 16 sequences of
+32,768 keys (32 heads on 8, 128 channels; 1.1 GB of pages), or 9,728 tokens on
+16,384 keys (8 heads, --head-dim channels, no mask), three calls.
+
+  ncu --set full --clock-control none -k regex:paged_few_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged few
+  ncu --set full --clock-control none -k regex:paged_tiles_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged tiles
 """
 
 import argparse
@@ -57,6 +66,7 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=16384)
     p.add_argument("--chunk", type=int, default=8192)
     p.add_argument("--index", type=int, default=1)
+    p.add_argument("--paged", choices=("few", "tiles"))
     p.add_argument("--reps", type=int, default=2)
     p.add_argument("--burst", type=int, default=0)
     p.add_argument("--split", type=int, default=8192)
@@ -67,6 +77,8 @@ def main(argv=None):
     _build.ensure_built()
     if a.pipelined:
         return pipelined(a)
+    if a.paged:
+        return paged(a)
     if a.burst > 0:
         return burst(a)
     if a.quantize > 0:
@@ -172,6 +184,42 @@ def burst(a):
     kv_bytes = 2 * b.heads * M * Q.ROW_BYTES
     print(f"burst: {b.queries} candidates x {b.heads} heads against {M} keys, ranges of {a.split}: "
           f"{ms:.3f} ms per call, {kv_bytes / (ms * 1e-3) / 1e9:.0f} GB/s of Q8_0 KV, status {rc}")
+
+
+def paged(a):
+    import torch
+
+    from chunked_prefill_attention_gb300 import q8attn as Q
+
+    if a.paged == "few":
+        batch, n_q, keys, heads, kv_heads, D, page = 16, 1, 32768, 32, 8, 128, 64
+    else:
+        batch, n_q, keys, heads, kv_heads, D, page = 1, 9728, 16384, 8, 8, a.head_dim, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    width = keys // page
+    slots = torch.arange(keys, device="cuda")
+    pages = [torch.empty((batch * width, kv_heads, page, Q.row_bytes(D)), dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    for b in range(batch):
+        k, v = (torch.randn((keys, kv_heads, D), generator=g, device="cuda").half() for _ in range(2))
+        Q.q8kv_append_paged(k, v, *pages, slots + b * keys)
+    table = torch.arange(batch * width, dtype=torch.int32, device="cuda").view(batch, width)
+    lens = torch.full((batch,), keys, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, batch * n_q + 1, n_q, dtype=torch.int32, device="cuda")
+    q = torch.randn((batch * n_q, heads, D), generator=g, device="cuda").half()
+    out = torch.empty_like(q)
+    ws = torch.empty(max(1, Q.paged_workspace_floats(batch, batch * n_q, heads, kv_heads, n_q, keys, D)), device="cuda")
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for i in range(3):
+        if i == 1:
+            ev[0].record()
+        Q.attn_paged(q, *pages, table, lens, cu, n_q, keys, causal=a.paged == "few", out=out, workspace=ws)
+    ev[1].record()
+    torch.cuda.synchronize()
+    us = ev[0].elapsed_time(ev[1]) / 2 * 1e3
+    kv_bytes, flops = 2 * batch * keys * kv_heads * Q.row_bytes(D), 4 * D * heads * batch * n_q * keys
+    print(f"attn_paged {a.paged}: {us:.1f} us per call, {kv_bytes / us / 1e3:.0f} GB/s of Q8_0 KV, "
+          f"{flops / us / 1e6:.0f} TFLOP/s")
 
 
 if __name__ == "__main__":
