@@ -20,7 +20,7 @@
 //           neither is the limit (key tiles of 96 keys, 256 rows: 654 -> 701 TFLOP/s).
 //   others  dequantisation, a lane per 34-byte block: nine warps at D = 64, where five
 //           were the limit (701 -> 807 TFLOP/s), five at D = 128, where nine take
-//           shared memory from the MMAs (803 -> 697).
+//           shared memory from the MMAs (803 -> 697), thirteen in pairs (below).
 //
 // D = 64: key tiles of 96 keys and three score buffers in TMEM, which the steps (A and B
 // of each key tile in turn) use one after another, so that the scores of a tile's next key
@@ -29,6 +29,9 @@
 // softmax threads, one row each): 64 keys take 32 cycles a k-step so, 48 with Q in
 // shared memory, and with B's Q there for a third buffer D = 128 reached 747 TFLOP/s
 // instead of 803.  O has no separate columns for the residuals of V.
+//
+// Pairs (calls of at most 128 rows per K/V head): both tiles hold the same rows and take the
+// key tiles in turn, so no half of the CTA idles; dequantisation is the limit then.
 //
 // Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 807 (fp16) and
 // 821 (bf16) TFLOP/s, D = 128 822 and 900, of 1,699 sustained for a plain bf16 product;
@@ -423,7 +426,7 @@ __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile,
 
 // K of key tile i + 1, then V of key tile i: V's place in the ring is free only after
 // O's update of key tile i - 2, and K must not wait behind it.  The groups go
-// round the warps from tile to tile, so five warps share twelve (sixteen) evenly.
+// round the warps from tile to tile, so any number of warps shares them evenly.
 template <int D, bool kPair, bool kExactV>
 __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w, uint8_t* smem, uint32_t sbase,
                                         Ctl* ctl) {

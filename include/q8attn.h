@@ -500,10 +500,11 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *                max_q, max_kv, D) floats; overwritten.  Calls (and captured graphs) that share one
  *                must be ordered on one stream.
  * Numerics: keys and values enter the tensor cores exactly (with bf16 output and
- * more than 64 rows per K/V head, values rounded once to fp16); scores, maxima, sums
- * and the accumulated values are fp32; each weight is rounded once to fp16, the
- * output once to its type.  Values d*q are within fp16's range.  The result does not depend on timing.  A sequence with a bad
- * page number gets an unspecified result, the others theirs.
+ * max_q * group above 16, values rounded once to fp16); scores, maxima, sums and the
+ * accumulated values are fp32; each weight is rounded once to fp16, the output once to
+ * its type.  The values d*q of a sequence's keys and values are within fp16's range, also
+ * those that a row does not see.  The result does not depend on timing.  A sequence
+ * with a bad page number gets an unspecified result, the others theirs.
  * Errors: as attn_rope; Q8A_ERR_INVALID_ARG also for a too small workspace.
  */
 int attn_paged(const void *q, int32_t dtype, int64_t q_token_stride, int64_t total_q,
