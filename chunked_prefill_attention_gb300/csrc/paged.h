@@ -78,8 +78,11 @@ struct PagedArgs {
   int32_t share_tiles;        // key tiles of a share; 0: from the lengths, on the device
   int64_t part_ml;            // tile kernel: floats of `part` before the shares' (m, l)
   int64_t ctas;               // tile kernel: its grid
+  int32_t wide;               // tile kernel: whose rows start 32-byte aligned (kWide...)
   uint64_t timeout_ns;
 };
+
+constexpr int32_t kWideQ = 1, kWideOut = 2, kWidePart = 4;
 
 // Few query rows per K/V head: one launch over key tiles plus the merge.
 // `rows`: the largest tokens * group of the sequences it takes (a bound).

@@ -302,6 +302,9 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
     b.ctas = plan.t.ctas;
     b.part = workspace + plan.few_floats;
     b.part_ml = plan.t.part_ml;
+    auto even = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
+    b.wide = (even(q) && q_token_stride % 16 == 0 ? q8a::kWideQ : 0) | (even(out) ? q8a::kWideOut : 0) |
+             (even(b.part) ? q8a::kWidePart : 0);
     e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t, st);
   }
   if (plan.few && e == cudaSuccess) {

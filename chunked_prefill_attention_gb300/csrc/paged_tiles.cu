@@ -33,8 +33,8 @@
 // Pairs (calls of at most 128 rows per K/V head): both tiles hold the same rows and take the
 // key tiles in turn, so no half of the CTA idles; dequantisation is the limit then.
 //
-// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 807 (fp16) and
-// 821 (bf16) TFLOP/s, D = 128 822 and 900, of 1,699 sustained for a plain bf16 product;
+// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 828 (fp16) and
+// 838 (bf16) TFLOP/s, D = 128 827 and 924, of 1,699 sustained for a plain bf16 product;
 // K's residuals make S cost twice its nominal work, V's (fp16) O.  At D = 64 softmax
 // (1,290 cycles a step), dequantisation and MMA issue are now within 20 % of one another.
 //
@@ -164,6 +164,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "%15, %16};" ::"r"(taddr),
       Q8A_W8(r, 0), Q8A_W8(r, 8)
       : "memory");
+}
+
+// Eight words of a thread's own row of Q, O or a partial state.  32 rows are 32 lines of L1
+// each time, so 256 bits at once where the rows start 32-byte aligned: a CTA of one key tile
+// (64 channels) 7.84 -> 7.48 us, of two (128 channels) 12.1 -> 10.6.
+__device__ __forceinline__ void load_row8(const uint4* p, bool wide, uint32_t* v) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+  } else {
+    const uint4 x = __ldg(p), y = __ldg(p + 1);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  }
+}
+__device__ __forceinline__ void store_row8(uint4* p, bool wide, const uint32_t* v) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), Q8A_W8(v, 0) : "memory");
+  } else {
+    p[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    p[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // The work of this CTA: rows r0 .. r0 + 255 of a (sequence, K/V head), key tiles
@@ -695,7 +717,8 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
       float2* ml = reinterpret_cast<float2*>(a.part + a.part_ml);
       ml[at] = make_float2(m_run, l_run);
     }
-    float4* dst = reinterpret_cast<float4*>(a.part + at * D);
+    uint4* dst = reinterpret_cast<uint4*>(a.part + at * D);
+    const bool wide = a.wide & kWidePart;
 #pragma unroll 1
     for (int h = 0; h < D / 32; ++h) {
       uint32_t o[32];
@@ -703,14 +726,13 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
       tmem_wait_ld(o);
       if (active)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[8 * h + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        for (int i = 0; i < 4; ++i) store_row8(dst + 8 * h + 2 * i, wide, o + 8 * i);
     }
     return;
   }
   const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
   uint4* dst = reinterpret_cast<uint4*>(static_cast<QT*>(a.out) + ((u.sq.q0 + tok) * a.heads + head) * D);
+  const bool wide = a.wide & kWideOut;
 #pragma unroll 1
   for (int h = 0; h < D / 32; ++h) {
     uint32_t o[32];
@@ -718,11 +740,11 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
     tmem_wait_ld(o);
     if (active) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t y[4];
+      for (int i = 0; i < 2; ++i) {
+        uint32_t y[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float y0 = __uint_as_float(o[8 * i + 2 * k]) * inv, y1 = __uint_as_float(o[8 * i + 2 * k + 1]) * inv;
+        for (int k = 0; k < 8; ++k) {
+          const float y0 = __uint_as_float(o[16 * i + 2 * k]) * inv, y1 = __uint_as_float(o[16 * i + 2 * k + 1]) * inv;
           if (std::is_same<QT, __half>::value) {
             y[k] = pack_half2(y0, y1);
           } else {
@@ -730,7 +752,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
             y[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
         }
-        dst[4 * h + i] = make_uint4(y[0], y[1], y[2], y[3]);
+        store_row8(dst + 4 * h + 2 * i, wide, y);
       }
     }
   }
@@ -744,14 +766,13 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, const Unit& u, int x,
   const int tok = row / a.group;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const QT*>(a.q) + (u.sq.q0 + tok) * a.q_stride +
                                                     static_cast<int64_t>(u.kvh * a.group + row - tok * a.group) * D);
+  const bool wide = a.wide & kWideQ;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row < u.n_rows) v = __ldg(src + i);
-    q[i / 8][4 * i % 32] = v.x;
-    q[i / 8][4 * i % 32 + 1] = v.y;
-    q[i / 8][4 * i % 32 + 2] = v.z;
-    q[i / 8][4 * i % 32 + 3] = v.w;
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t* v = &q[i / 4][8 * i % 32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0u;
+    if (row < u.n_rows) load_row8(src + 2 * i, wide, v);
   }
 }
 

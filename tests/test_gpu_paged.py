@@ -673,6 +673,29 @@ def test_nothing_is_written_beside_the_buffers(Q, q_lens, kv_lens, D, page):
     assert (pages.transpose(1, 2)[~used] == 0x5A).all() and (pages_v.transpose(1, 2)[~used] == 0x5A).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1], [700]), ([1], [40000]), ([13], [3000]), ([40, 17], [700, 9000]),
+                                            ([300], [4000]), ([600, 700], [600, 700])])
+def test_rows_aligned_to_16_bytes_only(Q, q_lens, kv_lens, dtype, D):
+    """q, out and the workspace 16 bytes past 32-byte alignment, q's rows an odd number of 16 bytes
+    apart: the same bits."""
+    x = Batch(q_lens, kv_lens, 4, 2, D, 32, dtype, seed=51)
+    want = Q.attn_paged(*x.args())
+    x.check(want)
+    T, H = x.q.shape[:2]
+    stride = H * D + 8
+    raw = torch.empty(T * stride + 8, dtype=dtype, device="cuda")
+    q = raw[8:].as_strided((T, H, D), (stride, D, 1))
+    q.copy_(x.q)
+    out = torch.full((T * H * D + 8,), float("nan"), dtype=dtype, device="cuda")[8:].view(T, H, D)
+    n = Q.paged_workspace_floats(len(q_lens), T, H, 2, max(q_lens), max(kv_lens), D)
+    ws = torch.full((n + 4,), float("nan"), device="cuda")[4:]
+    assert all(t.data_ptr() % 32 == 16 for t in ([q, out, ws] if n else [q, out]))
+    Q.attn_paged(q, *x.args()[1:], out=out, workspace=ws if n else None)
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_batches(Q, seed):
     rng = np.random.default_rng(seed)
