@@ -18,9 +18,13 @@
 //   13, 14  issue the MMAs of S and of O.  One warp for both spends about 1,340 cycles a
 //           step at D = 64 on its waits and issues, against 768 of tensor work; apart,
 //           neither is the limit (key tiles of 96 keys, 256 rows: 654 -> 701 TFLOP/s).
-//   others  dequantisation, a lane per 34-byte block: nine warps at D = 64, where five
-//           were the limit (701 -> 807 TFLOP/s), five at D = 128, where nine take
-//           shared memory from the MMAs (803 -> 697), thirteen in pairs (below).
+//   others  dequantisation, a lane per 34-byte block, some warps for K and some for V: a warp's
+//           time per key tile is one chain of waits, loads and stores, and with both tensors
+//           in every warp that chain was the limit (pairs 290 -> 266 us, whole CTAs up to 6 %).
+//           Five and four warps at D = 64 (four and four 384 us, five and three 390, these
+//           380); two and two at D = 128, where more of them take shared memory and issue
+//           slots from the rest (three and three 705 us, these 638, bf16); in pairs seven
+//           and six.
 //
 // D = 64: key tiles of 96 keys and three score buffers in TMEM, which the steps (A and B
 // of each key tile in turn) use one after another, so that the scores of a tile's next key
@@ -33,10 +37,11 @@
 // Pairs (calls of at most 128 rows per K/V head): both tiles hold the same rows and take the
 // key tiles in turn, so no half of the CTA idles; dequantisation is the limit then.
 //
-// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 828 (fp16) and
-// 838 (bf16) TFLOP/s, D = 128 827 and 924, of 1,699 sustained for a plain bf16 product;
-// K's residuals make S cost twice its nominal work, V's (fp16) O.  At D = 64 softmax
-// (1,290 cycles a step), dequantisation and MMA issue are now within 20 % of one another.
+// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 858 (fp16) and
+// 901 (bf16) TFLOP/s, D = 128 851 and 1,023, of 1,699 sustained for a plain bf16 product;
+// K's residuals make S cost twice its nominal work, V's (fp16) O.  What the others wait for
+// most is dequantisation (without it 319 us of 374 at D = 64, bf16; half of the products less
+// gives 368, no exponentials 357).
 //
 // Every wait is bounded, as in chunk_step.cu.
 
@@ -73,7 +78,8 @@ struct Geo {
   static constexpr int NR = D == 64 || kPair ? 4 : 3;
   static constexpr int NS = D == 64 ? 3 : 2;            // score buffers
   static constexpr int kThreads = kPair ? 768 : (D == 64 ? 640 : 512);
-  static constexpr int kDq = kThreads / 32 - 11;        // dequantising warps
+  static constexpr int kKDq = kPair ? 7 : D == 64 ? 5 : 2, kVDq = kPair ? 6 : D == 64 ? 4 : 2;   // K's, V's dequantising warps
+  static_assert(kKDq + kVDq + 11 <= kThreads / 32, "warps");
   static constexpr int ROWS = kPair ? BM : 2 * BM;      // query rows of a CTA
   // shared memory
   static constexpr int OFF_K = 0;                       // [ND][hi | lo]
@@ -396,9 +402,10 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
 }
 
 // One block of one row (nine-word window w; even blocks start word-aligned, odd ones
-// two bytes into the first word) -> 16-byte chunks of the swizzled row.
-template <bool kLo>
-__device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], bool odd, uint8_t* hi_row, uint8_t* lo_row,
+// two bytes into the first word) -> 16-byte chunks of the swizzled row.  `odd` is the same for
+// a warp: as a branch 672 us, as selections of words 710 (D = 128, bf16).
+template <bool kLo, bool odd>
+__device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], uint8_t* hi_row, uint8_t* lo_row,
                                               int chunk0, int sw) {
   const __half2 d2 = __half2half2(__ushort_as_half(static_cast<unsigned short>(odd ? w[0] >> 16 : w[0] & 0xFFFFu)));
 #pragma unroll
@@ -434,7 +441,10 @@ __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile,
     uint32_t c[9];
 #pragma unroll
     for (int k = 0; k < 9; ++k) c[k] = p[k];
-    dequant_block<kLo>(c, odd, hi, lo, chunk0, row & 7);
+    if (odd)
+      dequant_block<kLo, true>(c, hi, lo, chunk0, row & 7);
+    else
+      dequant_block<kLo, false>(c, hi, lo, chunk0, row & 7);
   } else {   // keys that the sequence does not have: whatever the page holds is not read
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -446,47 +456,33 @@ __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile,
   }
 }
 
-// K of key tile i + 1, then V of key tile i: V's place in the ring is free only after
-// O's update of key tile i - 2, and K must not wait behind it.  The groups go
-// round the warps from tile to tile, so any number of warps shares them evenly.
-template <int D, bool kPair, bool kExactV>
+// K's or V's tiles, by warps w of G::kKDq or G::kVDq.  The groups go round the warps from tile to
+// tile, so any number of warps shares them evenly.
+template <int D, bool kPair, bool kV, bool kLo>
 __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w, uint8_t* smem, uint32_t sbase,
                                         Ctl* ctl) {
   using G = Geo<D, kPair>;
-  constexpr int kGroups = G::BN / 32 * (D / 32);   // groups of a tensor's tile: 6 or 8
+  constexpr int kGroups = G::BN / 32 * (D / 32);   // groups of a tile: 6 or 8
+  constexpr int kWarps = kV ? G::kVDq : G::kKDq;
   const uint64_t budget = 2 * a.timeout_ns;
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
   const int T = key_tiles<kPair>(u);
-  int mine = w;   // this warp's next group of the iteration: K's, then V's behind them
-  for (int i = -1; i < T; ++i) {
-    const int k = i + 1;
-    if (k < T) {
-      const int sd = k % ND;
-      if (!wait_bar(bar(G::B_RAWFULL + k % G::NR), (k / G::NR) & 1, ctl, budget, a.status)) return;
-      if (!wait_bar(bar(G::B_KEMPTY + sd), ((k / ND) & 1) ^ 1, ctl, budget, a.status)) return;
-      const int n_valid = u.sq.kv - (u.t0 + k) * G::BN;
+  int mine = w;   // this warp's next group of the tile
 #pragma unroll 1
-      for (; mine < kGroups; mine += G::kDq)
-        dequant_group<D, kPair, true>(smem + G::OFF_RAW + k % G::NR * 2 * G::RAWB, smem + G::OFF_K + sd * 2 * G::TILE, mine,
-                               n_valid, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(bar(G::B_KFULL + sd));
-      mine -= kGroups;
-    }
-    if (i >= 0) {
-      const int sd = i % ND;
-      if (!wait_bar(bar(G::B_VEMPTY + sd), ((i / ND) & 1) ^ 1, ctl, budget, a.status)) return;
-      const int n_valid = u.sq.kv - (u.t0 + i) * G::BN;
+  for (int t = 0; t < T; ++t) {
+    const int s = t % G::NR, sd = t % ND;
+    if (!wait_bar(bar(G::B_RAWFULL + s), (t / G::NR) & 1, ctl, budget, a.status)) return;
+    if (!wait_bar(bar((kV ? G::B_VEMPTY : G::B_KEMPTY) + sd), ((t / ND) & 1) ^ 1, ctl, budget, a.status)) return;
+    const int n_valid = u.sq.kv - (u.t0 + t) * G::BN;
 #pragma unroll 1
-      for (; mine < kGroups; mine += G::kDq)
-        dequant_group<D, kPair, kExactV>(smem + G::OFF_RAW + i % G::NR * 2 * G::RAWB + G::RAWB,
-                                  smem + G::OFF_V + sd * 2 * G::TILE, mine, n_valid, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(bar(G::B_VFULL + sd));
-      mbar_arrive(bar(G::B_RAWEMPTY + i % G::NR));
-      mine -= kGroups;
-    }
+    for (; mine < kGroups; mine += kWarps)
+      dequant_group<D, kPair, kLo>(smem + G::OFF_RAW + (2 * s + kV) * G::RAWB,
+                                   smem + (kV ? G::OFF_V : G::OFF_K) + sd * 2 * G::TILE, mine, n_valid, lane);
+    fence_proxy_async_smem();
+    mbar_arrive(bar((kV ? G::B_VFULL : G::B_KFULL) + sd));
+    mbar_arrive(bar(G::B_RAWEMPTY + s));
+    mine -= kGroups;
   }
 }
 
@@ -566,7 +562,7 @@ __device__ __forceinline__ void value_mma(const PagedArgs& a, const Unit& u, uin
         for (int k = 0; k < G::BN / 16; ++k)
           mma_ts(o, p + 8 * k, vd + static_cast<uint64_t>((part * G::TILE + k * 2048) >> 4), kIdesc, 1u);
       mma_commit(bar(G::B_PV + buf));
-      if ((kPair ? n >> 1 : t) == u.T[x] - 1) mma_commit(bar(G::B_ODONE + x));
+      if ((kPair ? n >> 1 : t) == (x ? u.T[1] : u.T[0]) - 1) mma_commit(bar(G::B_ODONE + x));
       if (last_reader<kPair>(u, t, x)) mma_commit(bar(G::B_VEMPTY + sd));
     }
     __syncwarp();
@@ -590,7 +586,7 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
   const int tok = row / a.group;
   const int head = u.kvh * a.group + row - tok * a.group;
   const uint32_t t_o = tmem + lane_off + G::T_O + D * x;
-  const int T = u.T[x];
+  const int T = x ? u.T[1] : u.T[0];
 
   // ---- Q's row, as fp16 (bf16 scaled by a power of two), into TMEM
   float sl2 = a.scale_log2;
@@ -799,9 +795,9 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
     for (int i = 0; i < G::NBAR; ++i) {
       uint32_t count = 1;
       if (i == G::B_Q) count = 256;                                      // softmax threads
-      if (i >= G::B_RAWEMPTY && i < G::B_RAWEMPTY + G::NR) count = 32 * G::kDq;   // dequantising threads
-      if (i >= G::B_KFULL && i < G::B_KFULL + ND) count = 32 * G::kDq;
-      if (i >= G::B_VFULL && i < G::B_VFULL + ND) count = 32 * G::kDq;
+      if (i >= G::B_RAWEMPTY && i < G::B_RAWEMPTY + G::NR) count = 32 * (G::kKDq + G::kVDq);   // dequantising threads
+      if (i >= G::B_KFULL && i < G::B_KFULL + ND) count = 32 * G::kKDq;
+      if (i >= G::B_VFULL && i < G::B_VFULL + ND) count = 32 * G::kVDq;
       if (i >= G::B_PFULL && i < G::B_PFULL + G::NS) count = 128;           // softmax threads of a tile
       mbar_init(sbase + G::OFF_BAR + 8u * i, count);
     }
@@ -838,7 +834,11 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
     } else if (warp == 14) {
       value_mma<D, kPair, kExactV>(a, u, sbase, tmem, ctl);
     } else {
-      dequant<D, kPair, kExactV>(a, u, warp < 12 ? warp - 8 : warp - 11, smem, sbase, ctl);
+      const int w = warp < 12 ? warp - 8 : warp - 11;
+      if (w < G::kKDq)
+        dequant<D, kPair, false, true>(a, u, w, smem, sbase, ctl);
+      else if (w < G::kKDq + G::kVDq)
+        dequant<D, kPair, true, kExactV>(a, u, w - G::kKDq, smem, sbase, ctl);
     }
   }
   tc_fence_before();
