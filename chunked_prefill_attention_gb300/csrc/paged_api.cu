@@ -5,7 +5,9 @@
 // All kernels of these calls are launched with programmatic stream serialization: a
 // step of a server is a chain of short kernels, and each may be scheduled while its
 // predecessor's last CTAs run.  Each waits for the predecessor's completion before it
-// touches memory (pdl_wait), so nothing else changes.
+// touches memory (pdl_wait), so nothing else changes.  What a predecessor may have written
+// (queries, pages, slots, lengths) is never read through the non-coherent path, whose data
+// must not change while the kernel is resident, the wait included.
 
 #include <cmath>
 #include <cstdarg>

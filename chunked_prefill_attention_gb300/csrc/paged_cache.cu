@@ -230,9 +230,9 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
 // kRope: 0 none, 1 half, 2 interleaved.
 template <typename T, int kD, int kRope>
 __global__ void __launch_bounds__(kAppThreads, kRope ? 4 : 5)
-append_kernel(const T* __restrict__ k, const T* __restrict__ v, int64_t n_tokens, int64_t k_stride,
-              int64_t v_stride, const int64_t* __restrict__ slots, const RopeArgs r, const PagePool pool,
-              uint32_t* status, int32_t row_tiles) {
+append_kernel(const T* k, const T* v, int64_t n_tokens, int64_t k_stride,
+              int64_t v_stride, const int64_t* slots, const RopeArgs r, const PagePool pool, uint32_t* status,
+              int32_t row_tiles) {
   constexpr int kBlk = kD / 32;
   constexpr int kRow = kBlk * 34;
   constexpr int kTok = 32 / kBlk;
@@ -394,8 +394,7 @@ constexpr int kReadRows = 4;   // rows of a thread, in flight together
 // from one or two 32-byte sectors that its neighbours read as well.
 template <typename T, int kD>
 __global__ void __launch_bounds__(kReadThreads)
-read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t* __restrict__ slots,
-            const PagePool pool, uint32_t* status) {
+read_kernel(T* k, T* v, int64_t n_rows, const int64_t* slots, const PagePool pool, uint32_t* status) {
   constexpr int kRow = kD / 32 * 34;
   constexpr int kPer = kD / 8;                     // threads of a row
   constexpr int kPass = kReadThreads / kPer;       // rows of a block and pass
@@ -421,7 +420,7 @@ read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t*
   uint32_t head[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
-    slot[u] = row0 + u * kPass < n_rows ? __ldg(slots + t) : -1;
+    slot[u] = row0 + u * kPass < n_rows ? slots[t] : -1;
     head[u] = h;
     t += dt;
     h += dh;
@@ -447,10 +446,10 @@ read_kernel(T* __restrict__ k, T* __restrict__ v, int64_t n_rows, const int64_t*
   for (int u = 0; u < kU; ++u) {
     if (at[u]) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(at[u] + (code0 & ~3));
-      w[u][0] = __ldg(p);
-      w[u][1] = __ldg(p + 1);
-      w[u][2] = (bb & 1) ? 0u : __ldg(p + 2);
-      d[u] = __ldg(reinterpret_cast<const unsigned short*>(at[u] + 34 * bb));
+      w[u][0] = p[0];
+      w[u][1] = p[1];
+      w[u][2] = (bb & 1) ? 0u : p[2];
+      d[u] = *reinterpret_cast<const unsigned short*>(at[u] + 34 * bb);
     }
   }
 #pragma unroll

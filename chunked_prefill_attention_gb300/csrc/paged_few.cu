@@ -369,7 +369,7 @@ paged_few_kernel(const PagedArgs a) {
                           : st == 1 ? (t == 3 && h == 1 ? 0 : 4 * t + 18 + 2 * h)
                                     : 32 + 16 * (st - 2) + 4 * t + 2 * h;
             raw[p][st][h] =
-                row < n_rows ? __ldg(reinterpret_cast<const uint32_t*>(qp + 64 * p + c)) : 0u;
+                row < n_rows ? *reinterpret_cast<const uint32_t*>(qp + 64 * p + c) : 0u;
           }
       if (sizeof(QT) == 2 && !std::is_same<QT, __half>::value) {
         uint32_t top = 0;   // largest magnitude, as bits

@@ -177,11 +177,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 // (64 channels) 7.84 -> 7.48 us, of two (128 channels) 12.1 -> 10.6.
 __device__ __forceinline__ void load_row8(const uint4* p, bool wide, uint32_t* v) {
   if (wide) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(p));
   } else {
-    const uint4 x = __ldg(p), y = __ldg(p + 1);
+    const uint4 x = p[0], y = p[1];
     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
   }
 }

@@ -613,6 +613,37 @@ def test_captured_prompts_replay(Q, q_lens, kv_lens):
     assert (outs[0][x.n_rows - drop:] == 5.0).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 40, 700])
+def test_calls_in_a_row_see_each_others_writes(Q, tokens):
+    """The same rows are written, read back, attended to and written again without a wait of the host between:
+    each call sees what the call before it wrote."""
+    H, D, page, steps = 4, 64, 16, 60
+    n_pages = -(-tokens // page)
+    shape = (n_pages, H, page, 68)
+    kp, vp = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    slots = torch.arange(tokens, device="cuda")
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([tokens], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    q = torch.ones((1, H, D), dtype=F16, device="cuda")
+    vals = [torch.full((tokens, H, D), 127.0 * 2 ** -6 * (i + 1), dtype=F32, device="cuda") for i in range(steps)]
+    outs = [tuple(torch.empty((tokens, H, D), dtype=F32, device="cuda") for _ in range(2)) for _ in range(steps)]
+    att = [torch.empty_like(q) for _ in range(steps)]
+    ws = torch.empty(max(Q.paged_workspace_floats(1, 1, H, H, 1, tokens, D), 4), device="cuda")
+    torch.cuda.synchronize()
+    for i in range(steps):
+        Q.q8kv_append_paged(vals[i], vals[i], kp, vp, slots)
+        Q.q8kv_read_paged(kp, vp, slots, F32, out=outs[i])
+        Q.attn_paged(q, kp, vp, table, lens, cu, 1, tokens, out=att[i], workspace=ws)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        # amax / 127 = 2^-6 (i + 1) exactly, so every code is 127 and every value exact; equal values average to
+        # themselves but for the weights' rounding (2^-11 each way) and the output's
+        assert torch.equal(outs[i][0], vals[i]) and torch.equal(outs[i][1], vals[i]), i
+        x = float(vals[i][0, 0, 0])
+        assert (att[i].double() - x).abs().max() <= 3 * 2.0 ** -11 * x, i
+
+
 def test_two_streams_at_once(Q):
     """Independent calls on two streams, each with its own workspace."""
     a = Batch([1, 1], [40000, 3000], 8, 2, 128, 64, BF16, seed=31)
