@@ -188,10 +188,10 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
 namespace {
 
 // Sequences of at most so many rows (tokens * group) go to the few-row kernel.  Both
-// kernels at 16 rows, 16 sequences of 32,768 keys, 8 K/V heads: 142 us against 328 (64
-// channels), 334 against 552 (128); a few-row kernel made for 32 rows took 310 and 430
-// there, but 50 and 61 against 36 and 50 for 2,048 keys and 587 and 820 against 329 and
-// 554 at 64 rows (in two passes), so from 17 rows on the tile kernel takes them.
+// kernels at 16 rows, 16 sequences of 8 K/V heads: 141 us against 253 for 32,768 keys of 64
+// channels, 275 against 420 of 128; for 2,048 keys 28 against 30 and 50 against 41.  At 32 rows
+// a few-row kernel made for them took 310 and 430 (50 and 61 for 2,048 keys), the tile
+// kernel 254 and 422 (30 and 42), so from 17 rows on the tile kernel takes them.
 constexpr int64_t kFewRows = 16;
 
 // The launches of a call, from its bounds alone.

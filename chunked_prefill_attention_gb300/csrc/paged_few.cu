@@ -900,8 +900,8 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
 
 template <typename QT, int D>
 cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStream_t stream) {
-  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
-  // of 108 at 64 channels, 334 instead of 194 at 128
+  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 141 us instead
+  // of 107 at 64 channels, 275 instead of 192 at 128
   if (direct) {
     const int ctas = a.batch * a.kv_heads;
     return rows <= 8 ? launch_few<QT, D, 1, true>(a, ctas, stream) : launch_few<QT, D, 2, true>(a, ctas, stream);

@@ -73,9 +73,9 @@ struct Geo {
   static constexpr int ATOM = BN * 128;                 // bytes of one such column
   static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
   // Raw ring.  In pairs a key tile serves 128 rows, so the copies' latency counts more: at
-  // D = 64 (16 sequences of 32,768 keys, 128 rows) 3 stages 357 us, 4 333, 6 and more the
-  // same; at D = 128 3 stages 566, 4 551.
-  static constexpr int NR = D == 64 || kPair ? 4 : 3;
+  // D = 64 (16 sequences of 32,768 keys, 8 K/V heads, 32 rows) 3 stages 278 us, 4 259, 6 254;
+  // at D = 128 3 stages 446, 4 422.  Otherwise 6 and 4 of them change nothing.
+  static constexpr int NR = D == 64 ? (kPair ? 6 : 4) : (kPair ? 4 : 3);
   static constexpr int NS = D == 64 ? 3 : 2;            // score buffers
   static constexpr int kThreads = kPair ? 768 : (D == 64 ? 640 : 512);
   static constexpr int kKDq = kPair ? 7 : D == 64 ? 5 : 2, kVDq = kPair ? 6 : D == 64 ? 4 : 2;   // K's, V's dequantising warps
@@ -939,8 +939,8 @@ TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, 
   // themselves, on the device, or for many sequences by the bounds.  Up to 76 pairs fill
   // one wave of SMs with at least two shares each; 77 to 101 two waves with three; from there
   // on only lengths that differ give anything to share.  4 sequences of 8,192 to 32,768
-  // keys, 64 rows, 8 K/V heads: 95 us with nine shares each, 64 so (64 channels), 152
-  // and 97 (128 channels).
+  // keys, 64 rows, 8 K/V heads: 75 us by the bounds, 54 by the lengths (64 channels), 117
+  // and 78 (128 channels).
   const int64_t bn = head_dim == 64 ? Geo<64, false>::BN : Geo<128, false>::BN;
   const int64_t tiles = (max_kv + bn - 1) / bn;
   p.shares = tiles >= 8 && (p.slots <= kSms * 2 / 3 || (batch > 1 && p.slots <= kSms));
