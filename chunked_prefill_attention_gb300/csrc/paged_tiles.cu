@@ -40,8 +40,8 @@
 // Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 858 (fp16) and
 // 901 (bf16) TFLOP/s, D = 128 851 and 1,023, of 1,699 sustained for a plain bf16 product;
 // K's residuals make S cost twice its nominal work, V's (fp16) O.  What the others wait for
-// most is dequantisation (without it 319 us of 374 at D = 64, bf16; half of the products less
-// gives 368, no exponentials 357).
+// most is dequantisation (D = 64, bf16, 362 us: without it 311, without exponentials 347, with
+// half of S's products and a sixth of O's 359).
 //
 // Every wait is bounded, as in chunk_step.cu.
 
