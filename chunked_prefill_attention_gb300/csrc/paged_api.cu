@@ -198,6 +198,8 @@ constexpr int64_t kFewRows = 16;
 struct Plan {
   bool few, direct, tiles;
   q8a::TilesPlan t;
+  int64_t few_rows;   // rows a K/V head of the few-row kernel's sequences, at most: it sizes its tiles
+                      // and their partial states, so workspace and launch both take it from here
   int64_t few_floats, floats;
 };
 Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, int32_t kv_heads, int64_t max_kv,
@@ -211,9 +213,9 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // call whose bounds leave no room for a short one.  Single tokens beside prompts keep their
   // own kernel: there a long cache would be one CTA's.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
-  const int64_t few_rows = p.tiles ? kFewRows : max_q * group;
+  p.few_rows = p.tiles ? kFewRows : max_q * group;
   p.direct = q8a::paged_few_direct(batch, kv_heads, max_kv, head_dim);
-  p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, few_rows) : 0;
+  p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
 }
@@ -311,7 +313,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   }
   if (plan.few && e == cudaSuccess) {
     a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;
-    e = q8a::launch_paged_few(a, dtype, head_dim, plan.tiles ? kFewRows : max_q * a.group, plan.direct, st);
+    e = q8a::launch_paged_few(a, dtype, head_dim, plan.few_rows, plan.direct, st);
   }
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
 }

@@ -1,0 +1,45 @@
+// Stands in for the launches of attn_paged when it is preloaded before the library: it
+// writes down what the C-ABI layer asks for.  No CUDA call is made.
+#include <cstdint>
+
+#include "../chunked_prefill_attention_gb300/csrc/internal.h"
+#include "../chunked_prefill_attention_gb300/csrc/paged.h"
+
+namespace {
+struct Record {
+  int64_t few_calls, few_rows, few_direct, few_limit;
+  int64_t tiles_calls, tiles_floats, tiles_part;   // part: floats before the tile kernel's workspace
+};
+Record g_rec;
+const float* g_part;
+uint32_t g_words[64];
+}  // namespace
+
+namespace q8a {
+uint32_t* host_status_word() { return g_words; }
+cudaError_t launch_paged_few(const PagedArgs& a, int32_t, int32_t, int64_t rows, bool direct, cudaStream_t) {
+  g_rec.few_calls++;
+  g_rec.few_rows = rows;
+  g_rec.few_direct = direct;
+  g_rec.few_limit = a.row_limit;
+  return cudaSuccess;
+}
+cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t, int32_t, const TilesPlan& plan, cudaStream_t) {
+  g_rec.tiles_calls++;
+  g_rec.tiles_floats = plan.floats;
+  g_rec.tiles_part = a.part - g_part;
+  return cudaSuccess;
+}
+}  // namespace q8a
+
+extern "C" {
+void record_start(const void* workspace) {
+  g_rec = Record{};
+  g_part = static_cast<const float*>(workspace);
+}
+void record_take(int64_t* out) {
+  const int64_t v[7] = {g_rec.few_calls, g_rec.few_rows, g_rec.few_direct, g_rec.few_limit,
+                        g_rec.tiles_calls, g_rec.tiles_floats, g_rec.tiles_part};
+  for (int i = 0; i < 7; ++i) out[i] = v[i];
+}
+}
