@@ -49,6 +49,9 @@ cudaError_t launch_append(const void* k, const void* v, int32_t dtype, int64_t n
 cudaError_t launch_read(void* k, void* v, int32_t dtype, int64_t n_tokens, int32_t head_dim,
                         const int64_t* slots, const PagePool& pool, uint32_t* status, cudaStream_t stream);
 
+// Most keys of a sequence: lengths are int32, and a tile's end must not pass 2^31.
+constexpr int64_t kMaxKeys = 0x7FFF0000;
+
 // Arguments of the attention over pages.
 struct PagedArgs {
   const void* q;              // [total_q][heads][D], token stride q_stride elements

@@ -206,6 +206,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
                 int32_t head_dim) {
   Plan p{};
   if (max_q > total_q) max_q = total_q;
+  if (max_kv > q8a::kMaxKeys) max_kv = q8a::kMaxKeys;
   p.tiles = max_q * group > kFewRows;
   if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
   // The tile kernel takes every sequence of a call of at most 128 rows each (one of few

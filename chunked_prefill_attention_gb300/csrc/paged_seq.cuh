@@ -16,7 +16,7 @@ struct Seq {
 __device__ __forceinline__ Seq read_seq(const PagedArgs& a, int b) {
   Seq s;
   int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-  const int64_t kv = a.kv_lens[b], most = i64min(a.table_stride << a.page_shift, 0x7FFF0000);
+  const int64_t kv = a.kv_lens[b], most = i64min(a.table_stride << a.page_shift, kMaxKeys);
   const bool wrong = q0 < 0 || q1 < q0 || q1 > a.total_q || kv < 0 || kv > most;
   if (wrong) *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
   q0 = i64max(0, i64min(q0, a.total_q));

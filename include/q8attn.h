@@ -487,8 +487,8 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *                stride a multiple of 8.
  *   block_table  int32 [batch][table_stride] on the device; only the pages that
  *                kv_lens reaches are read.
- *   kv_lens      int32 [batch] on the device, at most table_stride * page_tokens;
- *                0 is allowed.
+ *   kv_lens      int32 [batch] on the device, at most table_stride * page_tokens and
+ *                2^31 - 65536; 0 is allowed.
  *   cu_q         int32 [batch + 1] on the device: sequence b's rows are
  *                cu_q[b] .. cu_q[b + 1] - 1 of q (none is allowed); not decreasing,
  *                at most total_q.  Rows from cu_q[batch] on are left as they were.

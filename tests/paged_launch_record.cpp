@@ -9,6 +9,7 @@ namespace {
 struct Record {
   int64_t few_calls, few_rows, few_direct, few_limit;
   int64_t tiles_calls, tiles_floats, tiles_part;   // part: floats before the tile kernel's workspace
+  int64_t shares, share_tiles;
 };
 Record g_rec;
 const float* g_part;
@@ -28,6 +29,8 @@ cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t, int32_t, const Tiles
   g_rec.tiles_calls++;
   g_rec.tiles_floats = plan.floats;
   g_rec.tiles_part = a.part - g_part;
+  g_rec.shares = plan.shares;
+  g_rec.share_tiles = plan.share_tiles;
   return cudaSuccess;
 }
 }  // namespace q8a
@@ -38,8 +41,8 @@ void record_start(const void* workspace) {
   g_part = static_cast<const float*>(workspace);
 }
 void record_take(int64_t* out) {
-  const int64_t v[7] = {g_rec.few_calls, g_rec.few_rows, g_rec.few_direct, g_rec.few_limit,
-                        g_rec.tiles_calls, g_rec.tiles_floats, g_rec.tiles_part};
-  for (int i = 0; i < 7; ++i) out[i] = v[i];
+  const int64_t v[9] = {g_rec.few_calls, g_rec.few_rows, g_rec.few_direct, g_rec.few_limit,
+                        g_rec.tiles_calls, g_rec.tiles_floats, g_rec.tiles_part, g_rec.shares, g_rec.share_tiles};
+  for (int i = 0; i < 9; ++i) out[i] = v[i];
 }
 }

@@ -12,12 +12,12 @@ import pytest
 
 from tests.conftest import ROOT
 
-FIELDS = ("few_calls", "few_rows", "few_direct", "few_limit", "tiles_calls", "tiles_floats", "tiles_part")
+FIELDS = ("few_calls", "few_rows", "few_direct", "few_limit", "tiles_calls", "tiles_floats", "tiles_part", "shares", "share_tiles")
 WORKSPACE = 0x7000000000   # never dereferenced
 
 
 def child(cases):
-    """Runs in the child: the launches of each case (total_q, heads, kv_heads, max_q, max_kv, D, batch)."""
+    """Runs in the child: the launches of each case (total_q, heads, kv_heads, max_q, max_kv, D, batch, page)."""
     from chunked_prefill_attention_gb300 import q8attn as Q
     lib, rec = Q.load(), ctypes.CDLL(None)
     P = ctypes.c_void_p
@@ -25,12 +25,12 @@ def child(cases):
     few_floats.restype, few_floats.argtypes = ctypes.c_int64, [ctypes.c_int32, ctypes.c_int64]
     rec.record_start.argtypes, rec.record_take.argtypes = [P], [P]
     out = []
-    for total, heads, kv, max_q, max_kv, D, batch in cases:
+    for total, heads, kv, max_q, max_kv, D, batch, page in cases:
         floats = lib.q8a_paged_workspace_floats(batch, total, heads, kv, max_q, max_kv, D)
-        width = -(-max_kv // 16)
+        width = -(-max_kv // page)
         rec.record_start(WORKSPACE)
-        rc = lib.attn_paged(P(0x100000), 0, heads * D, total, heads, kv, D, P(0x200000), P(0x300000), 4, 16,
-                            kv * 16 * D // 32 * 34, P(0x400000), width, P(0x500000), P(0x600000), batch, max_q, max_kv,
+        rc = lib.attn_paged(P(0x100000), 0, heads * D, total, heads, kv, D, P(0x200000), P(0x300000), 4, page,
+                            kv * page * D // 32 * 34, P(0x400000), width, P(0x500000), P(0x600000), batch, max_q, max_kv,
                             0.125, 1, P(0x700000), P(WORKSPACE), floats, P(0))
         got = (ctypes.c_int64 * len(FIELDS))()
         rec.record_take(got)
@@ -76,6 +76,20 @@ def test_workspace_holds_what_is_launched_whatever_the_bounds(launches):
     for total, group, max_q, max_kv, D, batch in itertools.product(
             (1, 2, 3, 16, 40, 300), (1, 3, 4, 8), (1, 2, 4, 9, 16, 17, 300, 1 << 20, (1 << 62) + 1),
             (1, 512, 1025, 70000), (64, 128), (1, 2, 70)):
-        cases.append((total, 2 * group, 2, max_q, max_kv, D, batch))
+        cases.append((total, 2 * group, 2, max_q, max_kv, D, batch, 16))
     for case, r in zip(cases, launches(cases)):
         check(case, r)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_shares_of_the_longest_caches(launches, D):
+    """max_kv may be anything that the table's rows hold, also more than a length (an int32) can be; calls of more than
+    64 sequences share by it."""
+    cases = [(total, 1, 1, 5 + total // batch, max_kv, D, batch, 4096)
+             for batch, total in ((65, 1200), (90, 2000), (140, 3100)) for max_kv in (100000, 1 << 31, 1 << 36, 1 << 42, ((1 << 31) - 1) << 12)]
+    keys = 96 if D == 64 else 64
+    for case, r in zip(cases, launches(cases)):
+        check(case, r)
+        assert r["shares"]
+        most = -(-min(case[4], (1 << 31) - 1) // keys)
+        assert most // 3 <= r["share_tiles"] <= most, (case, r)   # one to three parts of the longest possible length
