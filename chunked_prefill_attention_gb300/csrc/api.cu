@@ -77,20 +77,30 @@ bool q8a::pdl_enabled() { return g_pdl; }
 q8a::PdlScope::PdlScope() : prev(g_pdl) { g_pdl = true; }
 q8a::PdlScope::~PdlScope() { g_pdl = prev; }
 
-// The host-mapped failure word: one page of this library's memory, registered
-// with CUDA on first use (registration pins it; nothing is allocated).  A
-// kernel whose wait runs out stores its status code there as well as in the
-// device word, so q8a_status reads it without a CUDA call.
+// The host-mapped failure words: one page of this library's memory, registered
+// with CUDA on first use (registration pins it; nothing is allocated), with a few
+// words for each device.  A chunk step whose wait runs out stores its status code there as
+// well as in the device word, a paged kernel there alone, so q8a_status reads them
+// without a CUDA call.
 namespace {
 alignas(4096) uint32_t g_host_status_page[4096 / sizeof(uint32_t)];
+constexpr int kHostStride = 16;   // words between devices: a 64-byte line each
+constexpr int kHostDevices = 4096 / (kHostStride * sizeof(uint32_t));
+static_assert(q8a::kHostWords <= kHostStride, "a device's words");
 std::mutex g_host_status_mu;
 std::atomic<int> g_host_status_state{0};   // 0 not tried, 1 registered, 2 registration failed
 uint32_t* g_host_status_dev = nullptr;
 }  // namespace
 
-uint32_t* q8a::host_status_word() {
+uint32_t* q8a::host_status_words() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  if (dev >= kHostDevices) return nullptr;
   const int st = g_host_status_state.load(std::memory_order_acquire);
-  if (st != 0) return st == 1 ? g_host_status_dev : nullptr;
+  if (st != 0) return st == 1 ? g_host_status_dev + dev * kHostStride : nullptr;
   std::lock_guard<std::mutex> lock(g_host_status_mu);
   if (g_host_status_state.load(std::memory_order_relaxed) == 0) {
     // registration is not a stream operation; relaxed capture mode keeps it
@@ -112,14 +122,35 @@ uint32_t* q8a::host_status_word() {
     cudaThreadExchangeStreamCaptureMode(&mode);
     g_host_status_state.store(result, std::memory_order_release);
   }
-  return g_host_status_state.load(std::memory_order_relaxed) == 1 ? g_host_status_dev : nullptr;
+  return g_host_status_state.load(std::memory_order_relaxed) == 1 ? g_host_status_dev + dev * kHostStride : nullptr;
 }
 
 namespace {
-int bad_index(const char* fn, uint32_t s) {
-  return fail(Q8A_ERR_INVALID_ARG,
-              "%s: a paged call met a slot, page, length or query offset out of range (status 0x%x)", fn, s);
+
+// Codes of several words as one: every failure's bit, the role of the first.
+uint32_t join_status(uint32_t a, uint32_t b) { return a ? a | (b & 0xFFu) : b; }
+
+// A device's host-mapped words, read, or read and cleared in one step, so that a code stored
+// meanwhile is in this answer or in the next.
+uint32_t host_status(int dev, bool clear) {
+  uint32_t s = 0;
+  for (uint32_t i = 0; i < q8a::kHostWords; ++i) {
+    uint32_t* w = &g_host_status_page[dev * kHostStride + i];
+    s = join_status(s, clear ? __atomic_exchange_n(w, 0u, __ATOMIC_ACQ_REL) : __atomic_load_n(w, __ATOMIC_ACQUIRE));
+  }
+  return s;
 }
+
+int report_status(const char* fn, uint32_t s) {
+  if (s & 1u)
+    return fail(Q8A_ERR_TIMEOUT, "%s: a device-side wait ran out (status 0x%x, role %u)%s", fn, s, (s >> 8) & 0xFFu,
+                s & 2u ? "; a paged call also met an index out of range" : "");
+  if (s != 0)
+    return fail(Q8A_ERR_INVALID_ARG,
+                "%s: a paged call met a slot, page, length or query offset out of range (status 0x%x)", fn, s);
+  return ok();
+}
+
 }  // namespace
 
 const char* q8a::launch_note() { return g_note; }
@@ -292,7 +323,7 @@ int prepare_chunk_step(const char* fn, const void* q, int64_t q_pos0, const void
     a->head_group = static_cast<int32_t>(g < 1 ? 1 : (g > 8 ? 8 : g));
   }
   a->timeout_ns = g_timeout_ns.load();
-  a->host_status = q8a::host_status_word();
+  a->host_status = q8a::host_status_words();
   return Q8A_OK;
 }
 
@@ -624,32 +655,25 @@ int attn_finalize(const float* l, const float* o, void* out, int64_t batch, int3
 int q8a_device_status(void* stream, uint32_t* status_out, int32_t clear) {
   uint32_t s = 0;
   cudaError_t e = q8a::read_device_status(static_cast<cudaStream_t>(stream), &s, clear != 0);
-  // the paged kernels record in the host-mapped word alone
-  if (e == cudaSuccess && s == 0) s = __atomic_load_n(&g_host_status_page[0], __ATOMIC_ACQUIRE);
-  if (e == cudaSuccess && clear) __atomic_store_n(&g_host_status_page[0], 0u, __ATOMIC_RELEASE);
+  int dev = -1;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kHostDevices) s = join_status(s, host_status(dev, clear != 0));
   if (status_out) *status_out = s;
   if (e != cudaSuccess) return cuda_fail(e, "q8a_device_status");
-  if (s & 2u) return bad_index("q8a_device_status", s);
-  if (s != 0)
-    return fail(Q8A_ERR_TIMEOUT, "q8a_device_status: a device-side wait ran out (status 0x%x, role %u)",
-                s, (s >> 8) & 0xFFu);
-  return ok();
+  return report_status("q8a_device_status", s);
 }
 
 int q8a_status(void* stream) {
   if (g_host_status_state.load(std::memory_order_acquire) == 2)
-    return fail(Q8A_ERR_UNSUPPORTED, "q8a_status: the host-mapped status word could not be registered; "
+    return fail(Q8A_ERR_UNSUPPORTED, "q8a_status: the host-mapped status words could not be registered; "
                                      "use q8a_device_status");
   if (stream) {
     const cudaError_t e = cudaStreamQuery(static_cast<cudaStream_t>(stream));   // does not block
     if (e != cudaSuccess && e != cudaErrorNotReady) return cuda_fail(e, "q8a_status");
   }
-  const uint32_t s = __atomic_load_n(&g_host_status_page[0], __ATOMIC_ACQUIRE);
-  if (s & 2u) return bad_index("q8a_status", s);
-  if (s != 0)
-    return fail(Q8A_ERR_TIMEOUT, "q8a_status: a device-side wait ran out (status 0x%x, role %u)", s,
-                (s >> 8) & 0xFFu);
-  return ok();
+  uint32_t s = 0;
+  for (int dev = 0; dev < kHostDevices; ++dev) s = join_status(s, host_status(dev, false));
+  return report_status("q8a_status", s);
 }
 
 int q8a_set_wait_timeout_ns(uint64_t ns) {

@@ -110,7 +110,7 @@ struct ChunkArgs {
                           // quantised just before the step, stay in L2 for every CTA
                           // that reads them (the pipelined prefill; head_dim 64)
   uint64_t timeout_ns;    // budget of every device-side wait
-  uint32_t* host_status;  // device address of the host-mapped failure word, or null
+  uint32_t* host_status;  // device address of the device's host-mapped words, or null
   // Split form (split_keys > 0): block row y of the grid folds keys
   // [y*split_keys, min((y+1)*split_keys, kv_len)) of the chunk into an empty
   // partial state at part_m/part_l/part_o + y * (bh*n_q) rows; the partials
@@ -140,10 +140,14 @@ int chunk_step_tiles(const void* q, int64_t q_pos0, const void* k_q8, const void
                      float scale, int32_t causal, int64_t tile_begin, int64_t tile_end,
                      bool l2_keep_kv, cudaStream_t stream);
 
-// Device address of the host-mapped failure word that q8a_status reads (the
-// first call registers the library's page for it), or null when the page could
-// not be registered.
-uint32_t* host_status_word();
+// The host-mapped words of a device's failures.  Each is stored by one kind of kernel with
+// one kind of code, so none erases another's.
+enum : uint32_t { kHostChunk = 0, kHostPagedTimeout = 1, kHostPagedIndex = 2, kHostWords = 3 };
+
+// Device address of the current device's host-mapped words, which q8a_status reads (the
+// first call registers the library's page for them), or null when the page could
+// not be registered or has no room for the device.
+uint32_t* host_status_words();
 
 // Budget of every device-side wait (q8a_set_wait_timeout_ns).
 uint64_t wait_timeout_ns();

@@ -11,8 +11,9 @@ namespace q8a {
 // Element types of the paged calls (Q8A_F16, Q8A_BF16, Q8A_F32 of the ABI).
 enum : int32_t { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
-// Codes that the paged kernels store into the host-mapped status word: bit 0 a
-// wait that ran out, bit 1 an index or length out of range; bits 8..15 the role.
+// Codes that the paged kernels store into the device's host-mapped status words, each
+// into its own (kHostPagedTimeout, kHostPagedIndex): bit 0 a wait that ran out, bit 1 an
+// index or length out of range; bits 8..15 the role.
 enum : uint32_t { kRolePaged = 6, kRoleIndex = 7 };
 constexpr uint32_t kStatusTimeout = 1u | (kRolePaged << 8);
 constexpr uint32_t kStatusIndex = 2u | (kRoleIndex << 8);
@@ -62,7 +63,7 @@ struct PagedArgs {
   const int32_t* kv_lens;     // [batch], the new tokens included
   const int32_t* cu_q;        // [batch + 1], first query row of each sequence
   float* part;                // partial states of the split units
-  uint32_t* status;           // device address of the host-mapped status word
+  uint32_t* status;           // device address of the device's host-mapped status words
   int64_t n_pages;
   int64_t page_stride;
   int64_t q_stride;

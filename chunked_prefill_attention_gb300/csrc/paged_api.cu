@@ -92,9 +92,9 @@ int check_pool(const char* fn, const void* k_pages, const void* v_pages, int64_t
   return Q8A_OK;
 }
 
-int status_word(const char* fn, uint32_t** out) {
-  *out = q8a::host_status_word();
-  if (!*out) return refuse(Q8A_ERR_CUDA, fn, "the host-mapped status word could not be registered");
+int status_words(const char* fn, uint32_t** out) {
+  *out = q8a::host_status_words();
+  if (!*out) return refuse(Q8A_ERR_CUDA, fn, "the host-mapped status words could not be registered");
   return Q8A_OK;
 }
 
@@ -154,7 +154,7 @@ int q8kv_append_paged(const void* k, const void* v, int32_t dtype, int64_t n_tok
     r = q8a::RopeArgs{positions, inv_freq, rot_dim, layout == Q8A_ROPE_INTERLEAVED, mscale, 1.0f};
   }
   uint32_t* status = nullptr;
-  if (int rc = status_word(fn, &status)) return rc;
+  if (int rc = status_words(fn, &status)) return rc;
   const cudaError_t e = q8a::launch_append(k, v, dtype, n_tokens, head_dim, k_token_stride, v_token_stride, slots, r,
                                            pool, status, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
@@ -177,7 +177,7 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
   if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 8))
     return refuse(Q8A_ERR_MISALIGNED, fn, "k_out and v_out need 16-byte, slots 8-byte alignment");
   uint32_t* status = nullptr;
-  if (int rc = status_word(fn, &status)) return rc;
+  if (int rc = status_words(fn, &status)) return rc;
   const cudaError_t e = q8a::launch_read(k_out, v_out, dtype, n_tokens, head_dim, slots, pool, status,
                                          static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
@@ -296,7 +296,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   a.causal = causal ? 1 : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.timeout_ns = q8a::wait_timeout_ns();
-  if (int rc = status_word(fn, &a.status)) return rc;
+  if (int rc = status_words(fn, &a.status)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (plan.tiles) {

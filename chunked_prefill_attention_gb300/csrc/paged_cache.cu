@@ -20,6 +20,7 @@
 
 #include "internal.h"
 #include "paged.h"
+#include "paged_seq.cuh"
 #include "ptx.cuh"
 #include "q8_codes.cuh"
 
@@ -330,7 +331,7 @@ append_kernel(const T* k, const T* v, int64_t n_tokens, int64_t k_stride,
       const int64_t off = slot & ((1ll << pool.page_shift) - 1);
       at = page * pool.page_stride + ((static_cast<int64_t>(head) << pool.page_shift) + off) * kRow;
     } else {
-      *reinterpret_cast<volatile uint32_t*>(status) = kStatusIndex;
+      record_index(status);
     }
   }
   __syncwarp();
@@ -438,7 +439,7 @@ read_kernel(T* k, T* v, int64_t n_rows, const int64_t* slots, const PagePool poo
       const uint32_t off = static_cast<uint32_t>(slot[u]) & ((1u << pool.page_shift) - 1);
       at[u] = base + page * pool.page_stride + ((static_cast<int64_t>(head[u]) << pool.page_shift) + off) * kRow;
     } else if (slot[u] >= 0) {
-      *reinterpret_cast<volatile uint32_t*>(status) = kStatusIndex;
+      record_index(status);
     }
   }
   uint32_t w[kU][3], d[kU];

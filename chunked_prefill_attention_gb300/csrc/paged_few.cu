@@ -105,7 +105,7 @@ struct Waiter {
       const int out = static_cast<uint64_t>(clock64() - t0) > budget;
       if (__any_sync(kFull, out)) {
         bad = true;
-        if ((threadIdx.x & 31) == 0) *reinterpret_cast<volatile uint32_t*>(status) = kStatusTimeout;
+        if ((threadIdx.x & 31) == 0) record_timeout(status);
         return;
       }
     }
@@ -326,7 +326,7 @@ paged_few_kernel(const PagedArgs a) {
       __syncwarp();
       if (lane < have) {
         if (page < 0 || page >= a.n_pages) {
-          *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+          record_index(a.status);
           page = 0;
         }
         const int off = (key0 + (lane << piece_shift)) & ((1 << a.page_shift) - 1);

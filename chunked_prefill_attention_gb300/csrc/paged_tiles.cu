@@ -126,7 +126,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl* ctl
         stop = 1;
       } else if (static_cast<uint64_t>(clock64() - t0) > budget) {
         *reinterpret_cast<volatile uint32_t*>(&ctl->abort) = 1u;
-        *reinterpret_cast<volatile uint32_t*>(status) = kStatusTimeout;
+        record_timeout(status);
         stop = 1;
       }
     }
@@ -385,7 +385,7 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
     __syncwarp();
     if (lane < have) {
       if (page < 0 || page >= a.n_pages) {
-        *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+        record_index(a.status);
         page = 0;
       }
       const int off = (key0 + (lane << shift)) & ((1 << a.page_shift) - 1);
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   // the CTA's two); in pairs two, but one for a share of a single key tile
   const int full = (tiles + u.per - 1) / u.per;
   if (static_cast<int64_t>(ctl.first) + full > a.ctas) {   // lengths beyond the call's bounds
-    *reinterpret_cast<volatile uint32_t*>(a.status) = kStatusIndex;
+    record_index(a.status);
     return;
   }
   const bool two = kPair && u.per > 1;

@@ -617,7 +617,8 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
 
 
 def device_status(clear=True, stream=None):
-    """(rc, status word) of the current device; synchronises the stream."""
+    """(rc, status bits) of the current device; synchronises the stream.  Bit 0: a device-side wait ran out
+    (Q8A_ERR_TIMEOUT); bit 1: a paged call met an index out of range (alone Q8A_ERR_INVALID_ARG)."""
     st = ctypes.c_uint32(0)
     s = ctypes.c_void_p(stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
     rc = load().q8a_device_status(s, ctypes.byref(st), 1 if clear else 0)
@@ -625,8 +626,9 @@ def device_status(clear=True, stream=None):
 
 
 def status(stream=None):
-    """Return code of the sync-free status check (q8a_status): Q8A_OK, or
-    Q8A_ERR_TIMEOUT once a kernel has recorded a run-out wait."""
+    """Return code of the sync-free status check (q8a_status): Q8A_OK, Q8A_ERR_TIMEOUT once a kernel of
+    any device has recorded a run-out wait, or Q8A_ERR_INVALID_ARG once a paged call has met an index out
+    of range."""
     s = ctypes.c_void_p(stream.cuda_stream if stream is not None else None)
     return load().q8a_status(s)
 

@@ -416,7 +416,8 @@ int q8a_prefill_graph_destroy(q8a_prefill_graph *graph);
  * Slots, page numbers, lengths and offsets live on the device, so a captured
  * call may be replayed with others.  The kernels check each one: a slot, page or
  * length beyond the pool or the table is never followed.  It is recorded, and
- * q8a_status and q8a_device_status then return Q8A_ERR_INVALID_ARG until cleared.
+ * q8a_status and q8a_device_status then return Q8A_ERR_INVALID_ARG (or Q8A_ERR_TIMEOUT, where
+ * a wait ran out as well) until cleared.
  */
 enum { Q8A_F16 = 0, Q8A_BF16 = 1, Q8A_F32 = 2 };
 enum { Q8A_ROPE_HALF = 0, Q8A_ROPE_INTERLEAVED = 1 };
@@ -520,31 +521,36 @@ int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads
                                    int64_t max_q, int64_t max_kv, int32_t head_dim);
 
 /*
- * q8a_device_status -- read (and optionally clear) the status word of the
- * current device: 0 when no device-side wait has run out since the last clear.
- * Synchronises `stream`.  Returns Q8A_OK, Q8A_ERR_TIMEOUT (when the word is
- * nonzero; *status_out then holds it: bit 0 set, bits 8..15 the role that gave
- * up first: 1 softmax, 2 dequantisation, 3 producer, 4 MMA issue, 5 final drain,
- * 6 paged attention), Q8A_ERR_INVALID_ARG (bit 1: a paged call met an index out
- * of range) or Q8A_ERR_CUDA.  status_out may be NULL.
+ * q8a_device_status -- read (and optionally clear) what the kernels of the current
+ * device have recorded: 0 when no device-side wait has run out and no paged call has
+ * met an index out of range since the last clear.  Synchronises `stream`; kernels of
+ * other streams count as far as they have run.  *status_out (may be NULL) holds bit 0
+ * when a wait ran out, bit 1 when a paged call met an index out of range, both where
+ * both happened, and in bits 8..15 the role: of the chunk-step wait that gave up first
+ * (1 softmax, 2 dequantisation, 3 producer, 4 MMA issue, 5 final drain), else 6 a
+ * wait of the paged attention, else 7 an index.  Returns Q8A_OK, Q8A_ERR_TIMEOUT (bit 0),
+ * Q8A_ERR_INVALID_ARG (bit 1 alone) or Q8A_ERR_CUDA.
  */
 int q8a_device_status(void *stream, uint32_t *status_out, int32_t clear);
 
 /*
  * q8a_status -- the sync-free status check: whether any kernel of this library
- * has recorded a device-side wait that ran out since the last clear, read from
- * a host-mapped word without synchronising anything and without blocking.  A
- * block of a kernel whose wait ran out copies the device's status code (as
- * q8a_device_status reports it) into that word once its roles have stopped;
+ * has recorded a failure (as q8a_device_status reports it) since the last clear, on
+ * any device, read from host-mapped words without synchronising anything and without
+ * blocking.  A block of a chunk step whose wait ran out copies the device's status code
+ * into its device's word once its roles have stopped, the paged kernels store into
+ * theirs at once;
  * the store reaches the host while the kernel runs, so the answer covers the
- * library's kernels that have run so far on any stream, not work still queued.  The word is one page of the
+ * library's kernels that have run so far on any stream, not work still queued.  The words
+ * are one page of the
  * library's own memory, registered with CUDA (cudaHostRegister, mapped and
  * portable) by the first chunk-step or paged call of the process; nothing is allocated.
- * q8a_device_status with `clear` clears it too.
+ * q8a_device_status with `clear` clears the current device's too.
  *   stream   if not NULL, also asks cudaStreamQuery(stream), which does not
  *            block, and reports a CUDA error that the stream's work raised.
  * Returns Q8A_OK, Q8A_ERR_TIMEOUT (a wait ran out; q8a_last_error() names the
- * role), Q8A_ERR_INVALID_ARG (a paged call met an index out of range), Q8A_ERR_CUDA (from cudaStreamQuery) or Q8A_ERR_UNSUPPORTED (the page
+ * role), Q8A_ERR_INVALID_ARG (no wait ran out, but a paged call met an index out of
+ * range), Q8A_ERR_CUDA (from cudaStreamQuery) or Q8A_ERR_UNSUPPORTED (the page
  * could not be registered: use q8a_device_status).
  */
 int q8a_status(void *stream);

@@ -17,7 +17,7 @@ uint32_t g_words[64];
 }  // namespace
 
 namespace q8a {
-uint32_t* host_status_word() { return g_words; }
+uint32_t* host_status_words() { return g_words; }
 cudaError_t launch_paged_few(const PagedArgs& a, int32_t, int32_t, int64_t rows, bool direct, cudaStream_t) {
   g_rec.few_calls++;
   g_rec.few_rows = rows;
