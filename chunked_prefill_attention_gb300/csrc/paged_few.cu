@@ -65,6 +65,8 @@ constexpr int kMaxWarps = kMaxCtas * kWarps;
 constexpr int kMinShare = 2;       // tiles of a warp's share
 constexpr int kDescInts = 8;       // join record of a share boundary
 constexpr float kLazy = 8.0f;      // the reference moves when exceeded by more than 2^8
+// Powers of two of V's scales: of subnormal ones (below 2^-14), and of 65504 and beyond.
+constexpr float kMostUp = 2097152.0f, kLeastUp = 1.0f / 1024.0f;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 template <int D, int NT>
@@ -206,6 +208,7 @@ paged_few_kernel(const PagedArgs a) {
   constexpr int S = Sh::S, KT = Sh::KT, RW = Sh::RW, P = Sh::P, R = Pt::R, NREG = Pt::NREG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+  __shared__ __align__(16) float v_ups[kWarps][D / 32];
   __shared__ int64_t sums[kDirect ? 1 : kWarps], found[kDirect ? 1 : kWarps][2];
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -413,8 +416,9 @@ paged_few_kernel(const PagedArgs a) {
         lim[nt][c] = a.causal ? min(sq.kv, sq.kv - sq.n_q + r / a.group + 1) : sq.kv;
       }
     }
-    // keys that every row of the unit sees: tiles below need no mask
+    // keys that every row of the unit sees: tiles below need no mask; keys that some row sees
     const int clear = a.causal ? sq.kv - sq.n_q + rt * R / a.group + 1 : sq.kv;
+    const int seen = a.causal ? sq.kv - sq.n_q + (min(rt * R + R, n_rows) - 1) / a.group + 1 : sq.kv;
 
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -430,7 +434,15 @@ paged_few_kernel(const PagedArgs a) {
         m[nt][c] = -INFINITY;
         l[nt][c] = 0.0f;
       }
-    int v_exp = 0;   // largest exponent (fp16, biased) of V's scales so far; weights carry 2^(21 - v_exp)
+    // V's scales carry a power of two per block of channels (v_ups) that keeps the largest so far
+    // below 2^7: its product with a weight stays below 2^15 and keeps fp16's 11 bits down to 2^-20
+    // of the largest scale.  Only keys that every row sees count: see `apart`.  One power for all
+    // blocks would cost a block its bits where another is 2^20 times larger; in registers the
+    // powers cost spills (16 sequences of 32,768 keys, 128 channels, 1 token: 201 us, so 198.5;
+    // 193 with one power).
+    __syncwarp();
+    if (lane < D / 32) v_ups[warp][lane] = kMostUp;
+    __syncwarp();
 
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
@@ -483,12 +495,15 @@ paged_few_kernel(const PagedArgs a) {
         }
       }
       // ---- V's scales of keys S g + i
-      uint32_t dv_bits[S][D / 32];
+      float dv[S][D / 32];
+      float v_up[D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) v_up[k] = v_ups[warp][k];
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const uint16_t* rv = reinterpret_cast<const uint16_t*>(vw + (S * g + i) * RW);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) dv_bits[i][k] = rv[17 * k];
+        for (int k = 0; k < D / 32; ++k) dv[i][k] = half_bits(rv[17 * k]) * v_up[k];
       }
 #pragma unroll
       for (int mt = 0; mt < S / 2; ++mt)
@@ -496,15 +511,16 @@ paged_few_kernel(const PagedArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][nt][e] *= sl2[nt][e & 1];
-      if (key0 + KT > clear) {
+      const bool masked = key0 + KT > clear;
+      if (masked) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           const int key = key0 + S * g + i;
-          // rows of the tile that hold no key of the sequence: whatever the page
+          // rows of the tile that hold no key that any row sees: whatever the page
           // or the ring holds there
-          if (key >= sq.kv)
+          if (key >= seen)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) dv_bits[i][k] = 0u;
+            for (int k = 0; k < D / 32; ++k) dv[i][k] = 0.0f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -513,24 +529,35 @@ paged_few_kernel(const PagedArgs a) {
         }
       }
       {
-        uint32_t top = 0;
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) top = max(top, dv_bits[i][k] & 0x7FFFu);
-        const int e = static_cast<int>(__reduce_max_sync(kFull, top) >> 10);
-        if (e > v_exp) {   // uniform over the warp
-          const float f = __int_as_float((127 + v_exp - e) << 23);
-          v_exp = e;
+          for (int k = 0; k < D / 32; ++k) top = fmaxf(top, fabsf(dv[i][k]));
+        if (__any_sync(kFull, top >= 128.0f)) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int k = 0; k < D / 32; ++k) {
+            float mine = 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < S; ++i)
+              if (key0 + S * g + i < clear) mine = fmaxf(mine, fabsf(dv[i][k]));
+            const int e = static_cast<int>(__reduce_max_sync(kFull, __float_as_uint(mine)) >> 23);
+            const float f = fmaxf(__int_as_float((127 + 127 + 6 - max(e, 127 + 6)) << 23), kLeastUp / v_up[k]);
+            v_up[k] *= f;
+            __syncwarp();
+            if (lane == 0) v_ups[warp][k] = v_up[k];
+            __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[i][nt][k] *= f;
+            for (int i = 0; i < S; ++i) dv[i][k] *= f;
+#pragma unroll
+            for (int i = 2 * k; i < 2 * k + 2; ++i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[i][nt][x] *= f;
+          }
         }
       }
-      const float v_up = __int_as_float((127 + 21 - v_exp) << 23);
 
       // ---- the running reference: moved only when a score exceeds it by more than 2^8
       bool over = false;
@@ -562,6 +589,56 @@ paged_few_kernel(const PagedArgs a) {
             }
           }
       }
+      // A key that some rows see and others do not (a later token of a burst) may have a far
+      // larger scale than all before it, or an infinite one, which must not touch the rows that
+      // do not see it: then the tile's keys of that kind are added apart, in fp32.  They are
+      // at most a burst's tokens but one, in a sequence's last tiles.
+      if (masked) {
+        bool apart = false;
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            apart |= key0 + S * g + i >= clear && !(fabsf(dv[i][k]) < 128.0f);   // NaN too
+        if (__any_sync(kFull, apart)) {
+#pragma unroll 1
+          for (int kg = 0; kg < 8; ++kg)
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+              const int key = key0 + S * kg + i;
+              if (key < clear || key >= seen) continue;   // uniform
+              const uint32_t* rv = vw + (S * kg + i) * RW;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float w[2];
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc)
+                  w[cc] = ex2_approx(__shfl_sync(kFull, s[i / 2][nt][2 * (i & 1) + cc], 4 * kg + t) -
+                                     (m[nt][cc] == -INFINITY ? 0.0f : m[nt][cc]));
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                  // channels as in the products: m-tile 2 k + h, codes 2 h and 2 h + 1 of the lane's word
+                  const int p = k / 2;
+                  uint32_t word = rv[17 * p + (k & 1 ? 9 : 1) + g];
+                  if ((k & 1) == 0) word = __byte_perm(word, rv[17 * p], sel_v);
+                  const float d = half_bits(reinterpret_cast<const uint16_t*>(rv)[17 * k]) * v_ups[warp][k];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float v = d * static_cast<float>(static_cast<int8_t>(word >> (8 * e)));
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc)
+                      if (w[cc] != 0.0f) o[2 * k + e / 2][nt][2 * (e & 1) + cc] = fmaf(w[cc], v, o[2 * k + e / 2][nt][2 * (e & 1) + cc]);
+                  }
+                }
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < S; ++i)
+            if (key0 + S * g + i >= clear)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) dv[i][k] = 0.0f;
+        }
+      }
       // ---- weights, per V block times its scale, and their transposition
       uint32_t pb[NT][D / 32][S];
 #pragma unroll
@@ -576,8 +653,7 @@ paged_few_kernel(const PagedArgs a) {
           l[nt][1] += w1;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
-            const float dv = half_bits(dv_bits[i][k]) * v_up;
-            pb[nt][k][i] = transpose8(pack_half2(w0 * dv, w1 * dv));
+            pb[nt][k][i] = transpose8(pack_half2(w0 * dv[i][k], w1 * dv[i][k]));
           }
         }
       }
@@ -617,13 +693,12 @@ paged_few_kernel(const PagedArgs a) {
     it += n;
 
     // ---- the unit's rows, or this share's part of them
-    const float v_down = __int_as_float((127 - 21 + v_exp) << 23);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][nt][e] *= v_down;
+        for (int e = 0; e < 4; ++e) o[i][nt][e] *= __int_as_float((254 << 23) - __float_as_int(v_ups[warp][i / 2]));   // 1 / v_up
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -502,8 +502,10 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *                must be ordered on one stream.
  * Numerics: keys and values enter the tensor cores exactly (with bf16 output and
  * max_q * group above 16, values rounded once to fp16); scores, maxima, sums and the
- * accumulated values are fp32; each weight is rounded once to fp16, the output once to
- * its type.  The values d*q of a sequence's keys and values are within fp16's range, also
+ * accumulated values are fp32; each weight (with max_q * group up to 16: each product of a
+ * weight and the scale of a value's block) is rounded once to fp16, half a step of 2^-11
+ * or, for small ones, of 2^-31 of the largest such product that its row and block could have;
+ * the output is rounded once to its type.  The values d*q of a sequence's keys and values are within fp16's range, also
  * those that a row does not see.  The result does not depend on timing.  A sequence
  * with a bad page number gets an unspecified result, the others theirs.
  * Errors: as attn_rope; Q8A_ERR_INVALID_ARG also for a too small workspace.

@@ -1,0 +1,160 @@
+"""attn_paged where values differ by more than a factor of 2^20 between blocks of channels, between keys, and between
+what a row sees and what it does not.
+
+Tolerances.  As in Batch.check, with what belongs to the kernel that takes the call.  At most 16 rows per K/V head: a
+weight times its block's scale is rounded once to fp16, 2^-11 of it, and V is not rounded.  These products carry
+a power of two that puts the largest scale d of the block at 2^6 or more, the largest weight being 1 or more, so below
+fp16's normal range they are off by half a step, 2^-25, which is 2^-31 d, times codes of at most 127: together
+2^-31 n 127 d of the output, n the keys that the row sees and d their largest scale.  More rows: the products'
+terms of Batch.check.  A bound in A covers each score's error too.  Outputs of fp16 are off by half their smallest
+step, 2^-25, at least."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import q8_0
+from tests.test_gpu_paged import BF16, F16, Batch, Q, clean_status, rows_of, unit   # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def rewrite(x, b, pages, rows, at):
+    """Rows [n, kv_heads, bytes] of keys `at` of sequence b put into its pages."""
+    slots = x.slots(b, at.cuda())
+    pages[slots // x.page, :, slots % x.page] = rows.cuda()
+
+
+def set_values(x, b, v):
+    """Sequence b's values (fp32 [n, kv_heads, D]) put into its pages."""
+    rows = rows_of(v)
+    rewrite(x, b, x.v_pages, rows, torch.arange(len(v)))
+    x.v[b] = torch.from_numpy(q8_0.dequantize_kv(rows.numpy()))
+
+
+def check_rows(x, out, causal=True, rows=None):
+    """Every row (of `rows`, a set of (sequence, token), where given) against the 64-bit result over the keys that it
+    sees alone, by a bound per block of channels."""
+    few = max(x.q_lens) * x.group <= 16
+    u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D), 0
+    for b, (nq, n) in enumerate(zip(x.q_lens, x.kv_lens_host)):
+        for i in range(nq):
+            if rows is not None and (b, i) not in rows:
+                continue
+            m = min(n, n - nq + i + 1) if causal else n
+            got = out[first + i].double()
+            if m <= 0:
+                assert (got == 0).all()
+                continue
+            q = x.q[first + i].double().view(-1, x.group, x.D)
+            k, v = (t[:m].cuda().transpose(0, 1) for t in (x.k[b], x.v[b]))       # [kv_heads, m, D]
+            s = q @ k.transpose(1, 2) * scale
+            G = (q.abs() @ k.abs().transpose(1, 2) * scale).amax()
+            p = torch.softmax(s, -1)
+            y, A = (p @ v).view(-1, x.D), (p @ v.abs()).view(-1, x.D)
+            score = 2 * (2.0 ** -19 * G + 2.0 ** -21) * A
+            if few:
+                d = v.abs().view(v.shape[0], m, -1, 32).amax((1, 3))              # 127 d, [kv_heads, blocks]
+                d = d.repeat_interleave(32, -1).repeat_interleave(x.group, 0)
+                tol = 2.0 ** -11 * A + score + 2.0 ** -31 * m * d
+            else:
+                all_v = v.abs().sum(1).repeat_interleave(x.group, 0)
+                tol = 2.0 ** -11 * (1 if out.dtype == F16 else 2) * A + score + 2.0 ** -11 * y.abs() + 2.0 ** -32 * all_v
+            tol = tol + u * (y.abs() + tol) + 2.0 ** -25
+            bad = ~((got - y).abs() <= tol)
+            assert not bad.any(), (b, i, bad.nonzero()[:4].tolist(), float((got - y).abs().max()),
+                                   float(((got - y).abs() / tol).max()))
+        first += nq
+
+
+def sharp(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed):
+    """Few keys carry a row's weight, so that outputs are as large as single values."""
+    return Batch(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed=seed, q_scale=6.0)
+
+
+FEW = [([1], [700], 4, 4), ([1, 1], [40, 3000], 8, 2), ([4], [900], 8, 2), ([9], [300], 2, 2), ([16], [16], 1, 1),
+       ([1], [9000], 12, 1)]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads", FEW)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_blocks_of_very_different_scales(Q, q_lens, kv_lens, heads, kv_heads, D, dtype):
+    """One block of channels does not cost the others their bits."""
+    x = sharp(q_lens, kv_lens, heads, kv_heads, D, 16, dtype, seed=71)
+    g = torch.Generator().manual_seed(72)
+    lift = torch.tensor([2.0 ** e for e in (12, -13, 0, -6)][:D // 32]).repeat_interleave(32)
+    for b, n in enumerate(kv_lens):
+        set_values(x, b, torch.randn((n, kv_heads, D), generator=g) * lift)
+    check_rows(x, Q.attn_paged(*x.args()))
+
+
+BURSTS = [
+    # new tokens, keys, heads, kv heads: the tokens of a burst in one tile, over two, alone; 2 to 16 rows
+    ([4], [900], 8, 2), ([16], [1000], 1, 1), ([16], [33], 1, 1), ([5], [35], 2, 2), ([9], [9], 1, 1), ([4, 3], [64, 2050], 4, 1),
+    ([2], [20000], 8, 1), ([8], [4099], 2, 1), ([12, 1, 7], [500, 31, 129], 3, 3), ([7], [4], 2, 1),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads", BURSTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_a_later_tokens_scale(Q, q_lens, kv_lens, heads, kv_heads, D, dtype):
+    """Values that grow by 2^6 or more from token to token of a burst do not touch the rows before them."""
+    x = sharp(q_lens, kv_lens, heads, kv_heads, D, 16, dtype, seed=73)
+    g = torch.Generator().manual_seed(74)
+    for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
+        v = torch.randn((n, kv_heads, D), generator=g) * 2.0 ** -12
+        steps = min(nq, n) - 1
+        for j in range(steps):   # the keys after the first row's last one
+            v[n - steps + j] *= 2.0 ** min(25, 6 * (j + 1) + (j & 1) * 7)
+        set_values(x, b, v)
+    check_rows(x, Q.attn_paged(*x.args()))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads", BURSTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("scale,code", [(0x7C00, 0), (0x7C00, 5), (0x7E01, -3)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_infinite_and_nan_scales_that_a_row_does_not_see(Q, q_lens, kv_lens, heads, kv_heads, D, dtype, scale, code, which):
+    """A key of a burst with a scale that is no number spoils the rows that see it and no others."""
+    x = sharp(q_lens, kv_lens, heads, kv_heads, D, 16, dtype, seed=75)
+    pages, blk, clean, first = {"k": x.k_pages, "v": x.v_pages}[which], D // 32 - 1, set(), 0
+    spoiled = []
+    for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
+        at = max(0, n - max(1, min(nq, n) // 2))   # rows from here on see it
+        rows = pages[x.slots(b, torch.tensor([at], device="cuda")) // x.page, :,
+                     x.slots(b, torch.tensor([at], device="cuda")) % x.page].cpu().numpy().copy()
+        one = rows.reshape(-1, D // 32, 34)
+        one[:, blk, :2] = np.frombuffer(np.uint16(scale).tobytes(), dtype=np.uint8)
+        one[:, blk, 2:] = np.uint8(code & 0xFF)
+        rewrite(x, b, pages, torch.from_numpy(rows), torch.tensor([at]))
+        for i in range(nq):
+            if n - nq + i >= at:
+                spoiled.append(first + i)
+            else:
+                clean.add((b, i))
+        first += nq
+    out = Q.attn_paged(*x.args())
+    check_rows(x, out, rows=clean)
+    if which == "v":
+        assert not torch.isfinite(out[spoiled][..., 32 * blk:]).any()
+    elif code <= 0:   # an infinite scale times codes whose product with q is below 0 is a score of -inf: weight 0
+        assert not torch.isfinite(out[spoiled]).any()
+
+
+def test_bytes_that_hold_no_keys_do_not_count(Q):
+    """Rows of a page behind the last key, whatever they hold, and blocks of zeros."""
+    x = sharp([3, 1], [50, 70], 4, 2, 64, 16, F16, seed=76)
+    for b, n in enumerate(x.kv_lens_host):
+        v = x.v[b].float()
+        v[:, :, 32:] = 0.0
+        v[n // 2:, :, :32] *= 1e-3
+        set_values(x, b, v)
+    out = Q.attn_paged(*x.args())
+    check_rows(x, out)
+    assert (out[..., 32:] == 0).all()
