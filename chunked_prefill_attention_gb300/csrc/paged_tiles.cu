@@ -404,10 +404,18 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
 // One block of one row (nine-word window w; even blocks start word-aligned, odd ones
 // two bytes into the first word) -> 16-byte chunks of the swizzled row.  `odd` is the same for
 // a warp: as a branch 672 us, as selections of words 710 (D = 128, bf16).
-template <bool kLo, bool odd>
+//
+// A weight of 0 does not keep a row from what it does not see: 0 times an infinite or NaN value is NaN.
+// So V's scales count as at most 515.5, the largest whose values all fit fp16 (127 x 515.5 =
+// 65,468.5), NaN too: no value of V is anything but a number (one instruction a block, no
+// time: 799 and 800 us for whole prompts of 64 channels).  For K masked scores are assigned.
+// Giving NaN to the rows that see such a key as well, by a note of the first one, took 3 %
+// of the time where V's dequantising warps looked, 25 % where the producer did.
+template <bool kLo, bool odd, bool kV>
 __device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], uint8_t* hi_row, uint8_t* lo_row,
                                               int chunk0, int sw) {
-  const __half2 d2 = __half2half2(__ushort_as_half(static_cast<unsigned short>(odd ? w[0] >> 16 : w[0] & 0xFFFFu)));
+  __half2 d2 = __half2half2(__ushort_as_half(static_cast<unsigned short>(odd ? w[0] >> 16 : w[0] & 0xFFFFu)));
+  if (kV) d2 = __hmin2(d2, __half2half2(__ushort_as_half(0x6007)));   // 515.5; of NaN and a number the number
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint32_t c0 = odd ? w[1 + 2 * c] : __byte_perm(w[2 * c], w[2 * c + 1], 0x5432);
@@ -428,7 +436,7 @@ __device__ __forceinline__ void dequant_block(const uint32_t (&w)[9], uint8_t* h
 
 // One (32 rows, block) group of a tile: the lanes read consecutive rows, 17 words apart
 // (32 banks; 34 apart at D = 128: two lanes a bank).
-template <int D, bool kPair, bool kLo>
+template <int D, bool kPair, bool kV, bool kLo>
 __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile, int group, int n_valid, int lane) {
   using G = Geo<D, kPair>;
   const int row = (group % (G::BN / 32)) * 32 + lane, blk = group / (G::BN / 32);
@@ -442,9 +450,9 @@ __device__ __forceinline__ void dequant_group(const uint8_t* raw, uint8_t* tile,
 #pragma unroll
     for (int k = 0; k < 9; ++k) c[k] = p[k];
     if (odd)
-      dequant_block<kLo, true>(c, hi, lo, chunk0, row & 7);
+      dequant_block<kLo, true, kV>(c, hi, lo, chunk0, row & 7);
     else
-      dequant_block<kLo, false>(c, hi, lo, chunk0, row & 7);
+      dequant_block<kLo, false, kV>(c, hi, lo, chunk0, row & 7);
   } else {   // keys that the sequence does not have: whatever the page holds is not read
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -477,8 +485,8 @@ __device__ __forceinline__ void dequant(const PagedArgs& a, const Unit& u, int w
     const int n_valid = u.sq.kv - (u.t0 + t) * G::BN;
 #pragma unroll 1
     for (; mine < kGroups; mine += kWarps)
-      dequant_group<D, kPair, kLo>(smem + G::OFF_RAW + (2 * s + kV) * G::RAWB,
-                                   smem + (kV ? G::OFF_V : G::OFF_K) + sd * 2 * G::TILE, mine, n_valid, lane);
+      dequant_group<D, kPair, kV, kLo>(smem + G::OFF_RAW + (2 * s + kV) * G::RAWB,
+                                       smem + (kV ? G::OFF_V : G::OFF_K) + sd * 2 * G::TILE, mine, n_valid, lane);
     fence_proxy_async_smem();
     mbar_arrive(bar((kV ? G::B_VFULL : G::B_KFULL) + sd));
     mbar_arrive(bar(G::B_RAWEMPTY + s));

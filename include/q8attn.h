@@ -505,8 +505,12 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  * accumulated values are fp32; each weight (with max_q * group up to 16: each product of a
  * weight and the scale of a value's block) is rounded once to fp16, half a step of 2^-11
  * or, for small ones, of 2^-31 of the largest such product that its row and block could have;
- * the output is rounded once to its type.  The values d*q of a sequence's keys and values are within fp16's range, also
- * those that a row does not see.  The result does not depend on timing.  A sequence
+ * the output is rounded once to its type.  Scales d are not negative, and at most 515.5, so
+ * that all values d*q are within fp16's range; a key with a larger, infinite or NaN scale
+ * (Q8_0 of inputs beyond it) leaves the results of the rows that do not see it as they are.
+ * Rows that see it take it as it is; with max_q * group above 16 they may take a scale of V
+ * for 515.5, and get NaN where K has values beyond fp16's range.
+ * The result does not depend on timing.  A sequence
  * with a bad page number gets an unspecified result, the others theirs.
  * Errors: as attn_rope; Q8A_ERR_INVALID_ARG also for a too small workspace.
  */

@@ -41,33 +41,31 @@ def check_rows(x, out, causal=True, rows=None):
     few = max(x.q_lens) * x.group <= 16
     u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D), 0
     for b, (nq, n) in enumerate(zip(x.q_lens, x.kv_lens_host)):
+        last = torch.arange(nq, device="cuda") + n - nq if causal else torch.full((nq,), n - 1, device="cuda")
+        got = out[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)   # [kv_heads, group, nq, D]
+        q = x.q[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)
+        first += nq
+        k, v = (t.cuda().transpose(0, 1)[:, None] for t in (x.k[b], x.v[b]))                  # [kv_heads, 1, n, D]
+        seen = torch.arange(n, device="cuda") <= last[:, None]
+        none, at = last < 0, last.clamp(min=0)
+        s = (q @ k.transpose(2, 3) * scale).masked_fill(~seen, -math.inf)
+        p = torch.where(none[:, None], 0.0, torch.softmax(s, -1))
+        G = torch.where(seen, q.abs() @ k.abs().transpose(2, 3) * scale, 0.0).amax(-1, keepdim=True)
+        y, A = p @ v, p @ v.abs()
+        score = 2 * (2.0 ** -19 * G + 2.0 ** -21) * A
+        if few:
+            d = v.abs().unflatten(-1, (-1, 32)).amax(-1).cummax(2).values[:, :, at].repeat_interleave(32, -1)   # 127 d
+            tol = 2.0 ** -11 * A + score + 2.0 ** -31 * (last[:, None] + 1) * d
+        else:
+            tol = (2.0 ** -11 * (1 if out.dtype == F16 else 2) * A + score + 2.0 ** -11 * y.abs() +
+                   2.0 ** -32 * v.abs().cumsum(2)[:, :, at])
+        tol = torch.where(none[:, None], 0.0, tol + u * (y.abs() + tol) + 2.0 ** -25)
+        bad = ~((got - y).abs() <= tol)
         for i in range(nq):
             if rows is not None and (b, i) not in rows:
-                continue
-            m = min(n, n - nq + i + 1) if causal else n
-            got = out[first + i].double()
-            if m <= 0:
-                assert (got == 0).all()
-                continue
-            q = x.q[first + i].double().view(-1, x.group, x.D)
-            k, v = (t[:m].cuda().transpose(0, 1) for t in (x.k[b], x.v[b]))       # [kv_heads, m, D]
-            s = q @ k.transpose(1, 2) * scale
-            G = (q.abs() @ k.abs().transpose(1, 2) * scale).amax()
-            p = torch.softmax(s, -1)
-            y, A = (p @ v).view(-1, x.D), (p @ v.abs()).view(-1, x.D)
-            score = 2 * (2.0 ** -19 * G + 2.0 ** -21) * A
-            if few:
-                d = v.abs().view(v.shape[0], m, -1, 32).amax((1, 3))              # 127 d, [kv_heads, blocks]
-                d = d.repeat_interleave(32, -1).repeat_interleave(x.group, 0)
-                tol = 2.0 ** -11 * A + score + 2.0 ** -31 * m * d
-            else:
-                all_v = v.abs().sum(1).repeat_interleave(x.group, 0)
-                tol = 2.0 ** -11 * (1 if out.dtype == F16 else 2) * A + score + 2.0 ** -11 * y.abs() + 2.0 ** -32 * all_v
-            tol = tol + u * (y.abs() + tol) + 2.0 ** -25
-            bad = ~((got - y).abs() <= tol)
-            assert not bad.any(), (b, i, bad.nonzero()[:4].tolist(), float((got - y).abs().max()),
-                                   float(((got - y).abs() / tol).max()))
-        first += nq
+                bad[:, :, i] = False
+        assert not bad.any(), (b, bad.nonzero()[:4].tolist(), float((got - y).abs()[bad].max()),
+                               float(((got - y).abs() / tol)[bad].max()))
 
 
 def sharp(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed):
@@ -145,6 +143,69 @@ def test_infinite_and_nan_scales_that_a_row_does_not_see(Q, q_lens, kv_lens, hea
         assert not torch.isfinite(out[spoiled][..., 32 * blk:]).any()
     elif code <= 0:   # an infinite scale times codes whose product with q is below 0 is a score of -inf: weight 0
         assert not torch.isfinite(out[spoiled]).any()
+
+
+MANY = [
+    # 17 rows per K/V head and more: pairs with and without shares, whole CTAs with and without
+    ([17], [900], 1, 1), ([40, 17], [700, 90], 2, 2), ([30, 5], [3000, 100], 8, 2), ([32], [20], 4, 1), ([200], [500], 4, 2),
+    ([300], [300], 2, 2), ([129, 1, 40], [1000, 200, 40], 3, 3), ([260], [5000], 2, 1), ([70] * 9, [97 * i + 75 for i in range(9)], 20, 20),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads", MANY)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_a_later_tokens_scale_among_many_rows(Q, q_lens, kv_lens, heads, kv_heads, D, dtype):
+    x = sharp(q_lens, kv_lens, heads, kv_heads, D, 16, dtype, seed=77)
+    g = torch.Generator().manual_seed(78)
+    for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
+        v = torch.randn((n, kv_heads, D), generator=g) * 2.0 ** -12
+        v[n - min(nq, n) // 2:] *= 2.0 ** 25
+        set_values(x, b, v)
+    check_rows(x, Q.attn_paged(*x.args()))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads", MANY)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("which,scale,code", [("k", 0x7C00, 0), ("k", 0xFE01, -3), ("v", 0x7C00, 0), ("v", 0x7C00, 5),
+                                              ("v", 0x7E01, -3), ("v", 0x6400, 127), ("v", 0x6400, 60), ("v", 0x7BFF, 1)])
+def test_scales_among_many_rows(Q, q_lens, kv_lens, heads, kv_heads, D, dtype, which, scale, code):
+    """Infinite and NaN scales, and scales of V above 515.5, do not touch the rows that do not see them; K's spoil those
+    that do."""
+    x = sharp(q_lens, kv_lens, heads, kv_heads, D, 16, dtype, seed=79)
+    pages, blk, good, first, spoiled = {"k": x.k_pages, "v": x.v_pages}[which], D // 32 - 1, set(), 0, []
+    for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
+        at = max(0, n - max(1, min(nq, n) // 2))
+        slot = x.slots(b, torch.tensor([at], device="cuda"))
+        rows = pages[slot // x.page, :, slot % x.page].cpu().numpy().copy()
+        one = rows.reshape(-1, D // 32, 34)
+        one[:, blk, :2] = np.frombuffer(np.uint16(scale).tobytes(), dtype=np.uint8)
+        one[:, blk, 2:] = np.uint8(code & 0xFF)
+        rewrite(x, b, pages, torch.from_numpy(rows), torch.tensor([at]))
+        for i in range(nq):
+            if n - nq + i < at:
+                good.add((b, i))
+            else:
+                spoiled.append(first + i)
+        first += nq
+    out = Q.attn_paged(*x.args())
+    check_rows(x, out, rows=good)
+    if which == "k":
+        assert torch.isnan(out[spoiled]).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len", [20, 200])
+def test_the_largest_values(Q, q_len, D, dtype):
+    """Scales of 515.5, the largest that count: values up to 65,468.5, of both signs, averaged over many keys."""
+    x = Batch([q_len], [400], 2, 2, D, 16, dtype, seed=81, q_scale=0.05)
+    v = torch.randn((400, 2, D), generator=torch.Generator().manual_seed(82)) * 2e4
+    v[::7] = torch.sign(v[::7]) * 65468.5
+    set_values(x, 0, v.clamp(-65468.5, 65468.5))
+    assert x.v[0].abs().max() == 65468.5
+    check_rows(x, Q.attn_paged(*x.args()))
 
 
 def test_bytes_that_hold_no_keys_do_not_count(Q):
