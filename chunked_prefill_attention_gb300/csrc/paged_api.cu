@@ -38,6 +38,43 @@ int64_t elem_bytes(int32_t dtype) { return dtype == Q8A_F32 ? 4 : 2; }
 constexpr int64_t kMaxTokens = int64_t{1} << 31;
 constexpr int64_t kMaxStride = int64_t{1} << 32;   // elements between tokens
 
+// n rows of `width` bytes, `stride` apart.
+struct Rows {
+  uintptr_t at;
+  int64_t stride, width, n;
+  uintptr_t end() const {   // cut to the last address: the sizes that are accepted can pass it
+    const unsigned __int128 e = static_cast<unsigned __int128>(n - 1) * static_cast<uint64_t>(stride) + at +
+                                static_cast<uint64_t>(width);
+    return e > UINTPTR_MAX ? UINTPTR_MAX : static_cast<uintptr_t>(e);
+  }
+};
+// Whether a row of r has a byte of [lo, hi).
+bool meets(const Rows& r, uintptr_t lo, uintptr_t hi) {
+  if (hi <= r.at || lo >= r.end()) return false;
+  const int64_t gap = static_cast<int64_t>(lo - r.at) - r.width;   // the first row that ends behind lo
+  const int64_t first = lo <= r.at || gap < 0 ? 0 : gap / r.stride + 1;
+  return r.at + static_cast<uintptr_t>(first * r.stride) < hi;     // the last row ends at r.end() > lo
+}
+// Whether two sets of rows (both not empty) share a byte.  Slices of one buffer lie between each other
+// without; those have one stride, so that two rows of b stand for all.
+bool meet(const Rows& a, const Rows& b) {
+  if (a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.n > 1 && b.n > 1 && a.stride == b.stride) {
+    if (b.at < a.at) return meet(b, a);
+    return meets(a, b.at, b.at + b.width);   // a's rows from here on and b's go on in step
+  }
+  const Rows &few = a.n < b.n ? a : b, &many = a.n < b.n ? b : a;
+  for (int64_t i = 0; i < few.n; ++i) {
+    const uintptr_t lo = few.at + static_cast<uintptr_t>(i) * static_cast<uintptr_t>(few.stride);
+    if (lo >= many.end()) return false;
+    if (meets(many, lo, lo + few.width)) return true;
+  }
+  return false;
+}
+Rows rows_at(const void* p, int64_t n, int64_t width, int64_t stride) {
+  return Rows{reinterpret_cast<uintptr_t>(p), stride, width, n};
+}
+
 int check_heads(const char* fn, int32_t heads, int32_t head_dim, int32_t dtype, bool f32) {
   if (heads <= 0 || heads > 65535) return refuse(Q8A_ERR_INVALID_ARG, fn, "heads must be 1..65535 (got %d)", heads);
   if (head_dim != 64 && head_dim != 128)
@@ -120,6 +157,10 @@ int attn_rope(const void* x, void* out, int32_t dtype, int64_t n_tokens, int32_t
   if (!aligned(x, elem_bytes(dtype)) || !aligned(out, elem_bytes(dtype)))
     return refuse(Q8A_ERR_MISALIGNED, fn, "x and out need their element's alignment");
   if (int rc = check_rope(fn, positions, inv_freq, rot_dim, head_dim, layout, mscale)) return rc;
+  const int64_t width = heads * static_cast<int64_t>(head_dim) * elem_bytes(dtype);
+  if (x != out && meet(rows_at(x, n_tokens, width, x_token_stride * elem_bytes(dtype)),
+                       rows_at(out, n_tokens, width, out_token_stride * elem_bytes(dtype))))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "x and out overlap");
   const q8a::RopeArgs r{positions, inv_freq, rot_dim, layout == Q8A_ROPE_INTERLEAVED, mscale,
                         inverse ? -1.0f : 1.0f};
   const cudaError_t e = q8a::launch_rope(x, out, dtype, n_tokens, heads, head_dim, x_token_stride, out_token_stride,
@@ -148,6 +189,11 @@ int q8kv_append_paged(const void* k, const void* v, int32_t dtype, int64_t n_tok
   const int64_t per16 = 16 / elem_bytes(dtype);
   if (!aligned(k, 16) || !aligned(v, 16) || k_token_stride % per16 || v_token_stride % per16 || !aligned(slots, 8))
     return refuse(Q8A_ERR_MISALIGNED, fn, "k, v and their token strides need 16-byte, slots 8-byte alignment");
+  {
+    const int64_t page = static_cast<int64_t>(kv_heads) * page_tokens * row_bytes(head_dim);
+    if (meet(rows_at(k_pages, n_pages, page, page_stride_bytes), rows_at(v_pages, n_pages, page, page_stride_bytes)))
+      return refuse(Q8A_ERR_INVALID_ARG, fn, "k_pages and v_pages overlap");
+  }
   q8a::RopeArgs r{};
   if (positions || inv_freq) {
     if (int rc = check_rope(fn, positions, inv_freq, rot_dim, head_dim, layout, mscale)) return rc;
@@ -176,6 +222,9 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
   if (!k_out || !v_out || !slots) return refuse(Q8A_ERR_INVALID_ARG, fn, "null pointer");
   if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 8))
     return refuse(Q8A_ERR_MISALIGNED, fn, "k_out and v_out need 16-byte, slots 8-byte alignment");
+  const int64_t bytes = n_tokens * kv_heads * head_dim * elem_bytes(dtype);
+  if (meet(rows_at(k_out, 1, bytes, bytes), rows_at(v_out, 1, bytes, bytes)))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "k_out and v_out overlap");
   uint32_t* status = nullptr;
   if (int rc = status_words(fn, &status)) return rc;
   const cudaError_t e = q8a::launch_read(k_out, v_out, dtype, n_tokens, head_dim, slots, pool, status,
@@ -274,6 +323,14 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   if (workspace_floats < need)
     return refuse(Q8A_ERR_INVALID_ARG, fn, "workspace of %lld floats < %lld needed", (long long)workspace_floats,
                   (long long)need);
+  {
+    const int64_t row = static_cast<int64_t>(heads) * head_dim * 2;
+    const Rows q_rows = rows_at(q, total_q, row, q_token_stride * 2), o_rows = rows_at(out, total_q, row, row);
+    if (meet(q_rows, o_rows)) return refuse(Q8A_ERR_INVALID_ARG, fn, "q and out overlap");
+    const Rows ws = rows_at(workspace, 1, need * 4, need * 4);
+    if (need > 0 && (meet(q_rows, ws) || meet(o_rows, ws)))
+      return refuse(Q8A_ERR_INVALID_ARG, fn, "the workspace overlaps q or out");
+  }
   q8a::PagedArgs a{};
   a.q = q;
   a.out = out;

@@ -433,7 +433,8 @@ enum { Q8A_ROPE_HALF = 0, Q8A_ROPE_INTERLEAVED = 1 };
  * inv_freq's own fp64 rounding at any position; the arithmetic is fp32, rounded
  * once to the type.
  *   x, out      [n_tokens][H][D] of dtype with the given token strides.  out may
- *               be x (same stride); otherwise they must not overlap.
+ *               be x (same stride); otherwise they must not overlap (refused; slices of
+ *               one buffer that share no byte are fine).
  *   positions   int64 [n_tokens] on the device, any value.
  *   inv_freq    fp64 [rot_dim/2] on the device, radians per position (scaled for
  *               long contexts as the caller wants).
@@ -455,6 +456,7 @@ int attn_rope(const void *x, void *out, int32_t dtype, int64_t n_tokens, int32_t
  *   k, v        [n_tokens][kv_heads][D] of dtype, 16-byte aligned, token strides
  *               multiples of 16 bytes; finite.
  *   slots       int64 [n_tokens] on the device.
+ *   k_pages, v_pages  pools that share no byte (pages of both may take turns).
  * Errors: as attn_rope.
  */
 int q8kv_append_paged(const void *k, const void *v, int32_t dtype, int64_t n_tokens,
@@ -467,7 +469,7 @@ int q8kv_append_paged(const void *k, const void *v, int32_t dtype, int64_t n_tok
 /*
  * q8kv_read_paged -- read rows back: the values d*q of the rows at `slots`, each
  * rounded once to dtype, into k_out and v_out [n_tokens][kv_heads][D] (contiguous,
- * 16-byte aligned).  Slots in any order and number; a negative slot leaves its
+ * 16-byte aligned, not overlapping).  Slots in any order and number; a negative slot leaves its
  * token's output as it was.
  * Errors: as attn_rope.
  */
@@ -495,7 +497,8 @@ int q8kv_read_paged(const void *k_pages, const void *v_pages, int64_t n_pages, i
  *                at most total_q.  Rows from cu_q[batch] on are left as they were.
  *   max_q, max_kv  upper bounds of the sequences' rows and kv_lens.  They size the
  *                launches: of a sequence beyond them some rows may be left as they were.
- *   out          [total_q][heads][D] of q's type, contiguous, 16-byte aligned; not q.
+ *   out          [total_q][heads][D] of q's type, contiguous, 16-byte aligned; it shares
+ *                no byte with q, nor the workspace with either.
  *   workspace    fp32 scratch, 16-byte aligned, of at least
  *                q8a_paged_workspace_floats(batch, total_q, heads, kv_heads,
  *                max_q, max_kv, D) floats; overwritten.  Calls (and captured graphs) that share one

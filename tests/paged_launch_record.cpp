@@ -1,5 +1,5 @@
-// Stands in for the launches of attn_paged when it is preloaded before the library: it
-// writes down what the C-ABI layer asks for.  No CUDA call is made.
+// Stands in for the launches of the paged calls when it is preloaded before the library: it
+// writes down what the C-ABI layer asks of attn_paged's.  No CUDA call is made.
 #include <cstdint>
 
 #include "../chunked_prefill_attention_gb300/csrc/internal.h"
@@ -18,6 +18,18 @@ uint32_t g_words[64];
 
 namespace q8a {
 uint32_t* host_status_words() { return g_words; }
+cudaError_t launch_rope(const void*, void*, int32_t, int64_t, int32_t, int32_t, int64_t, int64_t, const RopeArgs&,
+                        cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t launch_append(const void*, const void*, int32_t, int64_t, int32_t, int64_t, int64_t, const int64_t*,
+                          const RopeArgs&, const PagePool&, uint32_t*, cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t launch_read(void*, void*, int32_t, int64_t, int32_t, const int64_t*, const PagePool&, uint32_t*,
+                        cudaStream_t) {
+  return cudaSuccess;
+}
 cudaError_t launch_paged_few(const PagedArgs& a, int32_t, int32_t, int64_t rows, bool direct, cudaStream_t) {
   g_rec.few_calls++;
   g_rec.few_rows = rows;
