@@ -17,6 +17,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import q8_0
+from tests import test_gpu_paged as paged
 from tests.test_gpu_paged import BF16, F16, Batch, Q, clean_status, rows_of, unit   # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -45,6 +46,9 @@ def check_rows(x, out, causal=True, rows=None):
         got = out[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)   # [kv_heads, group, nq, D]
         q = x.q[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)
         first += nq
+        if n == 0:
+            assert (got == 0).all()
+            continue
         k, v = (t.cuda().transpose(0, 1)[:, None] for t in (x.k[b], x.v[b]))                  # [kv_heads, 1, n, D]
         seen = torch.arange(n, device="cuda") <= last[:, None]
         none, at = last < 0, last.clamp(min=0)
@@ -71,6 +75,15 @@ def check_rows(x, out, causal=True, rows=None):
 def sharp(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed):
     """Few keys carry a row's weight, so that outputs are as large as single values."""
     return Batch(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed=seed, q_scale=6.0)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv_heads,D,page", paged.FEW + paged.MANY)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_the_bounds_of_the_kernel_that_takes_a_call(Q, q_lens, kv_lens, heads, kv_heads, D, page, dtype, causal):
+    """The tile kernel takes calls from 17 rows per K/V head on; up to 16 rows V is not rounded, bf16 or not."""
+    x = Batch(q_lens, kv_lens, heads, kv_heads, D, page, dtype, seed=len(q_lens) + sum(kv_lens))
+    check_rows(x, Q.attn_paged(*x.args(), causal=causal), causal)
 
 
 FEW = [([1], [700], 4, 4), ([1, 1], [40, 3000], 8, 2), ([4], [900], 8, 2), ([9], [300], 2, 2), ([16], [16], 1, 1),
