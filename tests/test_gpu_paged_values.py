@@ -42,6 +42,8 @@ def check_rows(x, out, causal=True, rows=None):
     few = max(x.q_lens) * x.group <= 16
     u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D), 0
     for b, (nq, n) in enumerate(zip(x.q_lens, x.kv_lens_host)):
+        if nq == 0:
+            continue
         last = torch.arange(nq, device="cuda") + n - nq if causal else torch.full((nq,), n - 1, device="cuda")
         got = out[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)   # [kv_heads, group, nq, D]
         q = x.q[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)
