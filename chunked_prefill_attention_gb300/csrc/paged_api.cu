@@ -296,8 +296,9 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
     return refuse(Q8A_ERR_INVALID_ARG, fn, "heads (%d) must be a positive multiple of kv_heads (%d)", heads, kv_heads);
   if (batch < 0 || batch > (1 << 20) || total_q < 0 || total_q >= kMaxTokens || max_q < 0 || max_kv < 0)
     return refuse(Q8A_ERR_INVALID_ARG, fn, "batch must be 0..2^20, total_q 0..2^31-1, max_q and max_kv not negative");
-  if (!(scale > 0.0f) || !std::isfinite(scale))
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "scale must be finite and > 0");
+  const float scale_log2 = scale * 1.4426950408889634f;   // log2(e)
+  if (!(scale > 0.0f) || !std::isfinite(scale_log2))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "scale must be > 0 and finite, also times log2(e)");
   if (int rc = check_stride(fn, "q", q_token_stride, heads, head_dim)) return rc;
   if (batch == 0 || total_q == 0 || max_q == 0) return q8a::clear_error();
   q8a::PagePool pool;
@@ -351,7 +352,7 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
   a.group = heads / kv_heads;
   a.page_shift = pool.page_shift;
   a.causal = causal ? 1 : 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.timeout_ns = q8a::wait_timeout_ns();
   if (int rc = status_words(fn, &a.status)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -106,6 +106,14 @@ def test_shares_of_the_longest_caches(launches, D):
         assert most // 3 <= r["share_tiles"] <= most, (case, r)   # one to three parts of the longest possible length
 
 
+def test_a_scale_that_is_no_number_in_base_2_is_refused(launches):
+    """The kernels take scale * log2(e), which passes fp32's range before the scale does."""
+    call = [1 << 24, 0, 64, 1, 1, 1, 64, 1 << 40, 1 << 41, 99, 16, 16 * 68, 0x4000, 99, 0x5000, 0x6000, 1, 1, 64, 0.0, 1, 1 << 25, 0,
+            0, 0]
+    cases = [("attn_paged", call[:19] + [s] + call[20:]) for s in (2.3e38, 2.4e38, 3.4e38, 1e-30)]
+    assert [rc for rc, _ in launches(cases, "child_overlap")] == [0, -1, -1, 0]
+
+
 def rows_meet(a, sa, na, b, sb, nb, wa, wb=None):
     """By every pair of rows."""
     wb = wa if wb is None else wb
