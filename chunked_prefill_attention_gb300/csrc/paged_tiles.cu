@@ -45,6 +45,7 @@
 //
 // Every wait is bounded, as in chunk_step.cu.
 
+#include <cfloat>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -606,7 +607,8 @@ __device__ __forceinline__ void softmax(const PagedArgs& a, const Unit& u, int x
       const int e = static_cast<int>(top >> 7);
       const int f = (e == 0 || e == 255) ? 0 : min(141 - e, 100);
       const float up = __int_as_float((127 + f) << 23);
-      sl2 *= __int_as_float((127 - f) << 23);
+      // not 0: the mask's -infinity times it has to stay (scores that small are 0 either way)
+      sl2 = fmaxf(sl2 * __int_as_float((127 - f) << 23), FLT_MIN);
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) {
         const uint32_t v = q[i / 32][i % 32];

@@ -36,11 +36,11 @@ def set_values(x, b, v):
     x.v[b] = torch.from_numpy(q8_0.dequantize_kv(rows.numpy()))
 
 
-def check_rows(x, out, causal=True, rows=None):
+def check_rows(x, out, causal=True, rows=None, scale=None):
     """Every row (of `rows`, a set of (sequence, token), where given) against the 64-bit result over the keys that it
     sees alone, by a bound per block of channels."""
     few = max(x.q_lens) * x.group <= 16
-    u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D), 0
+    u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D) if scale is None else scale, 0
     for b, (nq, n) in enumerate(zip(x.q_lens, x.kv_lens_host)):
         if nq == 0:
             continue
@@ -221,6 +221,15 @@ def test_the_largest_values(Q, q_len, D, dtype):
     set_values(x, 0, v.clamp(-65468.5, 65468.5))
     assert x.v[0].abs().max() == 65468.5
     check_rows(x, Q.attn_paged(*x.args()))
+
+
+@pytest.mark.parametrize("q_len", [3, 20, 200])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scores_that_vanish(Q, q_len, dtype):
+    """Queries and scales so small that all scores are 0: the average of what a row sees."""
+    for q_scale, scale in ((2.0 ** -100 if dtype == BF16 else 2.0 ** -14, 1e-20), (1.0, 1e-38), (1.0, 1e-44)):
+        x = Batch([q_len], [q_len + 30], 4, 2, 64, 16, dtype, seed=83, q_scale=q_scale)
+        check_rows(x, Q.attn_paged(*x.args(), scale=scale), scale=scale)
 
 
 def test_bytes_that_hold_no_keys_do_not_count(Q):
