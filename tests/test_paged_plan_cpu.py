@@ -65,7 +65,8 @@ def launches(lib, tmp_path_factory):
     def run(cases, name="child"):
         r = subprocess.run([sys.executable, "-c", f"import sys, json; from tests.test_paged_plan_cpu import {name}; "
                                                   f"{name}(json.load(sys.stdin))"],
-                           cwd=ROOT, env=dict(os.environ, LD_PRELOAD=so), input=json.dumps(cases), capture_output=True,
+                           cwd=ROOT, env=dict(os.environ, LD_PRELOAD=" ".join([os.environ.get("LD_PRELOAD", ""), so]).strip()),
+                           input=json.dumps(cases), capture_output=True,
                            text=True, timeout=300)
         assert r.returncode == 0, r.stdout + r.stderr
         return json.loads(r.stdout)
