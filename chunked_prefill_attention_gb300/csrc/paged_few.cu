@@ -54,6 +54,7 @@
 #include "paged.h"
 #include "paged_seq.cuh"
 #include "ptx.cuh"
+#include "q8_codes.cuh"
 
 namespace q8a {
 namespace {
@@ -130,25 +131,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Four signed codes as two half2, exactly: u = c + 128 under the exponent of
-// 1024 is 1024 + u; minus 1152.
 __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
-  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
+  __half2 l, h;
+  q8a::codes_to_half2(w, l, h);
+  lo = h2u(l);
+  hi = h2u(h);
 }
 
 __device__ __forceinline__ float half_bits(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Weight of a partial state with reference m under the joint reference top.
 __device__ __forceinline__ float join_weight(float m, float top) {
@@ -236,7 +227,7 @@ paged_few_kernel(const PagedArgs a) {
     inner = true;
   } else {
     int64_t mine = 0;
-    for (int b = tid; b < a.batch; b += kThreads) mine += units_of<D, NT>(a, read_seq(a, b)).all;
+    for (int i = tid; i < a.batch; i += kThreads) mine += units_of<D, NT>(a, read_seq(a, i)).all;
     const int64_t inc = warp_inclusive(mine, lane);
     if (lane == 31) sums[warp] = inc;
     __syncthreads();

@@ -55,6 +55,7 @@
 #include "paged.h"
 #include "paged_seq.cuh"
 #include "ptx.cuh"
+#include "q8_codes.cuh"
 
 namespace q8a {
 namespace {
@@ -143,28 +144,11 @@ template <uint32_t N>
 __device__ __forceinline__ void reg_dealloc() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// Four signed codes as two half2, exactly (1024 + 128 + c under the exponent of
-// 1024, minus 1152).
-__device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& lo, __half2& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
-  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  lo = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-  hi = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "

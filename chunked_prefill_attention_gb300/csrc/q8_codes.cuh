@@ -1,4 +1,5 @@
-// q8_codes.cuh -- the arithmetic of Q8_0 codes shared by the quantising kernels.
+// q8_codes.cuh -- the arithmetic of Q8_0 codes: codes to fp16, for the attention kernels, and
+// values to codes, for the quantising ones.
 // A unit that includes it must not be built with fast-math (IEEE rounding).
 #pragma once
 
@@ -7,9 +8,25 @@
 
 namespace q8a {
 
-// Two codes from two values, each as the low byte of a word: q = RN(x / d) by
-// the corrected quotient above (packed fp32x2), rounded half away from zero and
-// clamped to [-127, 127], every step exact in fp32:
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return h2u(__floats2half2_rn(lo, hi)); }
+
+// Four signed int8 codes -> two half2 (exact): flip the sign bit to get
+// u = q + 128 in [0, 255], place u under the fp16 exponent of 1024 (0x64uu is
+// 1024 + u exactly) and subtract 1152.
+__device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& lo, __half2& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
+  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1152
+  lo = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  hi = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+}
+
+// Two codes from two values, each as the low byte of a word: q = RN(x / d), rounded half away from
+// zero and clamped to [-127, 127], in packed fp32x2.  The quotient is corrected (Markstein, IBM J.
+// Res. Dev. 34(1), 1990): y = RN(1 / d) comes in, q0 = RN(x y) is within an ulp of x / d, the residual
+// r = x - q0 d is exact as one fma, and RN(q0 + r y) is RN(x / d).  The other steps are exact in fp32:
 //   floor(RZ(a + 0.5)) is a rounded half away from zero for 0 <= a < 2^23
 //     (a + 0.5 is exact for a >= 0.5; below, round-toward-zero keeps it < 1);
 //   clamping t to 127.5 first clamps floor(t) to 127 (and catches a >= 2^23);

@@ -6,8 +6,8 @@
 // IEEE fp32 divide, and q = round_half_away(x / d) with an IEEE fp32 divide by
 // the stored fp16 d, clamped to [-127, 127] (d == 0 -> all codes 0).
 //
-// The quotient x / d is formed as the correctly rounded fp32 quotient without a
-// divide per value: with y = RN(1/d) (one __frcp_rn per block), q0 = RN(x*y) is
+// The quotient x / d is formed (in q8_codes.cuh) as the correctly rounded fp32 quotient
+// without a divide per value: with y = RN(1/d) (one __frcp_rn per block), q0 = RN(x*y) is
 // within one ulp of x/d, the residual r = x - q0*d is exact as one fma, and
 // RN(q0 + r*y) is RN(x/d) -- Markstein's correction theorem for division
 // with a fused multiply-add (P. Markstein, IBM J. Res. Dev. 34(1), 1990; also
