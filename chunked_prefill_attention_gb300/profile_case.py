@@ -46,12 +46,16 @@ warm-up call and then --reps calls.  --burst 131072 holds 0.57 GB of Q8_0 KV.
 
 With --paged few or tiles it runs attn_paged: single tokens of 16 sequences of
 32,768 keys (32 heads on 8, 128 channels; 1.1 GB of pages), or 9,728 tokens on
-16,384 keys (8 heads, --head-dim channels, no mask), three calls.
+16,384 keys (8 heads, --head-dim channels, no mask), three calls; --bf16 for bf16
+queries instead of fp16.  With --paged append it runs q8kv_append_paged: 16,384 tokens of
+32 heads of 64 channels, fp16, all rotated in interleaved pairs.
 
   ncu --set full --clock-control none -k regex:paged_few_kernel -s 2 -c 1 \\
       python -m chunked_prefill_attention_gb300.profile_case --paged few
   ncu --set full --clock-control none -k regex:paged_tiles_kernel -s 2 -c 1 \\
       python -m chunked_prefill_attention_gb300.profile_case --paged tiles
+  ncu --set full --clock-control none -k regex:append_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged append
 """
 
 import argparse
@@ -66,7 +70,8 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=16384)
     p.add_argument("--chunk", type=int, default=8192)
     p.add_argument("--index", type=int, default=1)
-    p.add_argument("--paged", choices=("few", "tiles"))
+    p.add_argument("--paged", choices=("few", "tiles", "append"))
+    p.add_argument("--bf16", action="store_true")
     p.add_argument("--reps", type=int, default=2)
     p.add_argument("--burst", type=int, default=0)
     p.add_argument("--split", type=int, default=8192)
@@ -78,7 +83,7 @@ def main(argv=None):
     if a.pipelined:
         return pipelined(a)
     if a.paged:
-        return paged(a)
+        return append(a) if a.paged == "append" else paged(a)
     if a.burst > 0:
         return burst(a)
     if a.quantize > 0:
@@ -206,7 +211,7 @@ def paged(a):
     table = torch.arange(batch * width, dtype=torch.int32, device="cuda").view(batch, width)
     lens = torch.full((batch,), keys, dtype=torch.int32, device="cuda")
     cu = torch.arange(0, batch * n_q + 1, n_q, dtype=torch.int32, device="cuda")
-    q = torch.randn((batch * n_q, heads, D), generator=g, device="cuda").half()
+    q = torch.randn((batch * n_q, heads, D), generator=g, device="cuda").to(torch.bfloat16 if a.bf16 else torch.float16)
     out = torch.empty_like(q)
     ws = torch.empty(max(1, Q.paged_workspace_floats(batch, batch * n_q, heads, kv_heads, n_q, keys, D)), device="cuda")
     ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
@@ -220,6 +225,27 @@ def paged(a):
     kv_bytes, flops = 2 * batch * keys * kv_heads * Q.row_bytes(D), 4 * D * heads * batch * n_q * keys
     print(f"attn_paged {a.paged}: {us:.1f} us per call, {kv_bytes / us / 1e3:.0f} GB/s of Q8_0 KV, "
           f"{flops / us / 1e6:.0f} TFLOP/s")
+
+
+def append(a):
+    import torch
+
+    from chunked_prefill_attention_gb300 import q8attn as Q
+
+    T, H, D, page = 16384, 32, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((T, H, D), generator=g, device="cuda").half() for _ in range(2))
+    pages = [torch.empty((T // page, H, page, Q.row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    at, f = torch.arange(T, device="cuda"), Q.rope_inv_freq(D, device="cuda")
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for i in range(8):   # two first, so that the host runs ahead
+        if i == 2:
+            ev[0].record()
+        Q.q8kv_append_paged(k, v, *pages, at, at, f, interleaved=True)
+    ev[1].record()
+    torch.cuda.synchronize()
+    us = ev[0].elapsed_time(ev[1]) / 6 * 1e3
+    print(f"q8kv_append_paged: {us:.1f} us per call, {2 * T * H * (2 * D + Q.row_bytes(D)) / us / 1e3:.0f} GB/s")
 
 
 if __name__ == "__main__":
