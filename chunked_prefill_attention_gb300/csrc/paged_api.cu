@@ -237,10 +237,10 @@ int q8kv_read_paged(const void* k_pages, const void* v_pages, int64_t n_pages, i
 namespace {
 
 // Sequences of at most so many rows (tokens * group) go to the few-row kernel.  Both
-// kernels at 16 rows, 16 sequences of 8 K/V heads: 141 us against 253 for 32,768 keys of 64
-// channels, 275 against 420 of 128; for 2,048 keys 28 against 30 and 50 against 41.  At 32 rows
+// kernels at 16 rows, 16 sequences of 8 K/V heads: 142 us against 257 for 32,768 keys of 64
+// channels, 277 against 419 of 128; for 2,048 keys 28 against 30 and 51 against 42.  At 32 rows
 // a few-row kernel made for them took 310 and 430 (50 and 61 for 2,048 keys), the tile
-// kernel 254 and 422 (30 and 42), so from 17 rows on the tile kernel takes them.
+// kernel 257 and 421 (30 and 42), so from 17 rows on the tile kernel takes them.
 constexpr int64_t kFewRows = 16;
 
 // The launches of a call, from its bounds alone.
@@ -261,7 +261,11 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // The tile kernel takes every sequence of a call of at most 128 rows each (one of few
   // rows costs it no more than one of many, the other kernel's launches 8 us), and of a
   // call whose bounds leave no room for a short one.  Single tokens beside prompts keep their
-  // own kernel: there a long cache would be one CTA's.
+  // own kernel: there a long cache would be one CTA's.  So it is in pairs too where there are
+  // too many for shares, and the lengths, which would tell, are the device's: 20 sequences on 8
+  // K/V heads, one with a burst of 5 tokens, one with 262,144 keys take 2,112 us so and 128 with
+  // the short ones in the few-row kernel; but without the long one (2,000 keys) 50 and 60, and
+  // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
   p.direct = q8a::paged_few_direct(batch, kv_heads, max_kv, head_dim);

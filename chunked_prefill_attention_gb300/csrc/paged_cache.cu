@@ -7,12 +7,12 @@
 // formed in turns, in 64-bit fixed point: F = frac(f / 2 pi) 2^64 from the fp64
 // table, position * F modulo 2^64 (integer arithmetic drops the whole turns
 // exactly), and the top bits as a fraction of half a turn in [-1, 1) for
-// sincospif.  The angle is off by the table's own rounding (2^-53 relative)
-// and by 2^-25 half turns from the conversion to fp32.  Every block forms
-// the angles of its tokens once, in shared memory, for all its heads.
+// sincospif.  The angle is off by 2^-52 of itself (the division by 2 pi) and
+// by 2^-25 half turns from the conversion to fp32.
 //
-// All three kernels are bound by HBM: they read and write each value once and
-// every thread has 32 to 128 bytes in flight before the first use.
+// All three kernels read and write each value once, and every thread has 32 to 128
+// bytes in flight before the first use.  HBM bounds the rotation (81 % of the copy rate) and the
+// read (85 %); the append waits for its loads and barriers (42 %, see there).
 // This unit must not be built with fast-math (IEEE divides in the quantiser).
 
 #include <cuda_bf16.h>
@@ -83,7 +83,8 @@ constexpr int kMaxPairs = 64;
 // Four resident blocks and up to 16 heads a thread: 16,384 tokens, 32 x 128 bf16, half of the
 // channels turned in interleaved pairs, 49 us (three blocks and 8 heads 53, five blocks 54, eight
 // heads in flight 67), 65,536 tokens 176 us, 6.1 TB/s (203); all channels in halves 63 us
-// (three blocks 66, five 87).
+// (three blocks 66, five 87), where two vectors and eight pairs of angles a thread leave bf16 with
+// spills of 60 bytes of stores and 80 of loads (fp16 and fp32 none).
 template <typename T, int N, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads, 4)
 rope_kernel(const T* x, T* out, int64_t n_tokens, int32_t heads, int32_t head_dim, int64_t x_stride,
@@ -224,7 +225,9 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
 // the block's partners of the half layout (another part of the same row, in L1
 // or L2 by then), rotates in registers, quantises, and the warp's rows go
 // through shared memory so that each row leaves as consecutive words.
-// Instruction issue bounds it, not memory.  The half layout in whole runs of eight took 36 us,
+// It waits most of the time (16,384 tokens, 32 x 64 fp16, interleaved, 61 us: issue slots 67 %
+// busy, 42 % of the copy rate, long scoreboard the largest stall): every block forms the angles
+// of its tokens anew for eight rows, behind two barriers.  The half layout in whole runs of eight took 36 us,
 // with a test per channel 40 (16,384 tokens, 8 x 128 bf16, all channels turned).  Resident
 // blocks an SM: five without rotation (65,536 tokens, 8 x 128 bf16: 79 us; with four 88), four
 // with it.

@@ -19,10 +19,11 @@
 // those are rounded to fp16 (one rounding a weight, 2^-11 relative): the codes
 // of both tensors are never scaled in memory or rounded.  bf16 queries enter as
 // fp16 after scaling a row by a power of two (its largest value to [2^14,
-// 2^15)), which keeps their 8 bits down to 2^-38 of that value.
+// 2^15)), which keeps their 8 bits down to 2^-31 of that value (fp16's smallest
+// step is 2^-24).
 // (tcgen05 wants 64 or 128 rows and fp16 operands in shared memory: the codes
 // would have to be converted and stored at more than twice their bytes, for
-// at most 32 useful rows.)
+// at most 16 useful rows.)
 //
 // Layout.  The order of keys inside a tile and of channels inside a block is
 // free as long as both operands agree, and is chosen so that every shared
@@ -78,8 +79,10 @@ struct Shape {
   static constexpr int RW = 17 * P;              // words of a row
   static constexpr int TILE = KT * RW * 4;       // bytes of a tensor's tile: 2176
   static constexpr int STAGE = 2 * TILE;
-  // 16 rows of 128 channels: Q^T's fragments stay in shared memory (in registers they spill
-  // 324 bytes a thread) and take a stage of the ring
+  // 16 rows of 128 channels: Q^T's fragments stay in shared memory and take a stage of the ring
+  // (16 sequences of 32,768 keys: 334 us with them in registers, 275 so).  O's registers and the
+  // weights still spill: 180 bytes of stores and 392 of loads a thread (16 rows of 64 channels:
+  // 72 and 192; 8 rows of 128: 24 and 56).
   static constexpr bool QS = NT * D >= 256;
   static constexpr int STAGES = QS ? 2 : 3;
   static constexpr int RING = kWarps * STAGES * STAGE;
@@ -966,8 +969,8 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
 
 template <typename QT, int D>
 cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStream_t stream) {
-  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 141 us instead
-  // of 107 at 64 channels, 275 instead of 192 at 128
+  // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
+  // of 106 at 64 channels, 277 instead of 198 at 128
   if (direct) {
     const int ctas = a.batch * a.kv_heads;
     return rows <= 8 ? launch_few<QT, D, 1, true>(a, ctas, stream) : launch_few<QT, D, 2, true>(a, ctas, stream);

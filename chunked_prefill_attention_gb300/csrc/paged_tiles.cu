@@ -37,8 +37,8 @@
 // Pairs (calls of at most 128 rows per K/V head): both tiles hold the same rows and take the
 // key tiles in turn, so no half of the CTA idles; dequantisation is the limit then.
 //
-// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 858 (fp16) and
-// 901 (bf16) TFLOP/s, D = 128 851 and 1,023, of 1,699 sustained for a plain bf16 product;
+// Measured without a mask, 9,728 tokens on 16,384 keys, 8 heads: D = 64 854 (fp16) and
+// 901 (bf16) TFLOP/s, D = 128 847 and 1,020, of 1,699 sustained for a plain bf16 product;
 // K's residuals make S cost twice its nominal work, V's (fp16) O.  What the others wait for
 // most is dequantisation (D = 64, bf16, 362 us: without it 311, without exponentials 347, with
 // half of S's products and a sixth of O's 359).
@@ -75,7 +75,7 @@ struct Geo {
   static constexpr int ATOM = BN * 128;                 // bytes of one such column
   static constexpr int TILE = ATOMS * ATOM;             // one fp16 tile
   // Raw ring.  In pairs a key tile serves 128 rows, so the copies' latency counts more: at
-  // D = 64 (16 sequences of 32,768 keys, 8 K/V heads, 32 rows) 3 stages 278 us, 4 259, 6 254;
+  // D = 64 (16 sequences of 32,768 keys, 8 K/V heads, 32 rows) 3 stages 278 us, 4 259, 6 254 (257 since V's scales are clamped);
   // at D = 128 3 stages 446, 4 422.  Otherwise 6 and 4 of them change nothing.
   static constexpr int NR = D == 64 ? (kPair ? 6 : 4) : (kPair ? 4 : 3);
   static constexpr int NS = D == 64 ? 3 : 2;            // score buffers

@@ -4,7 +4,8 @@ Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  Tensors are torch CUDA tensors; their device pointers
 and the current torch stream are handed to the C ABI declared in
 include/q8attn.h.  There is no CPU fallback: if the library is missing or fails
-to load, every call raises.
+to load, every call raises.  No call records history for torch's autograd: results
+do not require a gradient, whatever their inputs do.
 """
 
 import ctypes
@@ -501,7 +502,8 @@ def rope_inv_freq(rot_dim, base=10000.0, factor=1.0, scaling="linear", original_
 def attn_rope(x, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False, out=None):
     """Rotary positions of packed x [T, H, D] (fp16, bf16 or fp32; a slice of a wider buffer is fine):
     the first 2 * len(inv_freq) channels of every head turned by positions [T] (int64) times inv_freq
-    (fp64, see rope_inv_freq).  `out` may be x.  `inverse` turns back (the gradient of the rotation)."""
+    (fp64, see rope_inv_freq).  `out` may be x.  `inverse` turns back: of a gradient in out, the gradient in x
+    (torch's autograd does not call it by itself)."""
     device = _device_of(x)
     code, T, H, D, stride = _packed("x", x, device)
     pos = _index("positions", positions, torch.int64, T, device)

@@ -430,8 +430,7 @@ enum { Q8A_ROPE_HALF = 0, Q8A_ROPE_INTERLEAVED = 1 };
  * with Q8A_ROPE_INTERLEAVED; the other channels are copied.  `inverse` turns back
  * (w -> -w): with mscale 1 it undoes the rotation, and it is the rotation's
  * transpose, so also its gradient.  The angle is exact to 2^-25 half turns plus
- * inv_freq's own fp64 rounding at any position; the arithmetic is fp32, rounded
- * once to the type.
+ * 2^-52 of itself, at any position; the arithmetic is fp32, rounded once to the type.
  *   x, out      [n_tokens][H][D] of dtype with the given token strides.  out may
  *               be x (same stride); otherwise they must not overlap (refused; slices of
  *               one buffer that share no byte are fine).
