@@ -12,7 +12,7 @@
 //
 // All three kernels read and write each value once, and every thread has 32 to 128
 // bytes in flight before the first use.  HBM bounds the rotation (81 % of the copy rate) and the
-// read (85 %); the append waits for its loads and barriers (42 %, see there).
+// read (85 %); the append waits for its loads and barriers (43 %, see there).
 // This unit must not be built with fast-math (IEEE divides in the quantiser).
 
 #include <cuda_bf16.h>
@@ -226,7 +226,7 @@ __device__ __forceinline__ void load8(const T* p, float* f) {
 // or L2 by then), rotates in registers, quantises, and the warp's rows go
 // through shared memory so that each row leaves as consecutive words.
 // It waits most of the time (16,384 tokens, 32 x 64 fp16, interleaved, 61 us: issue slots 67 %
-// busy, 42 % of the copy rate, long scoreboard the largest stall): every block forms the angles
+// busy, 43 % of the copy rate, long scoreboard the largest stall): every block forms the angles
 // of its tokens anew for eight rows, behind two barriers.  The half layout in whole runs of eight took 36 us,
 // with a test per channel 40 (16,384 tokens, 8 x 128 bf16, all channels turned).  Resident
 // blocks an SM: five without rotation (65,536 tokens, 8 x 128 bf16: 79 us; with four 88), four
