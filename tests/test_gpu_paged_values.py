@@ -39,11 +39,14 @@ def set_values(x, b, v):
 def check_rows(x, out, causal=True, rows=None, scale=None):
     """Every row (of `rows`, a set of (sequence, token), where given) against the 64-bit result over the keys that it
     sees alone, by a bound per block of channels."""
-    few = max(x.q_lens) * x.group <= 16
+    most, B = max(x.q_lens), len(x.q_lens)
+    # calls of 17 to 128 rows are the tile kernel's, longer ones too but for short sequences that their bounds allow
+    short = most * x.group > 128 and (x.q.shape[0] - (B - 1) * most) * x.group <= 16
     u, scale, first = unit(out.dtype), 1 / math.sqrt(x.D) if scale is None else scale, 0
     for b, (nq, n) in enumerate(zip(x.q_lens, x.kv_lens_host)):
         if nq == 0:
             continue
+        few = most * x.group <= 16 or (short and nq * x.group <= 16)
         last = torch.arange(nq, device="cuda") + n - nq if causal else torch.full((nq,), n - 1, device="cuda")
         got = out[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)   # [kv_heads, group, nq, D]
         q = x.q[first:first + nq].double().view(nq, -1, x.group, x.D).permute(1, 2, 0, 3)
