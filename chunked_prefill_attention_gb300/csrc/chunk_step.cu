@@ -62,7 +62,6 @@
 
 #include "internal.h"
 #include "ptx.cuh"
-#include "q8_codes.cuh"
 
 namespace q8a {
 
@@ -199,6 +198,11 @@ __device__ __forceinline__ void reg_dealloc() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -230,6 +234,19 @@ __device__ __forceinline__ void tmem_st32_at(uint32_t taddr, const uint32_t (&r)
       Q8A_W8(r, O + 0), Q8A_W8(r, O + 8), Q8A_W8(r, O + 16), Q8A_W8(r, O + 24)
       : "memory");
 }
+
+// Four signed int8 codes -> two half2 (exact): flip the sign bit to get
+// u = q + 128 in [0, 255], place u under the fp16 exponent of 1024 (0x64uu is
+// 1024 + u exactly) and subtract 1152.
+__device__ __forceinline__ void codes_to_half2(uint32_t w, __half2& lo, __half2& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x5140);
+  const uint32_t b = __byte_perm(u, 0x64646464u, 0x7362);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1152
+  lo = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  hi = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
 // The order of a launch's CTAs over (b, h) units and query units.  The (b, h)
 // units are taken in groups of `group` (ChunkArgs::head_group); within a group

@@ -1,4 +1,4 @@
-// q8_codes.cuh -- the arithmetic of Q8_0 codes: codes to fp16, for the attention kernels, and
+// q8_codes.cuh -- the arithmetic of Q8_0 codes: codes to fp16, for the paged attention, and
 // values to codes, for the quantising ones.
 // A unit that includes it must not be built with fast-math (IEEE rounding).
 #pragma once
