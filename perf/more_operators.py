@@ -323,8 +323,8 @@ def run(s):
         from chunked_prefill_attention_gb300 import q8attn
 
         if c["op"] == "extend":
-            kv, cu, slots, pos, n_free = q8attn.paged_extend(s["new_lens"], s["kv_lens"], s["block_table"],
-                                                             s["free_pages"], s["n_free"], c["page"], s["total"])
+            kv, cu, slots, pos, n_free = q8attn.q8kv_extend_paged(s["new_lens"], s["kv_lens"], s["block_table"],
+                                                                  s["free_pages"], s["n_free"], c["page"], s["total"])
             return kv, cu, slots, pos, n_free, s["block_table"]
         if c["op"] == "norm_rope":
             return q8attn.attn_norm_rope(s["q"], s["k"], s["q_weight"], s["k_weight"], s["positions"], s["inv_freq"],
