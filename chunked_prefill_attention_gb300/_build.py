@@ -11,9 +11,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libq8attn.so")
 SOURCES = ["api.cu", "quantize.cu", "state.cu", "chunk_step.cu", "pipeline.cu", "graph.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_tiles.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "paged.h", "paged_seq.cuh",
-           "q8_codes.cuh"]
+           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_tiles.cu", "paged_step_api.cu", "paged_step.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "paged.h", "paged_check.h", "paged_seq.cuh",
+           "q8_codes.cuh", "rotary.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -68,7 +68,7 @@ def build(verbose=False):
 
 
 SANITIZED_LIB = os.path.join(PKG, "libq8attn_sanitized.so")
-HOST_SOURCES = ["api.cu", "pipeline.cu", "graph.cu", "paged_api.cu"]   # the C-ABI layer: validation, streams, events, graphs
+HOST_SOURCES = ["api.cu", "pipeline.cu", "graph.cu", "paged_api.cu", "paged_step_api.cu"]   # the C-ABI layer: validation, streams, events, graphs
 
 
 def build_sanitized():

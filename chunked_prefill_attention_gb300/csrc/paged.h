@@ -50,6 +50,49 @@ cudaError_t launch_append(const void* k, const void* v, int32_t dtype, int64_t n
 cudaError_t launch_read(void* k, void* v, int32_t dtype, int64_t n_tokens, int32_t head_dim,
                         const int64_t* slots, const PagePool& pool, uint32_t* status, cudaStream_t stream);
 
+// Queries and keys of packed tokens, each head row divided by its root mean square and rotated.
+struct NormRopeArgs {
+  const void* x[2];           // q, k: [n_tokens][heads][D], token strides x_stride
+  void* out[2];
+  int64_t x_stride[2];
+  int64_t out_stride[2];
+  const void* weight[2];      // [D] of weight_dtype; null: that tensor is not normalised
+  int64_t n_tokens;
+  int32_t heads[2];           // heads[1] may be 0
+  int32_t weight_dtype;
+  float eps;
+  const int64_t* positions;   // [n_axes][n_tokens]
+  const int32_t* axes;        // [rot / 2] axis of each pair, or null: axis 0
+  const double* inv_freq;     // [rot / 2], radians per position
+  int32_t n_axes;
+  int32_t rot;                // 0: no rotation
+  int32_t interleaved;
+  float mscale;
+  uint32_t* status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int32_t dtype, int32_t head_dim, cudaStream_t stream);
+
+// Lengths, tables and slots of a step.
+struct ExtendArgs {
+  const int32_t* new_lens;    // [batch]
+  const int32_t* kv_lens;     // [batch] keys before the step
+  int32_t* table;             // [batch][table_stride]
+  const int32_t* free_pages;  // [free_capacity], the next page last
+  const int32_t* n_free;      // [1]
+  int32_t* kv_out;            // [batch], may be kv_lens
+  int32_t* cu_q;              // [batch + 1]
+  int64_t* slots;             // [total_q]
+  int64_t* positions;         // [total_q]
+  int32_t* n_free_out;        // [1], may be n_free
+  int64_t batch;
+  int64_t table_stride;
+  int64_t free_capacity;
+  int64_t total_q;
+  int32_t page_shift;
+  uint32_t* status;
+};
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream);
+
 // Most keys of a sequence: lengths are int32, and a tile's end must not pass 2^31.
 constexpr int64_t kMaxKeys = 0x7FFF0000;
 

@@ -1,0 +1,246 @@
+// paged_step.cu -- what a step of a server does around its attention: lengths, block tables and slots of its new
+// tokens, and the norms of its queries and keys with their rotary positions.
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "paged.h"
+#include "paged_seq.cuh"
+#include "ptx.cuh"
+#include "rotary.cuh"
+
+namespace q8a {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+// ---------------------------------------------------------------- extend --
+//
+// Sequence b gets new_lens[b] tokens behind its kv_lens[b] keys.  With P tokens a page it needs
+//   ceil((kv + n) / P) - ceil(kv / P)
+// more pages; the sums of the rows and of the pages before b (two exclusive scans) say where its rows start
+// and which of the free pages are its own, so nothing depends on the order in which blocks run.  A new page's first
+// row is a new token's, and that token's thread writes the page's number into the table.
+//
+// A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no
+// block waits for another's results; the blocks of one cluster only have to have read what the call may
+// overwrite in place (kv_lens, n_free) before block 0 does so.
+
+constexpr int kExtThreads = 1024;
+
+template <int kBlocks>
+__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtendArgs a) {
+  __shared__ int64_t sums[2][32];
+  __shared__ int32_t row0[kExtThreads], kv0[kExtThreads], page0[kExtThreads];
+  __shared__ int32_t taken;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int rank = kBlocks > 1 ? blockIdx.x : 0;
+  const int64_t page = int64_t{1} << a.page_shift;
+  const int64_t most = i64min(a.table_stride << a.page_shift, kMaxKeys);
+  const int64_t n_raw = a.n_free[0];
+  const int64_t n_free = i64max(0, i64min(n_raw, a.free_capacity));
+  bool wrong = n_raw != n_free;
+  int64_t rows = 0, pages = 0;   // of the sequences before this round's
+  if (tid == 0) taken = 0;
+  if (rank == 0 && tid == 0) a.cu_q[0] = 0;
+  for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
+    const int64_t b = b0 + tid;
+    const bool have = b < a.batch;
+    const int64_t n_in = have ? a.new_lens[b] : 0, kv = have ? a.kv_lens[b] : 0;
+    const int64_t n = i64max(n_in, 0);
+    const bool valid = n_in >= 0 && kv >= 0 && kv + n <= most;
+    const int64_t had = (kv + page - 1) >> a.page_shift;
+    const int64_t need = valid ? ((kv + n + page - 1) >> a.page_shift) - had : 0;
+    int64_t r = n, p = need;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(kFull, r, o), w = __shfl_up_sync(kFull, p, o);
+      if (lane >= o) {
+        r += v;
+        p += w;
+      }
+    }
+    if (lane == 31) {
+      sums[0][warp] = r;
+      sums[1][warp] = p;
+    }
+    __syncthreads();
+    int64_t all_r = rows, all_p = pages;
+    r += rows;
+    p += pages;
+    for (int w = 0; w < warps; ++w) {
+      const int64_t x = sums[0][w], y = sums[1][w];
+      if (w < warp) {
+        r += x;
+        p += y;
+      }
+      all_r += x;
+      all_p += y;
+    }
+    const bool granted = valid && (need == 0 || p <= n_free) && (n == 0 || r <= a.total_q);
+    if (have && !granted) wrong = true;
+    if (have && granted && need > 0) atomicMax(&taken, static_cast<int32_t>(p));   // the granted ones come first
+    const int64_t start = i64min(r - n, a.total_q);
+    row0[tid] = static_cast<int32_t>(have ? start : a.total_q);
+    kv0[tid] = granted ? static_cast<int32_t>(kv) : -1;
+    page0[tid] = static_cast<int32_t>(p - need - had);   // page i of the sequence is the free one page0 + i
+    if (rank == 0 && have) a.cu_q[b + 1] = static_cast<int32_t>(i64min(r, a.total_q));
+    // every block has read this round's lengths, and n_free
+    if (kBlocks > 1)
+      cooperative_groups::this_cluster().sync();
+    else
+      __syncthreads();
+    if (rank == 0 && have) a.kv_out[b] = static_cast<int32_t>(granted ? kv + n : kv);
+    const int64_t end = i64min(all_r, a.total_q);
+    for (int64_t t = i64min(rows, a.total_q) + rank * blockDim.x + tid; t < end; t += kBlocks * blockDim.x) {
+      int lo = 0;   // the last sequence that starts at or before t: of those that start there, the one with rows
+      for (int step = kExtThreads / 2; step > 0; step /= 2)
+        if (lo + step < static_cast<int>(blockDim.x) && row0[lo + step] <= t) lo += step;
+      int64_t slot = -1, pos = 0;
+      if (kv0[lo] >= 0) {
+        pos = kv0[lo] + (t - row0[lo]);
+        const int64_t i = pos >> a.page_shift, off = pos & (page - 1);
+        int32_t* entry = a.table + (b0 + lo) * a.table_stride + i;
+        int32_t at;
+        if (i >= (kv0[lo] + page - 1) >> a.page_shift) {
+          at = a.free_pages[n_free - 1 - (page0[lo] + i)];
+          if (off == 0) *entry = at;
+        } else {
+          at = *entry;
+        }
+        if (at >= 0)
+          slot = (static_cast<int64_t>(at) << a.page_shift) + off;
+        else
+          wrong = true;
+      }
+      a.slots[t] = slot;
+      a.positions[t] = pos;
+    }
+    rows = all_r;
+    pages = all_p;
+    __syncthreads();   // the tables of this round are used no more
+  }
+  if (a.batch == 0) {
+    if (kBlocks > 1)
+      cooperative_groups::this_cluster().sync();
+    else
+      __syncthreads();
+  }
+  for (int64_t t = i64min(rows, a.total_q) + rank * blockDim.x + tid; t < a.total_q; t += kBlocks * blockDim.x) {
+    a.slots[t] = -1;
+    a.positions[t] = 0;
+  }
+  if (rank == 0 && tid == 0) a.n_free_out[0] = static_cast<int32_t>(n_free - taken);
+  if (wrong) record_index(a.status);
+}
+
+// ------------------------------------------------------------- norm, rope --
+//
+// A head row x of D channels becomes
+//   y = x / sqrt(mean(x^2) + eps) * w,   then its channel pairs (a, b) -> (a cos t - b sin t, a sin t + b cos t),
+// t = position * f, the position that of the pair's axis; everything in fp32, rounded once.
+
+// A warp per token and run of heads, pairs (lane, lane + 32) of each row: any rotated width, any alignment.
+template <typename T, int kD>
+__global__ void __launch_bounds__(256) norm_rope_any_kernel(const NormRopeArgs a, int32_t heads_per_warp) {
+  constexpr int kP = kD / 64;   // pairs of a lane
+  __shared__ float weight[2][kD];
+  __shared__ uint64_t steps[kD / 2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pairs = a.rot / 2;
+  for (int i = threadIdx.x; i < 2 * kD; i += blockDim.x) {
+    const void* w = a.weight[i / kD];
+    const int c = i % kD;
+    weight[i / kD][c] = !w ? 1.0f
+                        : a.weight_dtype == kF16  ? __half2float(static_cast<const __half*>(w)[c])
+                        : a.weight_dtype == kBF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c])
+                                                  : static_cast<const float*>(w)[c];
+  }
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) steps[i] = turn_step(a.inv_freq[i]);
+  __syncthreads();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + warp;
+  if (t >= a.n_tokens) return;
+  float2 cs[kP];
+  int c0[kP], c1[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int p = lane + 32 * i;
+    cs[i] = make_float2(1.0f, 0.0f);
+    c0[i] = 2 * p;
+    c1[i] = 2 * p + 1;
+    if (p < pairs) {
+      int axis = a.axes ? a.axes[p] : 0;
+      if (axis < 0 || axis >= a.n_axes) {
+        record_index(a.status);
+        axis = 0;
+      }
+      cs[i] = rotation(a.positions[axis * a.n_tokens + t], steps[p], a.mscale, 1.0f);
+      if (!a.interleaved) {
+        c0[i] = p;
+        c1[i] = p + pairs;
+      }
+    }
+  }
+  const int h0 = blockIdx.y * heads_per_warp, h1 = min(a.heads[0] + a.heads[1], h0 + heads_per_warp);
+  for (int h = h0; h < h1; ++h) {
+    const int which = h >= a.heads[0];
+    const int head = which ? h - a.heads[0] : h;
+    const T* x = static_cast<const T*>(a.x[which]) + t * a.x_stride[which] + static_cast<int64_t>(head) * kD;
+    T* y = static_cast<T*>(a.out[which]) + t * a.out_stride[which] + static_cast<int64_t>(head) * kD;
+    float u[kP], v[kP], ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      u[i] = Elem<T>::get(x[c0[i]]);
+      v[i] = Elem<T>::get(x[c1[i]]);
+      ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) ss += __shfl_xor_sync(kFull, ss, o);
+    const float r = a.weight[which] ? rsqrtf(fmaf(ss, 1.0f / kD, a.eps)) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const float p = u[i] * r * weight[which][c0[i]], q = v[i] * r * weight[which][c1[i]];
+      const float2 z = turn_pair(p, q, cs[i]);
+      const bool turns = lane + 32 * i < pairs;   // the other channels keep their value, whatever it is
+      y[c0[i]] = Elem<T>::put(turns ? z.x : p);
+      y[c1[i]] = Elem<T>::put(turns ? z.y : q);
+    }
+  }
+}
+
+template <typename T, int kD>
+cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
+  const int heads = a.heads[0] + a.heads[1];
+  constexpr int64_t kFill = 152 * 64;   // warps
+  int hpw = 16;
+  while (hpw > 1 && a.n_tokens * ((heads + hpw - 1) / hpw) < kFill) hpw /= 2;
+  const int64_t blocks = (a.n_tokens + 7) / 8, groups = (heads + hpw - 1) / hpw;
+  if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
+  return launch_kernel(norm_rope_any_kernel<T, kD>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)),
+                       dim3(256), 0, stream, a, static_cast<int32_t>(hpw));
+}
+template <typename T>
+cudaError_t launch_norm_rope_t(const NormRopeArgs& a, int32_t head_dim, cudaStream_t stream) {
+  return head_dim == 64 ? launch_norm_rope_d<T, 64>(a, stream) : launch_norm_rope_d<T, 128>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
+  if (a.total_q <= 4096) return launch_kernel(extend_kernel<1>, dim3(1), dim3(kExtThreads), 0, stream, a);
+  return launch_kernel(extend_kernel<8>, dim3(8), dim3(kExtThreads), 0, stream, a);
+}
+
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int32_t dtype, int32_t head_dim, cudaStream_t stream) {
+  if (dtype == kF16) return launch_norm_rope_t<__half>(a, head_dim, stream);
+  if (dtype == kBF16) return launch_norm_rope_t<__nv_bfloat16>(a, head_dim, stream);
+  return launch_norm_rope_t<float>(a, head_dim, stream);
+}
+
+}  // namespace q8a

@@ -69,6 +69,9 @@ SIGNATURES = {
     "attn_paged": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
                                   _P, _P, _I64, _I64, _I64, _F, _I32, _P, _P, _I64, _P]),
     "q8a_paged_workspace_floats": (_I64, [_I64, _I64, _I32, _I32, _I64, _I64, _I32]),
+    "q8kv_extend_paged": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P]),
+    "attn_norm_rope": (ctypes.c_int, [_P, _P, _I32, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32, _I64, _I32, _P, _P,
+                                      _I32, _F, _P, _I32, _P, _P, _I32, _I32, _F, _P]),
     "q8a_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_U32), _I32]),
     "q8a_status": (ctypes.c_int, [_P]),
     "q8a_set_wait_timeout_ns": (ctypes.c_int, [_U64]),
@@ -616,6 +619,111 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
           max_kv, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
           ws, floats)
     return out
+
+
+def _table(name, t, device):
+    """Check a block table [batch, width]; its address and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous() and
+            t.get_device() == device):
+        _refuse(f"{name}: a contiguous int32 tensor [batch, width] on cuda:{device} is needed")
+    return t.data_ptr(), *t.shape
+
+
+def q8kv_extend_paged(new_lens, kv_lens, block_table, free_pages, n_free, page_tokens, total_q, out=None):
+    """A step's lengths, tables and slots: sequence b goes on by new_lens[b] tokens (int32 [B]) behind its kv_lens[b]
+    keys; the pages that it lacks come from the free ones (int32 free_pages, a stack of n_free[0] numbers) into its
+    row of block_table (int32 [B, width], written in place).  Returns (kv_lens, cu_q, slots, positions, n_free): the new
+    lengths, int32 [B + 1] first rows, int64 [total_q] slots and positions of the packed tokens (-1 and 0 behind the
+    last sequence), and int32 [1] pages left.  `out`: those five tensors to write into, of which the first and the
+    last may be kv_lens and n_free themselves."""
+    device = _device_of(new_lens)
+    B = new_lens.shape[0] if new_lens.dim() == 1 else -1
+    new = _index("new_lens", new_lens, torch.int32, B, device)
+    lens = _index("kv_lens", kv_lens, torch.int32, B, device)
+    table, rows, width = _table("block_table", block_table, device)
+    if rows != B:
+        _refuse(f"block_table has {rows} rows for {B} sequences")
+    capacity = free_pages.shape[0] if isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1 else -1
+    free = _index("free_pages", free_pages, torch.int32, capacity, device)
+    top = _index("n_free", n_free, torch.int32, 1, device)
+    if total_q < 0:
+        _refuse(f"total_q must not be negative (got {total_q})")
+    if out is None:
+        like = dict(device=new_lens.device)
+        ints = torch.empty(2 * B + 2, dtype=torch.int32, **like)
+        longs = torch.empty(2 * total_q, dtype=torch.int64, **like)
+        out = ints[:B], ints[B:2 * B + 1], longs[:total_q], longs[total_q:], ints[2 * B + 1:]
+    kv, cu, slots, pos, left = out
+    _call(load().q8kv_extend_paged, device, new, lens, B, table, width, free, capacity, top, page_tokens, total_q,
+          _index("out[0]", kv, torch.int32, B, device), _index("out[1]", cu, torch.int32, B + 1, device),
+          _index("out[2]", slots, torch.int64, total_q, device), _index("out[3]", pos, torch.int64, total_q, device),
+          _index("out[4]", left, torch.int32, 1, device))
+    return out
+
+
+def rope_axes(sections, device=None):
+    """int32 [sum(sections)]: the axis of each channel pair for attn_norm_rope, the first sections[0] pairs axis 0,
+    the next sections[1] axis 1, and so on."""
+    axes = torch.repeat_interleave(torch.arange(len(sections), dtype=torch.int32), torch.tensor(sections))
+    return axes.to(device) if device is not None else axes
+
+
+def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, axes=None, eps=1e-6,
+                   interleaved=False, mscale=1.0, out=None):
+    """The norm of every head of packed q [T, H, D] and k [T, H_kv, D] (fp16, bf16 or fp32; slices of a wider buffer
+    are fine; k may be None) and the rotation by its position, in one pass: x / sqrt(mean(x^2) + eps) * weight
+    (weights [D] of one type; None: that tensor is not normalised), then the first 2 * len(inv_freq) channels turned as
+    attn_rope does.  positions: int64 [T], or [A, T] with the axis of each channel pair in axes (int32
+    [len(inv_freq)], see rope_axes); None: no rotation.  `out`: a pair of tensors, which may be q and k.
+    Returns (q, k)."""
+    device = _device_of(q)
+    code, T, H, D, q_stride = _packed("q", q, device)
+    if out is None:
+        out = (torch.empty((T, H, D), dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    q_out, k_out = out
+    out_code, *shape, q_out_stride = _packed("out[0]", q_out, device)
+    if out_code != code or shape != [T, H, D]:
+        _bad_packed(q=q, out=q_out)
+    kv_heads = k_stride = k_out_stride = k_at = k_out_at = 0
+    if k is not None:
+        k_code, k_T, kv_heads, k_D, k_stride = _packed("k", k, device)
+        if k_code != code or (k_T, k_D) != (T, D) or kv_heads == 0:
+            _refuse(f"q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} must agree in tokens, channels and type")
+        out_code, *shape, k_out_stride = _packed("out[1]", k_out, device)
+        if out_code != code or shape != [T, kv_heads, D]:
+            _bad_packed(k=k, out=k_out)
+        k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None or k_weight is not None:
+        _refuse("without k there is neither an output nor a weight of it")
+    weights, w_dtype = [], None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            w_dtype = w_dtype or getattr(w, "dtype", None)
+            if w_dtype not in _DTYPES:
+                _refuse(f"{name}: a tensor of fp16, bf16 or fp32 is needed")
+            weights.append(_index(name, w, w_dtype, D, device))
+        else:
+            weights.append(None)
+    if (positions is None) != (inv_freq is None):
+        _refuse("positions and inv_freq come together")
+    pos = table = axis = None
+    rot = n_axes = 0
+    if positions is not None:
+        table, rot = _rope_table(inv_freq, device)
+        if not (isinstance(positions, torch.Tensor) and positions.dtype == torch.int64 and positions.dim() in (1, 2) and
+                positions.shape[-1] == T and positions.is_contiguous() and positions.get_device() == device):
+            _bad_index("positions", positions, torch.int64, T, device)
+        pos, n_axes = positions.data_ptr(), (positions.shape[0] if positions.dim() == 2 else 1)
+        if axes is not None:
+            axis = _index("axes", axes, torch.int32, rot // 2, device)
+    elif axes is not None:
+        _refuse("axes need positions")
+    _call(load().attn_norm_rope, device, q.data_ptr(), q_out.data_ptr(), H, q_stride, q_out_stride, k_at or None,
+          k_out_at or None, kv_heads, k_stride, k_out_stride, code, T, D, *weights,
+          _DTYPES[w_dtype] if w_dtype is not None else 0, eps, pos, n_axes, axis, table, rot, 1 if interleaved else 0,
+          mscale)
+    return q_out, k_out
 
 
 def device_status(clear=True, stream=None):

@@ -529,6 +529,65 @@ int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads
                                    int64_t max_q, int64_t max_kv, int32_t head_dim);
 
 /*
+ * q8kv_extend_paged -- the lengths, block tables, slots and positions of a step, on the
+ * device, from the number of new tokens of each sequence: sequence b goes on from
+ * kv_lens[b] keys to kv_lens[b] + new_lens[b], its new tokens are the packed rows
+ * cu_q[b] .. cu_q[b + 1] - 1, token i of them at position kv_lens[b] + i, and the pages that
+ * it lacks, ceil((kv + new) / page_tokens) - ceil(kv / page_tokens), are the next ones of the
+ * free pages, dealt to the sequences in order (their numbers go into its row of the table).
+ * What comes out is what q8kv_append_paged and attn_paged take.
+ *   new_lens, kv_lens  int32 [batch]; 0 new tokens are allowed.
+ *   block_table        int32 [batch][table_stride]; only the entries of new pages are written.
+ *   free_pages         int32 [free_capacity], a stack: n_free[0] page numbers, the next one last;
+ *                      it is not written.  n_free: int32 [1].
+ *   total_q            rows of the packed tensors: at least the sum of new_lens; those
+ *                      behind the last sequence get slot -1 and position 0 (padding).
+ *   kv_lens_out        int32 [batch], may be kv_lens.  n_free_out: int32 [1], may be n_free.
+ *   cu_q               int32 [batch + 1].  slots, positions: int64 [total_q].
+ * A sequence whose pages are more than are left, that passes its table's row or total_q,
+ * or whose lengths are negative is left as it was: its kv_lens stays, its tokens get slot
+ * -1 and position 0 (cu_q counts their rows, up to total_q), and the failure is recorded as an
+ * index out of range.  Sequences that need no page are served all the same.  A page number
+ * below 0 in the free list or in an entry that is read is recorded too, its tokens get slot -1.
+ * Nothing that is written shares a byte with the other arrays, but for the two that may be in place.
+ * Errors: Q8A_ERR_INVALID_ARG, Q8A_ERR_MISALIGNED, Q8A_ERR_CUDA.
+ */
+int q8kv_extend_paged(const int32_t *new_lens, const int32_t *kv_lens, int64_t batch,
+                      int32_t *block_table, int64_t table_stride, const int32_t *free_pages,
+                      int64_t free_capacity, const int32_t *n_free, int32_t page_tokens,
+                      int64_t total_q, int32_t *kv_lens_out, int32_t *cu_q, int64_t *slots,
+                      int64_t *positions, int32_t *n_free_out, void *stream);
+
+/*
+ * attn_norm_rope -- the norm of every query and key head and the rotation by its position, in
+ * one pass over both: a head row x of D channels becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * and of y the channel pairs of the first rot_dim channels are turned as attn_rope does, pair
+ * i by positions[axes[i]][t] * inv_freq[i]: with several axes (time, height, width) each pair
+ * takes the position of its own.
+ *   q, q_out     [n_tokens][heads][D] of dtype (Q8A_F16, Q8A_BF16, Q8A_F32) with the given token
+ *                strides; k, k_out [n_tokens][kv_heads][D], kv_heads 0: none.  An output may be
+ *                its input (same stride); otherwise no output shares a byte with an input or
+ *                the other output (slices of one buffer are fine).
+ *   q_weight, k_weight  [D] of weight_dtype on the device, or NULL: that tensor is not normalised.
+ *   eps          finite, not negative.
+ *   positions    int64 [n_axes][n_tokens] on the device, any value; with inv_freq NULL: no rotation.
+ *   axes         int32 [rot_dim/2] on the device, 0..n_axes-1 (an axis out of range is recorded, and
+ *                taken for 0); NULL with one axis.
+ *   inv_freq, rot_dim, layout, mscale   as for attn_rope.
+ * Numerics: fp32, rounded once to the type; the angles are those of attn_rope.  The sum of the
+ * squares is fp32 too: a row with values beyond 2^60 gives 0 where the formula does not.
+ * Errors: as attn_rope.
+ */
+int attn_norm_rope(const void *q, void *q_out, int32_t heads, int64_t q_token_stride,
+                   int64_t q_out_token_stride, const void *k, void *k_out, int32_t kv_heads,
+                   int64_t k_token_stride, int64_t k_out_token_stride, int32_t dtype,
+                   int64_t n_tokens, int32_t head_dim, const void *q_weight, const void *k_weight,
+                   int32_t weight_dtype, float eps, const int64_t *positions, int32_t n_axes,
+                   const int32_t *axes, const double *inv_freq, int32_t rot_dim, int32_t layout,
+                   float mscale, void *stream);
+
+/*
  * q8a_device_status -- read (and optionally clear) what the kernels of the current
  * device have recorded: 0 when no device-side wait has run out and no paged call has
  * met an index out of range since the last clear.  Synchronises `stream`; kernels of
