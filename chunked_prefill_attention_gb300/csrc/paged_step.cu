@@ -214,9 +214,236 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const NormRopeArgs a
   }
 }
 
+// Eight halves or four floats of one 16-byte access as floats, and back (one rounding).
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float* f);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& v, float* f) {
+  f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<__half>(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+  }
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float* f);
+template <>
+__device__ __forceinline__ uint4 pack<float>(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack<__half>(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same with 16-byte accesses: a head row is 2 L vectors of N elements, L lanes each take two.  Of the turned
+// channels in halves a lane's vectors are each other's partners; in interleaved pairs every vector holds whole ones.
+// A thread keeps to one token, its two vectors and the heads of one tensor (a block's), so its angles are formed
+// once, and with them the weights: a pair becomes r (a A - b B), r (a C + b E), r the row's factor, with
+//   A = w_a cos t, B = w_b sin t, C = w_a sin t, E = w_b cos t
+// in registers.
+template <typename T, int kD, bool kInter>
+__global__ void __launch_bounds__(256, 3)
+norm_rope_kernel(const NormRopeArgs a, int32_t heads_per_thread, int32_t q_groups) {
+  constexpr int N = 16 / sizeof(T), L = kD / (2 * N);
+  constexpr int kU = 2;   // heads in flight
+  __shared__ uint64_t steps[kD / 2];
+  __shared__ int32_t axis_of[kD / 2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x % L;
+  const int pairs = a.rot / 2;
+  const int which = static_cast<int>(blockIdx.y) >= q_groups;
+  const int h0 = (blockIdx.y - (which ? q_groups : 0)) * heads_per_thread;
+  const int n = min(a.heads[which] - h0, heads_per_thread);
+  const int64_t t_own = static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L;
+  const bool live = t_own < a.n_tokens;
+  const int64_t t = live ? t_own : a.n_tokens - 1;   // the lanes behind the last token read it too, and write nothing
+  int c0, c1;
+  bool turn0, turn1;
+  if (kInter) {
+    c0 = N * lane;
+    c1 = kD / 2 + N * lane;
+    turn0 = c0 < a.rot;
+    turn1 = c1 < a.rot;
+  } else {
+    const int turning = pairs / N;
+    turn0 = turn1 = lane < turning;
+    c0 = turn0 ? N * lane : a.rot + N * (lane - turning);
+    c1 = c0 + (turn0 ? pairs : (kD - a.rot) / 2);
+  }
+  const T* x = static_cast<const T*>(a.x[which]) + t * a.x_stride[which] + static_cast<int64_t>(h0) * kD;
+  T* y = static_cast<T*>(a.out[which]) + t * a.out_stride[which] + static_cast<int64_t>(h0) * kD;
+  uint4 x0[kU], x1[kU];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (h + u < n) {
+        x0[u] = *reinterpret_cast<const uint4*>(x + u * kD + c0);
+        x1[u] = *reinterpret_cast<const uint4*>(x + u * kD + c1);
+      }
+    x += kU * kD;
+  };
+  load(0);
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    steps[i] = turn_step(a.inv_freq[i]);
+    int axis = a.axes ? a.axes[i] : 0;
+    if (axis < 0 || axis >= a.n_axes) {
+      record_index(a.status);
+      axis = 0;
+    }
+    axis_of[i] = axis;
+  }
+  __syncthreads();
+  const void* weight = a.weight[which];
+  float wa[N], wb[N];   // of the two vectors; A and E of the pairs in their place later
+  float B[N], C[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    auto get = [&](int c) {
+      return !weight                     ? 1.0f
+             : a.weight_dtype == kF16    ? __half2float(static_cast<const __half*>(weight)[c])
+             : a.weight_dtype == kBF16   ? __bfloat162float(static_cast<const __nv_bfloat16*>(weight)[c])
+                                         : static_cast<const float*>(weight)[c];
+    };
+    wa[e] = get(c0 + e);
+    wb[e] = get(c1 + e);
+    B[e] = C[e] = 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    // pair e: (first vector, second vector) at e; interleaved: 2 e and 2 e + 1 of the first vector, then of the second
+    const bool turns = kInter && e >= N / 2 ? turn1 : turn0;
+    const int p = kInter ? (e < N / 2 ? c0 / 2 + e : c1 / 2 + e - N / 2) : c0 + e;
+    if (turns) {
+      const float2 cs = rotation(a.positions[axis_of[p] * a.n_tokens + t], steps[p], a.mscale, 1.0f);
+      float& fa = kInter ? (e < N / 2 ? wa[2 * e] : wb[2 * e - N]) : wa[e];
+      float& fb = kInter ? (e < N / 2 ? wa[2 * e + 1] : wb[2 * e + 1 - N]) : wb[e];
+      B[e] = fb * cs.y;
+      C[e] = fa * cs.y;
+      fa *= cs.x;
+      fb *= cs.x;
+    }
+  }
+  for (int h = 0; h < n; h += kU) {
+    uint4 y0[kU], y1[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      y0[u] = x0[u];
+      y1[u] = x1[u];
+    }
+    load(h + kU);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (h + u >= n) break;   // uniform
+      float p[N], q[N];
+      unpack<T>(y0[u], p);
+      unpack<T>(y1[u], q);
+      if (weight) {   // uniform
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          s0 = fmaf(p[e], p[e], s0);
+          s1 = fmaf(q[e], q[e], s1);
+        }
+        s0 += s1;
+#pragma unroll
+        for (int o = 1; o < L; o *= 2) s0 += __shfl_xor_sync(kFull, s0, o);
+        const float r = rsqrtf(fmaf(s0, 1.0f / kD, a.eps));
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          p[e] *= r;
+          q[e] *= r;
+        }
+      }
+      if (kInter) {
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+          const float a0 = p[2 * e], b0 = p[2 * e + 1], a1 = q[2 * e], b1 = q[2 * e + 1];
+          p[2 * e] = a0 * wa[2 * e];
+          p[2 * e + 1] = b0 * wa[2 * e + 1];
+          q[2 * e] = a1 * wb[2 * e];
+          q[2 * e + 1] = b1 * wb[2 * e + 1];
+          if (turn0) {   // a channel that is not turned takes nothing from its neighbour, not even 0 times infinity
+            p[2 * e] = fmaf(a0, wa[2 * e], -b0 * B[e]);
+            p[2 * e + 1] = fmaf(a0, C[e], p[2 * e + 1]);
+          }
+          if (turn1) {
+            q[2 * e] = fmaf(a1, wb[2 * e], -b1 * B[N / 2 + e]);
+            q[2 * e + 1] = fmaf(a1, C[N / 2 + e], q[2 * e + 1]);
+          }
+        }
+      } else if (turn0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float a0 = p[e], b0 = q[e];
+          p[e] = fmaf(a0, wa[e], -b0 * B[e]);
+          q[e] = fmaf(a0, C[e], b0 * wb[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          p[e] *= wa[e];
+          q[e] *= wb[e];
+        }
+      }
+      if (live) {
+        *reinterpret_cast<uint4*>(y + u * kD + c0) = pack<T>(p);
+        *reinterpret_cast<uint4*>(y + u * kD + c1) = pack<T>(q);
+      }
+    }
+    y += kU * kD;
+  }
+}
+
 template <typename T, int kD>
 cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
   const int heads = a.heads[0] + a.heads[1];
+  // 16-byte accesses where a vector lies in one half of the turned channels and every row starts 16-byte aligned
+  constexpr int N = 16 / sizeof(T), L = kD / (2 * N);
+  bool wide = a.rot % (2 * N) == 0;
+  for (int i = 0; i < (a.heads[1] ? 2 : 1); ++i)
+    wide = wide && (a.x_stride[i] | a.out_stride[i]) % N == 0 &&
+           (reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i])) % 16 == 0;
+  if (wide) {
+    // as many heads a thread as leave every SM its threads
+    constexpr int64_t kThreads = 152 * 1024;
+    auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
+    int hpt = 1;
+    while (hpt < 16 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads) hpt *= 2;
+    const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L), groups = groups_of(hpt);
+    if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
+    return launch_kernel(a.interleaved ? norm_rope_kernel<T, kD, true> : norm_rope_kernel<T, kD, false>,
+                         dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(256), 0, stream, a,
+                         static_cast<int32_t>(hpt), static_cast<int32_t>((a.heads[0] + hpt - 1) / hpt));
+  }
   constexpr int64_t kFill = 152 * 64;   // warps
   int hpw = 16;
   while (hpw > 1 && a.n_tokens * ((heads + hpw - 1) / hpw) < kFill) hpw /= 2;
