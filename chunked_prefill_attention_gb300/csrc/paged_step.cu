@@ -1,7 +1,6 @@
 // paged_step.cu -- what a step of a server does around its attention: lengths, block tables and slots of its new
 // tokens, and the norms of its queries and keys with their rotary positions.
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,29 +23,32 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // and which of the free pages are its own, so nothing depends on the order in which blocks run.  A new page's first
 // row is a new token's, and that token's thread writes the page's number into the table.
 //
-// A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no
-// block waits for another's results; the blocks of one cluster only have to have read what the call may
-// overwrite in place (kv_lens, n_free) before block 0 does so.
+// A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no block waits
+// for another's results.  A step of few tokens is one block's.  Many tokens are dealt to blocks that write what
+// belongs to the tokens (kTokens); a second launch then writes the lengths and the number of free
+// pages (kLens), which may lie in the place of those that the first one reads.
 
 constexpr int kExtThreads = 1024;
+enum : int { kWhole, kTokens, kLens };
 
-template <int kBlocks>
-__global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtendArgs a) {
+template <int kPart>
+__global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtendArgs a) {
   __shared__ int64_t sums[2][32];
   __shared__ int32_t row0[kExtThreads], kv0[kExtThreads], page0[kExtThreads];
   __shared__ int32_t taken;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int rank = kBlocks > 1 ? blockIdx.x : 0;
+  const bool lead = blockIdx.x == 0;
   const int64_t page = int64_t{1} << a.page_shift;
   const int64_t most = i64min(a.table_stride << a.page_shift, kMaxKeys);
   const int64_t n_raw = a.n_free[0];
   const int64_t n_free = i64max(0, i64min(n_raw, a.free_capacity));
   bool wrong = n_raw != n_free;
   int64_t rows = 0, pages = 0;   // of the sequences before this round's
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   if (tid == 0) taken = 0;
-  if (rank == 0 && tid == 0) a.cu_q[0] = 0;
+  if (kPart != kLens && lead && tid == 0) a.cu_q[0] = 0;
   for (int64_t b0 = 0; b0 < a.batch; b0 += blockDim.x) {
     const int64_t b = b0 + tid;
     const bool have = b < a.batch;
@@ -88,18 +90,16 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kExtThreads, 1
     row0[tid] = static_cast<int32_t>(have ? start : a.total_q);
     kv0[tid] = granted ? static_cast<int32_t>(kv) : -1;
     page0[tid] = static_cast<int32_t>(p - need - had);   // page i of the sequence is the free one page0 + i
-    if (rank == 0 && have) a.cu_q[b + 1] = static_cast<int32_t>(i64min(r, a.total_q));
-    // every block has read this round's lengths, and n_free
-    if (kBlocks > 1)
-      cooperative_groups::this_cluster().sync();
-    else
-      __syncthreads();
-    if (rank == 0 && have) a.kv_out[b] = static_cast<int32_t>(granted ? kv + n : kv);
+    if (kPart != kLens && lead && have) a.cu_q[b + 1] = static_cast<int32_t>(i64min(r, a.total_q));
+    __syncthreads();
+    if (kPart != kTokens && have) a.kv_out[b] = static_cast<int32_t>(granted ? kv + n : kv);
     const int64_t end = i64min(all_r, a.total_q);
-    for (int64_t t = i64min(rows, a.total_q) + rank * blockDim.x + tid; t < end; t += kBlocks * blockDim.x) {
+    int half = 1;   // of the search: the sequences of this round are at most 2 * half
+    while (2 * half < i64min(a.batch - b0, blockDim.x)) half *= 2;
+    for (int64_t t = i64min(rows, a.total_q) + first; kPart != kLens && t < end; t += stride) {
       int lo = 0;   // the last sequence that starts at or before t: of those that start there, the one with rows
-      for (int step = kExtThreads / 2; step > 0; step /= 2)
-        if (lo + step < static_cast<int>(blockDim.x) && row0[lo + step] <= t) lo += step;
+      for (int step = half; step > 0; step /= 2)
+        if (row0[lo + step] <= t) lo += step;
       int64_t slot = -1, pos = 0;
       if (kv0[lo] >= 0) {
         pos = kv0[lo] + (t - row0[lo]);
@@ -124,17 +124,12 @@ __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kExtThreads, 1
     pages = all_p;
     __syncthreads();   // the tables of this round are used no more
   }
-  if (a.batch == 0) {
-    if (kBlocks > 1)
-      cooperative_groups::this_cluster().sync();
-    else
-      __syncthreads();
-  }
-  for (int64_t t = i64min(rows, a.total_q) + rank * blockDim.x + tid; t < a.total_q; t += kBlocks * blockDim.x) {
+  for (int64_t t = i64min(rows, a.total_q) + first; kPart != kLens && t < a.total_q; t += stride) {
     a.slots[t] = -1;
     a.positions[t] = 0;
   }
-  if (rank == 0 && tid == 0) a.n_free_out[0] = static_cast<int32_t>(n_free - taken);
+  if (a.batch == 0) __syncthreads();
+  if (kPart != kTokens && tid == 0) a.n_free_out[0] = static_cast<int32_t>(n_free - taken);
   if (wrong) record_index(a.status);
 }
 
@@ -270,10 +265,10 @@ __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float* f) {
 //   A = w_a cos t, B = w_b sin t, C = w_a sin t, E = w_b cos t
 // in registers.
 template <typename T, int kD, bool kInter>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, 2)
 norm_rope_kernel(const NormRopeArgs a, int32_t heads_per_thread, int32_t q_groups) {
   constexpr int N = 16 / sizeof(T), L = kD / (2 * N);
-  constexpr int kU = 2;   // heads in flight
+  constexpr int kU = 4;   // heads in flight
   __shared__ uint64_t steps[kD / 2];
   __shared__ int32_t axis_of[kD / 2];
   pdl_launch_dependents();
@@ -434,7 +429,7 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
            (reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i])) % 16 == 0;
   if (wide) {
     // as many heads a thread as leave every SM its threads
-    constexpr int64_t kThreads = 152 * 1024;
+    constexpr int64_t kThreads = 152 * 512;
     auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
     int hpt = 1;
     while (hpt < 16 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads) hpt *= 2;
@@ -460,8 +455,11 @@ cudaError_t launch_norm_rope_t(const NormRopeArgs& a, int32_t head_dim, cudaStre
 }  // namespace
 
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
-  if (a.total_q <= 4096) return launch_kernel(extend_kernel<1>, dim3(1), dim3(kExtThreads), 0, stream, a);
-  return launch_kernel(extend_kernel<8>, dim3(8), dim3(kExtThreads), 0, stream, a);
+  if (a.total_q <= 4096)
+    return launch_kernel(extend_kernel<kWhole>, dim3(1), dim3(a.batch <= 256 && a.total_q <= 1024 ? 256 : kExtThreads), 0, stream, a);
+  const int64_t most = (a.total_q + kExtThreads - 1) / kExtThreads, blocks = most < 152 ? most : 152;
+  const cudaError_t e = launch_kernel(extend_kernel<kTokens>, dim3(static_cast<unsigned>(blocks)), dim3(kExtThreads), 0, stream, a);
+  return e != cudaSuccess ? e : launch_kernel(extend_kernel<kLens>, dim3(1), dim3(kExtThreads), 0, stream, a);
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int32_t dtype, int32_t head_dim, cudaStream_t stream) {

@@ -649,15 +649,18 @@ def q8kv_extend_paged(new_lens, kv_lens, block_table, free_pages, n_free, page_t
     if total_q < 0:
         _refuse(f"total_q must not be negative (got {total_q})")
     if out is None:
-        like = dict(device=new_lens.device)
-        ints = torch.empty(2 * B + 2, dtype=torch.int32, **like)
-        longs = torch.empty(2 * total_q, dtype=torch.int64, **like)
-        out = ints[:B], ints[B:2 * B + 1], longs[:total_q], longs[total_q:], ints[2 * B + 1:]
-    kv, cu, slots, pos, left = out
-    _call(load().q8kv_extend_paged, device, new, lens, B, table, width, free, capacity, top, page_tokens, total_q,
-          _index("out[0]", kv, torch.int32, B, device), _index("out[1]", cu, torch.int32, B + 1, device),
-          _index("out[2]", slots, torch.int64, total_q, device), _index("out[3]", pos, torch.int64, total_q, device),
-          _index("out[4]", left, torch.int32, 1, device))
+        # five small tensors: 7 us, where views of two buffers take 14
+        ints, longs = dict(dtype=torch.int32, device=new_lens.device), dict(dtype=torch.int64, device=new_lens.device)
+        kv, cu, left = torch.empty(B, **ints), torch.empty(B + 1, **ints), torch.empty(1, **ints)
+        slots, pos = torch.empty(total_q, **longs), torch.empty(total_q, **longs)
+        ptrs = kv.data_ptr(), cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), left.data_ptr()
+        out = kv, cu, slots, pos, left
+    else:
+        kv, cu, slots, pos, left = out
+        ptrs = (_index("out[0]", kv, torch.int32, B, device), _index("out[1]", cu, torch.int32, B + 1, device),
+                _index("out[2]", slots, torch.int64, total_q, device), _index("out[3]", pos, torch.int64, total_q, device),
+                _index("out[4]", left, torch.int32, 1, device))
+    _call(load().q8kv_extend_paged, device, new, lens, B, table, width, free, capacity, top, page_tokens, total_q, *ptrs)
     return out
 
 
@@ -678,33 +681,38 @@ def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=
     Returns (q, k)."""
     device = _device_of(q)
     code, T, H, D, q_stride = _packed("q", q, device)
-    if out is None:
-        out = (torch.empty((T, H, D), dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    q_out, k_out = out
-    out_code, *shape, q_out_stride = _packed("out[0]", q_out, device)
-    if out_code != code or shape != [T, H, D]:
-        _bad_packed(q=q, out=q_out)
     kv_heads = k_stride = k_out_stride = k_at = k_out_at = 0
     if k is not None:
         k_code, k_T, kv_heads, k_D, k_stride = _packed("k", k, device)
-        if k_code != code or (k_T, k_D) != (T, D) or kv_heads == 0:
+        if k_code != code or k_T != T or k_D != D or kv_heads == 0:
             _refuse(f"q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} must agree in tokens, channels and type")
-        out_code, *shape, k_out_stride = _packed("out[1]", k_out, device)
-        if out_code != code or shape != [T, kv_heads, D]:
-            _bad_packed(k=k, out=k_out)
-        k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
-    elif k_out is not None or k_weight is not None:
-        _refuse("without k there is neither an output nor a weight of it")
-    weights, w_dtype = [], None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            w_dtype = w_dtype or getattr(w, "dtype", None)
-            if w_dtype not in _DTYPES:
-                _refuse(f"{name}: a tensor of fp16, bf16 or fp32 is needed")
-            weights.append(_index(name, w, w_dtype, D, device))
-        else:
-            weights.append(None)
+        k_at = k.data_ptr()
+    elif k_weight is not None:
+        _refuse("k_weight without k")
+    if out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        q_out_stride, k_out = max(H * D, 1), None
+        if k is not None:
+            k_out = torch.empty((T, kv_heads, D), dtype=q.dtype, device=q.device)
+            k_out_stride, k_out_at = kv_heads * D, k_out.data_ptr()
+    else:
+        q_out, k_out = out
+        out_code, *shape, q_out_stride = _packed("out[0]", q_out, device)
+        if out_code != code or shape != [T, H, D]:
+            _bad_packed(q=q, out=q_out)
+        if (k is None) != (k_out is None):
+            _refuse("k and its output come together")
+        if k is not None:
+            out_code, *shape, k_out_stride = _packed("out[1]", k_out, device)
+            if out_code != code or shape != [T, kv_heads, D]:
+                _bad_packed(k=k, out=k_out)
+            k_out_at = k_out.data_ptr()
+    w_dtype = getattr(k_weight if q_weight is None else q_weight, "dtype", torch.float32)
+    w_code = _DTYPES.get(w_dtype)
+    if w_code is None:
+        _refuse(f"weights of {w_dtype}: fp16, bf16 or fp32 are needed")
+    wq = None if q_weight is None else _index("q_weight", q_weight, w_dtype, D, device)
+    wk = None if k_weight is None else _index("k_weight", k_weight, w_dtype, D, device)
     if (positions is None) != (inv_freq is None):
         _refuse("positions and inv_freq come together")
     pos = table = axis = None
@@ -720,9 +728,8 @@ def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=
     elif axes is not None:
         _refuse("axes need positions")
     _call(load().attn_norm_rope, device, q.data_ptr(), q_out.data_ptr(), H, q_stride, q_out_stride, k_at or None,
-          k_out_at or None, kv_heads, k_stride, k_out_stride, code, T, D, *weights,
-          _DTYPES[w_dtype] if w_dtype is not None else 0, eps, pos, n_axes, axis, table, rot, 1 if interleaved else 0,
-          mscale)
+          k_out_at or None, kv_heads, k_stride, k_out_stride, code, T, D, wq, wk, w_code, eps, pos, n_axes, axis, table,
+          rot, 1 if interleaved else 0, mscale)
     return q_out, k_out
 
 
