@@ -11,8 +11,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libq8attn.so")
 SOURCES = ["api.cu", "quantize.cu", "state.cu", "chunk_step.cu", "pipeline.cu", "graph.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_tiles.cu", "paged_step_api.cu", "paged_step.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "paged.h", "paged_check.h", "paged_seq.cuh",
+           "paged_api.cu", "paged_cache.cu", "paged_few.cu", "paged_few_range.cu", "paged_tiles.cu", "paged_tiles_window.cu",
+           "paged_tiles_prefix.cu", "paged_step_api.cu", "paged_step.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "paged.h", "paged_check.h", "paged_seq.cuh", "paged_few.cuh", "paged_tiles.cuh",
            "q8_codes.cuh", "rotary.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -127,6 +127,23 @@ struct PagedArgs {
   int64_t ctas;               // tile kernel: its grid
   int32_t wide;               // tile kernel: whose rows start 32-byte aligned (kWide...)
   uint64_t timeout_ns;
+  // kWindow: a row sees the keys of the last `window` positions up to its own, and the first `sinks`
+  int32_t window, sinks;
+  // kOwn, kPrefix: the keys before prefix_len (down to a whole page) are every sequence's
+  const int32_t* prefix_len;  // [1] on the device
+  int64_t prefix_most;        // what it may be at most
+  int32_t seqs;               // kPrefix: sequences of kv_lens and cu_q (batch is 1)
+  float* state;               // [total_q][heads][D] and then [total_q][heads]: outputs over the own keys,
+                              // and the logarithms (base 2) of their sums of weights
+};
+
+// Which keys the rows of a launch see.
+enum : int {
+  kPlain = 0,
+  kWindow = 1,   // window and sinks
+  kOwn = 2,      // those behind the shared prefix; the rows' states go to PagedArgs::state
+  kPrefix = 3    // the shared prefix: all rows of all sequences are one sequence's, whose join takes the
+                 // rows' states over their own keys in and writes `out`
 };
 
 constexpr int32_t kWideQ = 1, kWideOut = 2, kWidePart = 4;
@@ -154,5 +171,17 @@ TilesPlan plan_paged_tiles(int64_t batch, int64_t total_rows, int64_t max_rows, 
                            int32_t head_dim);
 cudaError_t launch_paged_tiles(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
                                cudaStream_t stream);
+// Key tiles that a row unit of a sequence of kv keys can take in a window, at most (`group` query heads a K/V head).
+int64_t window_tiles(int64_t kv, int64_t window, int64_t sinks, int32_t group, bool pair, int32_t head_dim);
+
+// The same launches where rows see other keys than all before them (the tile kernel's kOwn in pairs only).
+cudaError_t launch_paged_few_range(const PagedArgs& a, int mode, int32_t dtype, int32_t head_dim, int64_t rows,
+                                   bool direct, cudaStream_t stream);   // kWindow or kOwn
+cudaError_t launch_paged_tiles_window(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
+                                      cudaStream_t stream);
+cudaError_t launch_paged_tiles_own(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
+                                   cudaStream_t stream);
+cudaError_t launch_paged_tiles_prefix(const PagedArgs& a, int32_t dtype, int32_t head_dim, const TilesPlan& plan,
+                                      cudaStream_t stream);
 
 }  // namespace q8a

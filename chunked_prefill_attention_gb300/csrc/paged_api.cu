@@ -122,6 +122,9 @@ namespace {
 // kernel 257 and 421 (30 and 42), so from 17 rows on the tile kernel takes them.
 constexpr int64_t kFewRows = 16;
 
+// A number of keys, cut to the most that a sequence can have.
+int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; }
+
 // The launches of a call, from its bounds alone.
 struct Plan {
   bool few, direct, tiles;
@@ -130,11 +133,19 @@ struct Plan {
                       // and their partial states, so workspace and launch both take it from here
   int64_t few_floats, floats;
 };
+// `window`, `sinks`: of attn_paged_window, else 0.
 Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, int32_t kv_heads, int64_t max_kv,
-                int32_t head_dim) {
+                int32_t head_dim, int64_t window = 0, int64_t sinks = 0) {
   Plan p{};
   if (max_q > total_q) max_q = total_q;
   if (max_kv > q8a::kMaxKeys) max_kv = q8a::kMaxKeys;
+  int64_t few_kv = max_kv;
+  if (window) {   // the keys that a unit takes, at most
+    const int64_t bn = head_dim == 64 ? 96 : 64;
+    const int64_t most = window + sinks + max_q;
+    if (few_kv > most) few_kv = most;
+    max_kv = q8a::window_tiles(max_kv, window, sinks, static_cast<int32_t>(group), max_q * group <= 128, head_dim) * bn;
+  }
   p.tiles = max_q * group > kFewRows;
   if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
   // The tile kernel takes every sequence of a call of at most 128 rows each (one of few
@@ -147,7 +158,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.direct = q8a::paged_few_direct(batch, kv_heads, max_kv, head_dim);
+  p.direct = q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
@@ -166,6 +177,192 @@ int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads
   return plan_paged(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, head_dim).floats;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The arguments that the attention calls share.
+struct Call {
+  const void* q;
+  int32_t dtype;
+  int64_t q_token_stride, total_q;
+  int32_t heads, kv_heads, head_dim;
+  const void *k_pages, *v_pages;
+  int64_t n_pages;
+  int32_t page_tokens;
+  int64_t page_stride_bytes;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t *kv_lens, *cu_q;
+  int64_t batch, max_q, max_kv;
+  float scale;
+  int32_t causal;
+  void* out;
+  float* workspace;
+  int64_t workspace_floats;
+  bool empty() const { return batch == 0 || total_q == 0 || max_q == 0; }
+};
+
+// Checks what does not depend on the plan; fills in the kernels' arguments.  An empty call (Call::empty) is accepted
+// before its pointers are looked at.
+int check_call(const char* fn, const Call& c, q8a::PagedArgs* a) {
+  if (int rc = check_heads(fn, c.heads, c.head_dim, c.dtype, false)) return rc;
+  if (c.kv_heads <= 0 || c.heads % c.kv_heads)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "heads (%d) must be a positive multiple of kv_heads (%d)", c.heads, c.kv_heads);
+  if (c.batch < 0 || c.batch > (1 << 20) || c.total_q < 0 || c.total_q >= kMaxTokens || c.max_q < 0 || c.max_kv < 0)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "batch must be 0..2^20, total_q 0..2^31-1, max_q and max_kv not negative");
+  const float scale_log2 = c.scale * 1.4426950408889634f;   // log2(e)
+  if (!(c.scale > 0.0f) || !std::isfinite(scale_log2))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "scale must be > 0 and finite, also times log2(e)");
+  if (int rc = check_stride(fn, "q", c.q_token_stride, c.heads, c.head_dim)) return rc;
+  if (c.empty()) return Q8A_OK;
+  q8a::PagePool pool;
+  if (int rc = check_pool(fn, c.k_pages, c.v_pages, c.n_pages, c.page_tokens, c.page_stride_bytes, c.kv_heads, c.head_dim, &pool))
+    return rc;
+  if (!c.q || !c.out || !c.kv_lens || !c.cu_q || (c.table_stride > 0 && !c.block_table))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "null pointer");
+  if (c.out == c.q) return refuse(Q8A_ERR_INVALID_ARG, fn, "out must not be q");
+  if (c.table_stride < 0 || c.table_stride > 0x7FFFFFFFll)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "table stride must be 0..2^31-1 (got %lld)", (long long)c.table_stride);
+  if (c.max_kv > c.table_stride * c.page_tokens)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "max_kv %lld: the table's rows hold %lld keys", (long long)c.max_kv,
+                  (long long)(c.table_stride * c.page_tokens));
+  if (!aligned(c.q, 16) || !aligned(c.out, 16) || !aligned(c.workspace, 16) || c.q_token_stride % 8 ||
+      !aligned(c.kv_lens, 4) || !aligned(c.cu_q, 4) || !aligned(c.block_table, 4))
+    return refuse(Q8A_ERR_MISALIGNED, fn,
+                  "q, its token stride, out and workspace need 16-byte, the index arrays 4-byte alignment");
+  if (c.total_q * (c.heads / c.kv_heads) >= kMaxTokens)
+    return refuse(Q8A_ERR_UNSUPPORTED, fn, "total_q * heads / kv_heads must be below 2^31");
+  *a = q8a::PagedArgs{};
+  a->q = c.q;
+  a->out = c.out;
+  a->k = pool.k;
+  a->v = pool.v;
+  a->table = c.block_table;
+  a->kv_lens = c.kv_lens;
+  a->cu_q = c.cu_q;
+  a->part = c.workspace;
+  a->n_pages = c.n_pages;
+  a->page_stride = c.page_stride_bytes;
+  a->q_stride = c.q_token_stride;
+  a->table_stride = c.table_stride;
+  a->total_q = c.total_q;
+  a->batch = static_cast<int32_t>(c.batch);
+  a->heads = c.heads;
+  a->kv_heads = c.kv_heads;
+  a->group = c.heads / c.kv_heads;
+  a->page_shift = pool.page_shift;
+  a->causal = c.causal ? 1 : 0;
+  a->scale_log2 = scale_log2;
+  a->timeout_ns = q8a::wait_timeout_ns();
+  return Q8A_OK;
+}
+
+// Checks the workspace against what the plan needs of it, and that no buffers overlap; takes the status words.
+int check_workspace(const char* fn, const Call& c, int64_t need, q8a::PagedArgs* a) {
+  if (need > 0 && !c.workspace) return refuse(Q8A_ERR_INVALID_ARG, fn, "null workspace");
+  if (c.workspace_floats < need)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "workspace of %lld floats < %lld needed", (long long)c.workspace_floats,
+                  (long long)need);
+  const int64_t row = static_cast<int64_t>(c.heads) * c.head_dim * 2;
+  const Rows q_rows = rows_at(c.q, c.total_q, row, c.q_token_stride * 2), o_rows = rows_at(c.out, c.total_q, row, row);
+  if (meet(q_rows, o_rows)) return refuse(Q8A_ERR_INVALID_ARG, fn, "q and out overlap");
+  const Rows ws = rows_at(c.workspace, 1, need * 4, need * 4);
+  if (need > 0 && (meet(q_rows, ws) || meet(o_rows, ws)))
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "the workspace overlaps q or out");
+  return status_words(fn, &a->status);
+}
+
+// The tile kernel's share of a call, with its states at `part`.
+q8a::PagedArgs tiles_args(const q8a::PagedArgs& a, const q8a::TilesPlan& t, int32_t row_limit, float* part) {
+  q8a::PagedArgs b = a;
+  b.row_limit = row_limit;
+  b.shares = t.shares;
+  b.share_tiles = t.share_tiles;
+  b.ctas = t.ctas;
+  b.part = part;
+  b.part_ml = t.part_ml;
+  auto even = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
+  b.wide = (even(a.q) && a.q_stride % 16 == 0 ? q8a::kWideQ : 0) | (even(a.out) ? q8a::kWideOut : 0) |
+           (even(part) ? q8a::kWidePart : 0);
+  return b;
+}
+
+// attn_paged, or attn_paged_window where `window` is not 0.
+int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cudaStream_t st) {
+  q8a::PagedArgs a{};
+  if (int rc = check_call(fn, c, &a)) return rc;
+  if (c.empty()) return q8a::clear_error();
+  const Plan plan = plan_paged(c.batch, c.total_q, c.max_q, a.group, c.kv_heads, c.max_kv, c.head_dim, window, sinks);
+  if (int rc = check_workspace(fn, c, plan.floats, &a)) return rc;
+  a.window = static_cast<int32_t>(window);
+  a.sinks = static_cast<int32_t>(sinks);
+  cudaError_t e = cudaSuccess;
+  if (plan.tiles) {
+    const q8a::PagedArgs b =
+        tiles_args(a, plan.t, plan.few ? static_cast<int32_t>(kFewRows) : 0, c.workspace + plan.few_floats);
+    e = window ? q8a::launch_paged_tiles_window(b, c.dtype, c.head_dim, plan.t, st)
+               : q8a::launch_paged_tiles(b, c.dtype, c.head_dim, plan.t, st);
+  }
+  if (plan.few && e == cudaSuccess) {
+    a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;
+    e = window ? q8a::launch_paged_few_range(a, q8a::kWindow, c.dtype, c.head_dim, plan.few_rows, plan.direct, st)
+               : q8a::launch_paged_few(a, c.dtype, c.head_dim, plan.few_rows, plan.direct, st);
+  }
+  return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
+}
+
+// A call behind a shared prefix: first the rows' states over their own keys (own_few or own), then all rows together
+// over the prefix, whose join takes those states in.  Not `share`: attn_paged.
+struct PrefixPlan {
+  bool share, own_few, own_direct;
+  int64_t own_rows;
+  q8a::TilesPlan own, prefix;
+  int64_t state_floats, floats;
+  Plan plain;
+};
+// Sequences of more rows per K/V head than this fill the tiles of the tensor cores by themselves.
+constexpr int64_t kShareRows = 128;
+PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, int32_t kv_heads, int64_t max_kv,
+                       int64_t max_prefix, int32_t head_dim) {
+  PrefixPlan p{};
+  if (max_q > total_q) max_q = total_q;
+  if (max_kv > q8a::kMaxKeys) max_kv = q8a::kMaxKeys;
+  if (max_prefix > max_kv) max_prefix = max_kv;
+  p.share = batch > 1 && max_q * group <= kShareRows && max_prefix > 0;
+  if (!p.share) {
+    p.plain = plan_paged(batch, total_q, max_q, group, kv_heads, max_kv, head_dim);
+    p.floats = p.plain.floats;
+    return p;
+  }
+  // the own keys are those behind the prefix, as far as the bounds tell
+  const int64_t own_kv = max_kv > max_prefix ? max_kv - max_prefix : max_kv;
+  int64_t own_floats = 0;
+  p.own_rows = max_q * group;
+  p.own_few = p.own_rows <= kFewRows;
+  if (p.own_few) {
+    p.own_direct = q8a::paged_few_direct(batch, kv_heads, own_kv, head_dim);
+    own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
+  } else {
+    // of many sequences the shares are planned here, from the keys that any of them can have
+    p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, batch <= 64 ? own_kv : max_kv, head_dim);
+    own_floats = p.own.floats;
+  }
+  p.prefix = q8a::plan_paged_tiles(1, total_q * group, total_q * group, kv_heads, max_prefix, head_dim);
+  if (!p.prefix.shares) {   // whole units leave their states too, for the join
+    p.prefix.share_tiles = 0x3FFFFFFF;
+    p.prefix.part_ml = p.prefix.ctas * 256 * head_dim;
+    p.prefix.floats = p.prefix.ctas * 256 * (head_dim + 2);
+  }
+  p.state_floats = (total_q * group * kv_heads * (head_dim + 1) + 7) / 8 * 8;
+  p.floats = p.state_floats + (own_floats > p.prefix.floats ? own_floats : p.prefix.floats);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
 int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t total_q, int32_t heads, int32_t kv_heads,
                int32_t head_dim, const void* k_pages, const void* v_pages, int64_t n_pages, int32_t page_tokens,
                int64_t page_stride_bytes, const int32_t* block_table, int64_t table_stride, const int32_t* kv_lens,
@@ -173,89 +370,92 @@ int attn_paged(const void* q, int32_t dtype, int64_t q_token_stride, int64_t tot
                void* out, float* workspace, int64_t workspace_floats, void* stream) {
   q8a::NvtxRange nvtx_range("attn_paged");
   q8a::PdlScope early;   // see the top of this file
-  const char* fn = "attn_paged";
-  if (int rc = check_heads(fn, heads, head_dim, dtype, false)) return rc;
-  if (kv_heads <= 0 || heads % kv_heads)
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "heads (%d) must be a positive multiple of kv_heads (%d)", heads, kv_heads);
-  if (batch < 0 || batch > (1 << 20) || total_q < 0 || total_q >= kMaxTokens || max_q < 0 || max_kv < 0)
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "batch must be 0..2^20, total_q 0..2^31-1, max_q and max_kv not negative");
-  const float scale_log2 = scale * 1.4426950408889634f;   // log2(e)
-  if (!(scale > 0.0f) || !std::isfinite(scale_log2))
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "scale must be > 0 and finite, also times log2(e)");
-  if (int rc = check_stride(fn, "q", q_token_stride, heads, head_dim)) return rc;
-  if (batch == 0 || total_q == 0 || max_q == 0) return q8a::clear_error();
-  q8a::PagePool pool;
-  if (int rc = check_pool(fn, k_pages, v_pages, n_pages, page_tokens, page_stride_bytes, kv_heads, head_dim, &pool))
-    return rc;
-  if (!q || !out || !kv_lens || !cu_q || (table_stride > 0 && !block_table))
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "null pointer");
-  if (out == q) return refuse(Q8A_ERR_INVALID_ARG, fn, "out must not be q");
-  if (table_stride < 0 || table_stride > 0x7FFFFFFFll)
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "table stride must be 0..2^31-1 (got %lld)", (long long)table_stride);
-  if (max_kv > table_stride * page_tokens)
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "max_kv %lld: the table's rows hold %lld keys", (long long)max_kv,
-                  (long long)(table_stride * page_tokens));
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || q_token_stride % 8 ||
-      !aligned(kv_lens, 4) || !aligned(cu_q, 4) || !aligned(block_table, 4))
-    return refuse(Q8A_ERR_MISALIGNED, fn,
-                  "q, its token stride, out and workspace need 16-byte, the index arrays 4-byte alignment");
-  if (total_q * (heads / kv_heads) >= kMaxTokens)
-    return refuse(Q8A_ERR_UNSUPPORTED, fn, "total_q * heads / kv_heads must be below 2^31");
-  const Plan plan = plan_paged(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, head_dim);
-  const int64_t need = plan.floats;
-  if (need > 0 && !workspace) return refuse(Q8A_ERR_INVALID_ARG, fn, "null workspace");
-  if (workspace_floats < need)
-    return refuse(Q8A_ERR_INVALID_ARG, fn, "workspace of %lld floats < %lld needed", (long long)workspace_floats,
-                  (long long)need);
-  {
-    const int64_t row = static_cast<int64_t>(heads) * head_dim * 2;
-    const Rows q_rows = rows_at(q, total_q, row, q_token_stride * 2), o_rows = rows_at(out, total_q, row, row);
-    if (meet(q_rows, o_rows)) return refuse(Q8A_ERR_INVALID_ARG, fn, "q and out overlap");
-    const Rows ws = rows_at(workspace, 1, need * 4, need * 4);
-    if (need > 0 && (meet(q_rows, ws) || meet(o_rows, ws)))
-      return refuse(Q8A_ERR_INVALID_ARG, fn, "the workspace overlaps q or out");
-  }
+  const Call c{q, dtype, q_token_stride, total_q, heads, kv_heads, head_dim, k_pages, v_pages, n_pages, page_tokens,
+               page_stride_bytes, block_table, table_stride, kv_lens, cu_q, batch, max_q, max_kv, scale, causal, out,
+               workspace, workspace_floats};
+  return run_paged("attn_paged", c, 0, 0, static_cast<cudaStream_t>(stream));
+}
+
+int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_t heads, int32_t kv_heads, int64_t max_q,
+                                          int64_t max_kv, int64_t window, int64_t sinks, int32_t head_dim) {
+  if (q8a_paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim) < 0 || window < 1 || sinks < 0)
+    return -1;
+  if (batch == 0 || max_q == 0 || total_q == 0) return 0;
+  return plan_paged(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, head_dim, keys_at_most(window),
+                    keys_at_most(sinks)).floats;
+}
+
+int attn_paged_window(const void* q, int32_t dtype, int64_t q_token_stride, int64_t total_q, int32_t heads,
+                      int32_t kv_heads, int32_t head_dim, const void* k_pages, const void* v_pages, int64_t n_pages,
+                      int32_t page_tokens, int64_t page_stride_bytes, const int32_t* block_table, int64_t table_stride,
+                      const int32_t* kv_lens, const int32_t* cu_q, int64_t batch, int64_t max_q, int64_t max_kv,
+                      int64_t window, int64_t sinks, float scale, void* out, float* workspace, int64_t workspace_floats,
+                      void* stream) {
+  q8a::NvtxRange nvtx_range("attn_paged_window");
+  q8a::PdlScope early;   // see the top of this file
+  const char* fn = "attn_paged_window";
+  if (window < 1 || sinks < 0)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "window must be at least 1, sinks not negative (got %lld, %lld)",
+                  (long long)window, (long long)sinks);
+  const Call c{q, dtype, q_token_stride, total_q, heads, kv_heads, head_dim, k_pages, v_pages, n_pages, page_tokens,
+               page_stride_bytes, block_table, table_stride, kv_lens, cu_q, batch, max_q, max_kv, scale, 1, out,
+               workspace, workspace_floats};
+  return run_paged(fn, c, keys_at_most(window), keys_at_most(sinks), static_cast<cudaStream_t>(stream));
+}
+
+int64_t q8a_paged_prefix_workspace_floats(int64_t batch, int64_t total_q, int32_t heads, int32_t kv_heads, int64_t max_q,
+                                          int64_t max_kv, int64_t max_prefix, int32_t head_dim) {
+  if (q8a_paged_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, head_dim) < 0 || max_prefix < 0) return -1;
+  if (batch == 0 || max_q == 0 || total_q == 0) return 0;
+  return plan_prefix(batch, total_q, max_q, heads / kv_heads, kv_heads, max_kv, max_prefix, head_dim).floats;
+}
+
+int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int64_t total_q, int32_t heads,
+                      int32_t kv_heads, int32_t head_dim, const void* k_pages, const void* v_pages, int64_t n_pages,
+                      int32_t page_tokens, int64_t page_stride_bytes, const int32_t* block_table, int64_t table_stride,
+                      const int32_t* kv_lens, const int32_t* cu_q, int64_t batch, int64_t max_q, int64_t max_kv,
+                      const int32_t* prefix_table, int64_t prefix_pages, const int32_t* prefix_len, int64_t max_prefix,
+                      float scale, int32_t causal, void* out, float* workspace, int64_t workspace_floats, void* stream) {
+  q8a::NvtxRange nvtx_range("attn_paged_prefix");
+  q8a::PdlScope early;   // see the top of this file
+  const char* fn = "attn_paged_prefix";
+  const Call c{q, dtype, q_token_stride, total_q, heads, kv_heads, head_dim, k_pages, v_pages, n_pages, page_tokens,
+               page_stride_bytes, block_table, table_stride, kv_lens, cu_q, batch, max_q, max_kv, scale, causal, out,
+               workspace, workspace_floats};
+  if (prefix_pages < 0 || prefix_pages > 0x7FFFFFFFll || max_prefix < 0)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "prefix_pages must be 0..2^31-1, max_prefix not negative (got %lld, %lld)",
+                  (long long)prefix_pages, (long long)max_prefix);
   q8a::PagedArgs a{};
-  a.q = q;
-  a.out = out;
-  a.k = pool.k;
-  a.v = pool.v;
-  a.table = block_table;
-  a.kv_lens = kv_lens;
-  a.cu_q = cu_q;
-  a.part = workspace;
-  a.n_pages = n_pages;
-  a.page_stride = page_stride_bytes;
-  a.q_stride = q_token_stride;
-  a.table_stride = table_stride;
-  a.total_q = total_q;
-  a.batch = static_cast<int32_t>(batch);
-  a.heads = heads;
-  a.kv_heads = kv_heads;
-  a.group = heads / kv_heads;
-  a.page_shift = pool.page_shift;
-  a.causal = causal ? 1 : 0;
-  a.scale_log2 = scale_log2;
-  a.timeout_ns = q8a::wait_timeout_ns();
-  if (int rc = status_words(fn, &a.status)) return rc;
+  if (int rc = check_call(fn, c, &a)) return rc;
+  if (c.empty()) return q8a::clear_error();
+  if (max_prefix > 0 && (!prefix_table || !prefix_len)) return refuse(Q8A_ERR_INVALID_ARG, fn, "null prefix");
+  if (max_prefix > prefix_pages * page_tokens)
+    return refuse(Q8A_ERR_INVALID_ARG, fn, "max_prefix %lld: the prefix's pages hold %lld keys", (long long)max_prefix,
+                  (long long)(prefix_pages * page_tokens));
+  if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+    return refuse(Q8A_ERR_MISALIGNED, fn, "prefix_table and prefix_len need 4-byte alignment");
+  const PrefixPlan plan = plan_prefix(batch, total_q, max_q, a.group, kv_heads, max_kv, max_prefix, head_dim);
+  if (!plan.share) return run_paged(fn, c, 0, 0, static_cast<cudaStream_t>(stream));
+  if (int rc = check_workspace(fn, c, plan.floats, &a)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (plan.tiles) {
-    q8a::PagedArgs b = a;
-    b.row_limit = plan.few ? static_cast<int32_t>(kFewRows) : 0;
-    b.shares = plan.t.shares;
-    b.share_tiles = plan.t.share_tiles;
-    b.ctas = plan.t.ctas;
-    b.part = workspace + plan.few_floats;
-    b.part_ml = plan.t.part_ml;
-    auto even = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 32 == 0; };
-    b.wide = (even(q) && q_token_stride % 16 == 0 ? q8a::kWideQ : 0) | (even(out) ? q8a::kWideOut : 0) |
-             (even(b.part) ? q8a::kWidePart : 0);
-    e = q8a::launch_paged_tiles(b, dtype, head_dim, plan.t, st);
+  a.prefix_len = prefix_len;
+  a.prefix_most = keys_at_most(max_prefix);
+  a.state = workspace;
+  a.part = workspace + plan.state_floats;
+  cudaError_t e;
+  if (plan.own_few) {
+    a.row_limit = 0x7FFFFFFF;
+    e = q8a::launch_paged_few_range(a, q8a::kOwn, dtype, head_dim, plan.own_rows, plan.own_direct, st);
+  } else {
+    e = q8a::launch_paged_tiles_own(tiles_args(a, plan.own, 0, a.part), dtype, head_dim, plan.own, st);
   }
-  if (plan.few && e == cudaSuccess) {
-    a.row_limit = plan.tiles ? static_cast<int32_t>(kFewRows) : 0x7FFFFFFF;
-    e = q8a::launch_paged_few(a, dtype, head_dim, plan.few_rows, plan.direct, st);
+  if (e == cudaSuccess) {
+    q8a::PagedArgs b = tiles_args(a, plan.prefix, 0, a.part);
+    b.seqs = b.batch;
+    b.batch = 1;
+    b.table = prefix_table;
+    b.table_stride = prefix_pages;
+    e = q8a::launch_paged_tiles_prefix(b, dtype, head_dim, plan.prefix, st);
   }
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();
 }

@@ -36,4 +36,58 @@ __device__ __forceinline__ Seq read_seq(const PagedArgs& a, int b) {
   return s;
 }
 
+// Keys of the shared prefix: whole pages of it, so that what is left of it is every sequence's own.
+__device__ __forceinline__ int prefix_keys(const PagedArgs& a) {
+  const int64_t n = a.prefix_len[0];
+  if (n < 0 || n > a.prefix_most) record_index(a.status);
+  return static_cast<int>(i64max(0, i64min(n, a.prefix_most)) >> a.page_shift << a.page_shift);
+}
+
+// The key tiles of a run of rows: `sink` tiles from key 0 on, the others from key `base` on; `base` starts a
+// piece of a page (kPlain: all from key 0).
+struct Span {
+  int32_t sink, base;
+  int32_t low;   // kWindow: the first key of the first row's window
+};
+// Whether any row needs the piece of 2^shift keys from `key` on.  Those between the sinks and the window are not copied
+// (their pages may have been given away), so a tile has there whatever its buffer held.
+template <int kMode>
+__device__ __forceinline__ bool piece_needed(const PagedArgs& a, const Span& s, int key, int shift) {
+  return kMode != kWindow || key < a.sinks || key + (1 << shift) > s.low;
+}
+template <int kMode, int KT>
+__device__ __forceinline__ int key_of(const Span& s, int tile) {
+  if (kMode == kPlain || kMode == kPrefix) return tile * KT;
+  if (kMode == kOwn) return s.base + tile * KT;
+  return tile < s.sink ? tile * KT : s.base + (tile - s.sink) * KT;
+}
+// Of rows whose first token is at position p0 and whose last sees the keys before `end`; start: the first own key.
+template <int kMode, int KT>
+__device__ __forceinline__ Span span_of(const PagedArgs& a, int64_t p0, int end, int start, int piece_shift) {
+  if (kMode == kOwn) return Span{0, start, 0};
+  if (kMode != kWindow) return Span{0, 0, 0};
+  Span s;
+  s.low = static_cast<int32_t>(i64max(0, p0 - a.window + 1));
+  s.base = s.low >> piece_shift << piece_shift;
+  s.sink = (max(0, min(a.sinks, end)) + KT - 1) / KT;
+  if (static_cast<int64_t>(s.sink) * KT >= s.base) s.sink = s.base = 0;   // one run
+  return s;
+}
+// Tiles that reach the keys before `end`.
+template <int kMode, int KT>
+__device__ __forceinline__ int span_tiles(const Span& s, int end) {
+  if (kMode == kPlain || kMode == kPrefix) return (max(end, 0) + KT - 1) / KT;
+  return s.sink + (max(end - s.base, 0) + KT - 1) / KT;
+}
+
+// Weight of a partial state (reference m, sum l) under the joint reference top.  A row whose scores
+// are all NaN has no reference, and keeps its NaN.
+__device__ __forceinline__ float state_weight(float m, float l, float top) {
+  return m == -INFINITY ? (l != l ? l : 0.0f) : (m == top ? 1.0f : ex2_approx(m - top));
+}
+// The logarithm of a row's sum of weights; -infinity of a row that sees nothing.
+__device__ __forceinline__ float state_log(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(l);
+}
+
 }  // namespace q8a

@@ -69,6 +69,12 @@ SIGNATURES = {
     "attn_paged": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
                                   _P, _P, _I64, _I64, _I64, _F, _I32, _P, _P, _I64, _P]),
     "q8a_paged_workspace_floats": (_I64, [_I64, _I64, _I32, _I32, _I64, _I64, _I32]),
+    "attn_paged_window": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
+                                         _P, _P, _I64, _I64, _I64, _I64, _I64, _F, _P, _P, _I64, _P]),
+    "q8a_paged_window_workspace_floats": (_I64, [_I64, _I64, _I32, _I32, _I64, _I64, _I64, _I64, _I32]),
+    "attn_paged_prefix": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _I64, _I32, _I64, _P, _I64,
+                                         _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _F, _I32, _P, _P, _I64, _P]),
+    "q8a_paged_prefix_workspace_floats": (_I64, [_I64, _I64, _I32, _I32, _I64, _I64, _I64, _I32]),
     "q8kv_extend_paged": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P]),
     "attn_norm_rope": (ctypes.c_int, [_P, _P, _I32, _I64, _I64, _P, _P, _I32, _I64, _I64, _I32, _I64, _I32, _P, _P,
                                       _I32, _F, _P, _I32, _P, _P, _I32, _I32, _F, _P]),
@@ -587,15 +593,20 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
     and kv_lens[b] keys (int32 [B], the new tokens' own keys last) in the pages block_table[b] (int32
     [B, width]).  max_q, max_kv: bounds of the rows and keys of a sequence.  `workspace`: fp32 CUDA tensor
     of paged_workspace_floats(...) elements (allocated here when None).  Returns [total_q, H, D]."""
+    return _attention("attn_paged", q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, (), scale,
+                      (1 if causal else 0,), out, workspace, paged_workspace_floats, ())
+
+
+def _attention(name, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, before, scale, after, out, workspace,
+               floats_of, bounds):
+    """The call `name` on checked tensors: `before` and `after` are its arguments around scale, floats_of(..., *bounds)
+    its workspace."""
     device = _device_of(q)
     code, T, H, D, stride = _packed("q", q, device)
     n_pages, kv_heads, page_tokens, head_dim, page_stride = _pool(k_pages, v_pages, device)
     if D != head_dim:
         _refuse(f"q has head_dim {D}, the pages {head_dim}")
-    if not (isinstance(block_table, torch.Tensor) and block_table.dtype == torch.int32 and block_table.dim() == 2 and
-            block_table.is_contiguous() and block_table.get_device() == device):
-        _refuse(f"block_table: a contiguous int32 tensor [batch, width] on cuda:{device} is needed")
-    B, width = block_table.shape
+    table, B, width = _table("block_table", block_table, device)
     lens = _index("kv_lens", kv_lens, torch.int32, B, device)
     cu = _index("cu_q", cu_q, torch.int32, B + 1, device)
     if out is None:
@@ -605,7 +616,7 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
         _refuse(f"out: a contiguous tensor {(T, H, D)} of {q.dtype} on cuda:{device} is needed")
     ws = floats = 0
     if workspace is None:
-        floats = paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D)
+        floats = floats_of(B, T, H, kv_heads, max_q, max_kv, *bounds, D)
         if floats:
             workspace = torch.empty(floats, dtype=torch.float32, device=q.device)
             ws = workspace.data_ptr()
@@ -614,11 +625,53 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
         _refuse(f"workspace: a contiguous fp32 tensor on cuda:{device} is needed")
     else:
         ws, floats = workspace.data_ptr(), workspace.numel()
-    _call(load().attn_paged, device, q.data_ptr(), code, stride, T, H, kv_heads, D, k_pages.data_ptr(),
-          v_pages.data_ptr(), n_pages, page_tokens, page_stride, block_table.data_ptr(), width, lens, cu, B, max_q,
-          max_kv, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
-          ws, floats)
+    _call(getattr(load(), name), device, q.data_ptr(), code, stride, T, H, kv_heads, D, k_pages.data_ptr(),
+          v_pages.data_ptr(), n_pages, page_tokens, page_stride, table, width, lens, cu, B, max_q, max_kv, *before,
+          1.0 / math.sqrt(D) if scale is None else scale, *after, out.data_ptr(), ws, floats)
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_window_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, window, sinks, head_dim=HEAD_DIM):
+    """Floats of attn_paged_window's workspace for these bounds."""
+    n = int(load().q8a_paged_window_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, window, sinks, head_dim))
+    if n < 0:
+        raise Q8AttnError(Q8A_ERR_INVALID_ARG, "invalid sizes for the paged workspace")
+    return n
+
+
+def attn_paged_window(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, window, sinks=0, scale=None, out=None,
+                      workspace=None):
+    """attn_paged (causal) where the row at position p sees the keys p - window + 1 .. p and the sequence's first
+    `sinks` keys.  `workspace`: of paged_window_workspace_floats(...) elements (allocated here when None)."""
+    return _attention("attn_paged_window", q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, (window, sinks),
+                      scale, (), out, workspace, paged_window_workspace_floats, (window, sinks))
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_prefix_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, max_prefix, head_dim=HEAD_DIM):
+    """Floats of attn_paged_prefix's workspace for these bounds."""
+    n = int(load().q8a_paged_prefix_workspace_floats(batch, total_q, heads, kv_heads, max_q, max_kv, max_prefix, head_dim))
+    if n < 0:
+        raise Q8AttnError(Q8A_ERR_INVALID_ARG, "invalid sizes for the paged workspace")
+    return n
+
+
+def attn_paged_prefix(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, prefix_table, prefix_len,
+                      max_prefix=None, scale=None, causal=True, out=None, workspace=None):
+    """attn_paged for sequences whose first prefix_len[0] keys (int32 [1]) are the same pages, prefix_table (int32 [n]):
+    these are read once for all rows.  block_table names them too, and kv_lens counts their keys; whole pages are shared.
+    max_prefix: a bound of prefix_len (default: what prefix_table's pages hold).  `workspace`: of
+    paged_prefix_workspace_floats(...) elements (allocated here when None)."""
+    device = _device_of(q)
+    pages = prefix_table.shape[0] if isinstance(prefix_table, torch.Tensor) and prefix_table.dim() == 1 else -1
+    table = _index("prefix_table", prefix_table, torch.int32, pages, device)
+    length = _index("prefix_len", prefix_len, torch.int32, 1, device)
+    if max_prefix is None:
+        max_prefix = pages * (k_pages.shape[2] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4 else 0)
+    return _attention("attn_paged_prefix", q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv,
+                      (table, pages, length, max_prefix), scale, (1 if causal else 0,), out, workspace,
+                      paged_prefix_workspace_floats, (max_prefix,))
 
 
 def _table(name, t, device):

@@ -529,6 +529,55 @@ int64_t q8a_paged_workspace_floats(int64_t batch, int64_t total_q, int32_t heads
                                    int64_t max_q, int64_t max_kv, int32_t head_dim);
 
 /*
+ * attn_paged_window -- attn_paged (causal) where a row at position p sees only the keys of
+ * its window, p - window + 1 .. p, and the sequence's first `sinks` keys (which stay visible
+ * however far the window has moved).  Only the pages with such keys are read.
+ *   window  at least 1; sinks  0 or more.  Anything beyond a sequence's length is allowed.
+ * Numerics, bounds and errors as attn_paged; a key behind the window counts as one that the row does not
+ * see.  The workspace holds q8a_paged_window_workspace_floats(...) floats.
+ */
+int attn_paged_window(const void *q, int32_t dtype, int64_t q_token_stride, int64_t total_q,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, const void *k_pages,
+                      const void *v_pages, int64_t n_pages, int32_t page_tokens,
+                      int64_t page_stride_bytes, const int32_t *block_table, int64_t table_stride,
+                      const int32_t *kv_lens, const int32_t *cu_q, int64_t batch, int64_t max_q,
+                      int64_t max_kv, int64_t window, int64_t sinks, float scale, void *out,
+                      float *workspace, int64_t workspace_floats, void *stream);
+int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_t heads,
+                                          int32_t kv_heads, int64_t max_q, int64_t max_kv,
+                                          int64_t window, int64_t sinks, int32_t head_dim);
+
+/*
+ * attn_paged_prefix -- attn_paged for sequences whose first keys are the same pages (a system
+ * prompt, a document that many ask about): the pages of the shared prefix are read once for all
+ * rows of all sequences, those behind it for each sequence, and a row's two states are joined.
+ * The result is attn_paged's, up to rounding.
+ *   prefix_table  int32 [prefix_pages] on the device: the prefix's pages.
+ *   prefix_len    int32 [1] on the device, 0..max_prefix (a value out of range is recorded and
+ *                 taken for the nearest): keys that the sequences share.  Of a prefix that ends inside a
+ *                 page the whole pages are shared; what is left is read as the sequences' own.
+ *   max_prefix    upper bound of prefix_len, at most prefix_pages * page_tokens.
+ *   block_table   each row names the prefix's pages too, as for attn_paged: the first
+ *                 prefix_len / page_tokens entries may be read or not.  kv_lens counts the prefix's keys;
+ *                 a sequence may be shorter than the prefix, and sees its first kv_lens keys.
+ * Calls whose sequences have more than 128 rows per K/V head, or of one sequence, run as attn_paged.
+ * Numerics: attn_paged's with max_q * group above 16 for the prefix; an output joins two
+ * states in fp32.  Rows of sequences beyond the bounds max_q, max_kv get unspecified results.  Errors: as
+ * attn_paged.  The workspace holds q8a_paged_prefix_workspace_floats(...) floats.
+ */
+int attn_paged_prefix(const void *q, int32_t dtype, int64_t q_token_stride, int64_t total_q,
+                      int32_t heads, int32_t kv_heads, int32_t head_dim, const void *k_pages,
+                      const void *v_pages, int64_t n_pages, int32_t page_tokens,
+                      int64_t page_stride_bytes, const int32_t *block_table, int64_t table_stride,
+                      const int32_t *kv_lens, const int32_t *cu_q, int64_t batch, int64_t max_q,
+                      int64_t max_kv, const int32_t *prefix_table, int64_t prefix_pages,
+                      const int32_t *prefix_len, int64_t max_prefix, float scale, int32_t causal,
+                      void *out, float *workspace, int64_t workspace_floats, void *stream);
+int64_t q8a_paged_prefix_workspace_floats(int64_t batch, int64_t total_q, int32_t heads,
+                                          int32_t kv_heads, int64_t max_q, int64_t max_kv,
+                                          int64_t max_prefix, int32_t head_dim);
+
+/*
  * q8kv_extend_paged -- the lengths, block tables, slots and positions of a step, on the
  * device, from the number of new tokens of each sequence: sequence b goes on from
  * kv_lens[b] keys to kv_lens[b] + new_lens[b], its new tokens are the packed rows
