@@ -125,6 +125,20 @@ constexpr int64_t kFewRows = 16;
 // A number of keys, cut to the most that a sequence can have.
 int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; }
 
+// Whether the few-row kernel takes a CTA per (sequence, K/V head) where the keys of a sequence are bounded: by a
+// window, or behind a prefix.  No second launch then, but the longest CTA sets the time.  Against shares of all tiles,
+// 8 K/V heads, single tokens, us: windows of 2,048 keys of 64 channels (8 tiles a warp) 13 and 15 for one sequence, 19
+// and 21 for 16; of 4,096 22 and 16, 31 and 27.  At 128 channels 1,024 keys 14 and 17, 20 and 25; 2,048 keys 23 and
+// 18, 33 and 31.  Where the units are whole waves of two CTAs an SM longer ones gain too: 38 sequences
+// (304 units) 35 and 51 (4,096 of 64 channels), 63 and 86 (of 128); 64 sequences (512 units, 84 % of two
+// waves) 65 and 69, 120 and 125.  Up to 40 tiles a warp: a batch with one long sequence waits 50 us for it.
+bool few_direct(int64_t batch, int32_t kv_heads, int64_t keys, int32_t head_dim) {
+  const int64_t units = batch * kv_heads, slots = 2 * 152;
+  const int64_t per_warp = (keys + 8 * (2048 / head_dim) - 1) / (8 * (2048 / head_dim));   // tiles of 32 or 16 keys
+  const int64_t waves = (units + slots - 1) / slots;
+  return units <= 0x7FFFFFFF && (per_warp <= 8 || (per_warp <= 40 && units * 100 >= waves * slots * 84));
+}
+
 // The launches of a call, from its bounds alone.
 struct Plan {
   bool few, direct, tiles;
@@ -158,7 +172,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.direct = q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
+  p.direct = window ? few_direct(batch, kv_heads, few_kv, head_dim) : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
@@ -316,6 +330,7 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
 // over the prefix, whose join takes those states in.  Not `share`: attn_paged.
 struct PrefixPlan {
   bool share, own_few, own_direct;
+  int32_t join_rows;
   int64_t own_rows;
   q8a::TilesPlan own, prefix;
   int64_t state_floats, floats;
@@ -323,13 +338,25 @@ struct PrefixPlan {
 };
 // Sequences of more rows per K/V head than this fill the tiles of the tensor cores by themselves.
 constexpr int64_t kShareRows = 128;
+// Whether sharing pays.  Read for each sequence, a key of the prefix costs (relative to one of the few-row kernel for up
+// to 8 rows) 1, 1.35 for up to 16 rows, 2.4 in the tile kernel; read once, 2.4 for every 256 rows of the batch (what bounds the
+// tile kernel there is dequantisation, whose cost a byte is that much above the few-row kernel's).  The gain has to
+// outweigh the launches that sharing adds, 12 us, which is 3e7 channels, and twice that where the own keys are the tile
+// kernel's (32 rows a sequence, one K/V head, 128 channels, 64 sequences of 2,048 keys 40 and 32, of 8,192 44 and 70).  Shared and not, us (q rows a sequence): 8 K/V
+// heads, group 4, 64 channels, 4 sequences of 32,768 keys 38 and 36; 16 of 2,048 24 and 20, of 8,192 30 and 37,
+// of 32,768 39 and 102; 64 of 512 30 and 17, of 2,048 30 and 40, of 32,768 48 and 362; 128 channels, 64 of 32,768 74 and 726.
+bool share_pays(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_prefix, int32_t head_dim) {
+  const double each = max_rows <= 8 ? 1.0 : max_rows <= kFewRows ? 1.35 : 2.4;
+  const double units = static_cast<double>((total_rows + 255) / 256);
+  return static_cast<double>(max_prefix) * kv_heads * head_dim * (each * batch - 2.4 * units) > (max_rows <= kFewRows ? 3e7 : 6e7);
+}
 PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, int32_t kv_heads, int64_t max_kv,
                        int64_t max_prefix, int32_t head_dim) {
   PrefixPlan p{};
   if (max_q > total_q) max_q = total_q;
   if (max_kv > q8a::kMaxKeys) max_kv = q8a::kMaxKeys;
   if (max_prefix > max_kv) max_prefix = max_kv;
-  p.share = batch > 1 && max_q * group <= kShareRows && max_prefix > 0;
+  p.share = max_q * group <= kShareRows && share_pays(batch, total_q * group, max_q * group, kv_heads, max_prefix, head_dim);
   if (!p.share) {
     p.plain = plan_paged(batch, total_q, max_q, group, kv_heads, max_kv, head_dim);
     p.floats = p.plain.floats;
@@ -341,7 +368,7 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   p.own_rows = max_q * group;
   p.own_few = p.own_rows <= kFewRows;
   if (p.own_few) {
-    p.own_direct = q8a::paged_few_direct(batch, kv_heads, own_kv, head_dim);
+    p.own_direct = few_direct(batch, kv_heads, own_kv, head_dim);
     own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
   } else {
     // of many sequences the shares are planned here, from the keys that any of them can have
@@ -354,6 +381,8 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
     p.prefix.part_ml = p.prefix.ctas * 256 * head_dim;
     p.prefix.floats = p.prefix.ctas * 256 * (head_dim + 2);
   }
+  // a warp a row where they are enough for the machine, else a block a row
+  p.join_rows = total_q * group * kv_heads >= 152 * 8 ? 8 : 1;
   p.state_floats = (total_q * group * kv_heads * (head_dim + 1) + 7) / 8 * 8;
   p.floats = p.state_floats + (own_floats > p.prefix.floats ? own_floats : p.prefix.floats);
   return p;
@@ -455,6 +484,7 @@ int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int6
     b.batch = 1;
     b.table = prefix_table;
     b.table_stride = prefix_pages;
+    b.join_rows = plan.join_rows;
     e = q8a::launch_paged_tiles_prefix(b, dtype, head_dim, plan.prefix, st);
   }
   return e != cudaSuccess ? cuda_refuse(e, fn) : q8a::clear_error();

@@ -271,6 +271,11 @@ constexpr int kPlanned = 64;   // most sequences of a call whose shares are plan
 template <int D, bool kPair, int kMode>
 __device__ __forceinline__ int plan_shares(const PagedArgs& a, int lane) {
   if (a.share_tiles > 0) return a.share_tiles;
+  if (kMode == kPrefix) {   // one sequence: every unit has the same tiles, cut so that the grid is filled once
+    const Load one = load_of<D, kPair, kMode>(a, 0);
+    const int parts = static_cast<int>(max(static_cast<int64_t>(1), a.ctas / (static_cast<int64_t>(max(one.units, 1)) * a.kv_heads)));
+    return max(4, (one.tiles + parts - 1) / parts);
+  }
   Load mine[kPlanned / 32];
   int top = 0;
 #pragma unroll
@@ -906,6 +911,7 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
 template <typename QT, int D, bool kPair, int kMode>
 __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a) {
   __shared__ Ctl ctl;
+  __shared__ float sums[kMode == kPrefix ? 8 : 1][D + 1];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -913,7 +919,9 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   __syncthreads();
   if (ctl.b < 0) return;
   const Unit u = make_unit<D, kPair, kMode>(a, &ctl, 0);
-  const int in_unit = blockIdx.y * 8 + warp;
+  // kPrefix with few rows: a block per row, its warps deal the states out among themselves
+  const bool one = kMode == kPrefix && a.join_rows == 1;
+  const int in_unit = one ? blockIdx.y : blockIdx.y * 8 + warp;
   const int row = u.r0 + in_unit;
   if (row >= u.n_rows) return;
   const int tiles = tiles_of<D, kPair, kMode>(a, u.sq, u.span, u.r0 + in_unit / BM * BM, u.n_rows);
@@ -933,30 +941,76 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   const int64_t out_row = (u.sq.q0 + tok) * a.heads + u.kvh * a.group + row - tok * a.group;
   float top = -INFINITY;
   float l = 0.0f, y[D / 32] = {};
-  if (kMode == kPrefix) {
-    if (tok < a.cu_q[0] || tok >= a.cu_q[a.seqs]) return;   // a row of no sequence stays as it is
-    const float own = a.state[a.total_q * a.heads * D + out_row];
-    top = own;
+  if (kMode == kPlain) {
     for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + z * step].x);
-    l = state_weight(own, 1.0f, top) * 128.0f;   // the shares' weights carry 2^kLift
-    static_assert(kLift == 7.0f, "2^7");
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) y[i] = l * a.state[out_row * D + 32 * i + lane];
-    if (l == 0.0f)
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) y[i] = 0.0f;
-  } else {
-    for (int z = 0; z < n; ++z) top = fmaxf(top, ml[at0 + z * step].x);
-  }
 #pragma unroll 4
-  for (int z = 0; z < n; ++z) {
-    const int64_t at = at0 + z * step;
-    const float2 v = ml[at];
-    const float w = kMode != kPlain ? state_weight(v.x, v.y, top)
-                                    : v.x == -INFINITY ? 0.0f : (v.x == top ? 1.0f : ex2_approx(v.x - top));
-    l = fmaf(w, v.y, l);
+    for (int z = 0; z < n; ++z) {
+      const int64_t at = at0 + z * step;
+      const float2 v = ml[at];
+      const float w = v.x == -INFINITY ? 0.0f : (v.x == top ? 1.0f : ex2_approx(v.x - top));
+      l = fmaf(w, v.y, l);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) y[i] = fmaf(w, a.part[at * D + 32 * i + lane], y[i]);
+      for (int i = 0; i < D / 32; ++i) y[i] = fmaf(w, a.part[at * D + 32 * i + lane], y[i]);
+    }
+  } else {
+    // the states' references and sums a lane each, then their values, eight in flight
+    float own = 0.0f, own_y[D / 32];
+    if (kMode == kPrefix) {
+      if (tok < a.cu_q[0] || tok >= a.cu_q[a.seqs]) return;   // a row of no sequence stays as it is
+      own = a.state[a.total_q * a.heads * D + out_row];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) own_y[i] = a.state[out_row * D + 32 * i + lane];
+    }
+#pragma unroll 4
+    for (int z = lane; z < n; z += 32) top = fmaxf(top, ml[at0 + z * step].x);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (kMode == kPrefix) {
+      // the shares' weights carry 2^kLift: their logarithms are that much above the own keys'
+      static_assert(kLift == 7.0f, "2^7");
+      top = fmaxf(top, own);
+      l = one && warp > 0 ? 0.0f : state_weight(own, 1.0f, top) * 128.0f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) y[i] = l == 0.0f ? 0.0f : l * own_y[i];
+    }
+    const int per = one ? (n + 7) / 8 : n, last = one ? min(n, (warp + 1) * per) : n;   // this warp's states
+    for (int z0 = one ? warp * per : 0; z0 < last; z0 += 32) {
+      const float2 v = z0 + lane < last ? ml[at0 + (z0 + lane) * step] : make_float2(-INFINITY, 0.0f);
+      const float w_mine = state_weight(v.x, v.y, top);
+      float s = w_mine * v.y;
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(kFull, s, o);
+      l += s;
+      const float* part = a.part + (at0 + z0 * step) * D + lane;
+      const int here = min(32, last - z0);
+#pragma unroll 1
+      for (int z = 0; z < here; z += 8) {
+        float x[8][D / 32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) x[k][i] = z + k < here ? part[(z + k) * step * D + 32 * i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float w = __shfl_sync(kFull, w_mine, (z + k) & 31);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) y[i] = z + k < here ? fmaf(w, x[k][i], y[i]) : y[i];
+        }
+      }
+    }
+    if (one) {   // the warps' sums, in order
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) sums[warp][32 * i + lane] = y[i];
+      if (lane == 0) sums[warp][D] = l;
+      __syncthreads();
+      if (warp > 0) return;
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        l += sums[k][D];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) y[i] += sums[k][32 * i + lane];
+      }
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if (kMode == kOwn) {
@@ -997,7 +1051,8 @@ cudaError_t launch_tiles(const PagedArgs& a, const TilesPlan& plan, cudaStream_t
   }
   e = launch_kernel(kernel, dim3(static_cast<unsigned>(plan.ctas)), dim3(G::kThreads), G::SMEM, stream, a);
   if (e != cudaSuccess || !(kPair || kMode == kPrefix || a.shares)) return e;
-  return launch_kernel(paged_tiles_join_kernel<QT, D, kPair, kMode>, dim3(static_cast<unsigned>(plan.slots), G::ROWS / 8), dim3(256), 0, stream, a);
+  const unsigned rows = kMode == kPrefix ? a.join_rows : 8;
+  return launch_kernel(paged_tiles_join_kernel<QT, D, kPair, kMode>, dim3(static_cast<unsigned>(plan.slots), G::ROWS / rows), dim3(256), 0, stream, a);
 }
 
 template <bool kPair, int kMode>

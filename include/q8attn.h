@@ -553,14 +553,15 @@ int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_
  * rows of all sequences, those behind it for each sequence, and a row's two states are joined.
  * The result is attn_paged's, up to rounding.
  *   prefix_table  int32 [prefix_pages] on the device: the prefix's pages.
- *   prefix_len    int32 [1] on the device, 0..max_prefix (a value out of range is recorded and
- *                 taken for the nearest): keys that the sequences share.  Of a prefix that ends inside a
+ *   prefix_len    int32 [1] on the device, 0..max_prefix (where it is read, a value out of range is
+ *                 recorded and taken for the nearest): keys that the sequences share.  Of a prefix that ends inside a
  *                 page the whole pages are shared; what is left is read as the sequences' own.
  *   max_prefix    upper bound of prefix_len, at most prefix_pages * page_tokens.
  *   block_table   each row names the prefix's pages too, as for attn_paged: the first
  *                 prefix_len / page_tokens entries may be read or not.  kv_lens counts the prefix's keys;
  *                 a sequence may be shorter than the prefix, and sees its first kv_lens keys.
- * Calls whose sequences have more than 128 rows per K/V head, or of one sequence, run as attn_paged.
+ * Calls whose sequences have more than 128 rows per K/V head, and those whose bounds say that the
+ * launches that sharing adds would cost more than it saves (few sequences, short prefixes), run as attn_paged.
  * Numerics: attn_paged's with max_q * group above 16 for the prefix; an output joins two
  * states in fp32.  Rows of sequences beyond the bounds max_q, max_kv get unspecified results.  Errors: as
  * attn_paged.  The workspace holds q8a_paged_prefix_workspace_floats(...) floats.

@@ -235,8 +235,18 @@ class Shared(Batch):
         self.pages = self.table[0, :-(-prefix // page)].clone()
         self.len = torch.tensor([prefix], dtype=torch.int32, device="cuda")
 
-    def shared(self):
-        return (*self.args(), self.pages, self.len)
+    def shared(self, loose=True):
+        """The call's arguments.  Whether the prefix is shared goes by the bounds; loose ones, as of a captured step made for
+        long prefixes, make it so (but for two sequences of few rows, which never pay)."""
+        if not loose:
+            return (*self.args(), self.pages, self.len)
+        q, k_pages, v_pages, table, lens, cu, max_q, max_kv = self.args()
+        entries = (1 << 19) // self.page
+        pages = torch.full((entries,), 0x7FFFFFFF, dtype=torch.int32, device="cuda")
+        pages[:len(self.pages)] = self.pages
+        wide = torch.full((table.shape[0], entries + table.shape[1]), 0x7FFFFFFF, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        return q, k_pages, v_pages, wide, lens, cu, max_q, entries * self.page + max_kv - self.prefix, pages, self.len
 
 
 def before(causal):
@@ -246,13 +256,14 @@ def before(causal):
 PREFIX = [
     # new tokens, own keys, prefix, heads, kv heads, D, page
     ([1, 1], [1, 1], 16, 1, 1, 64, 16),
+    ([1, 1, 1], [1, 1, 1], 16, 1, 1, 64, 16),
     ([1, 1, 1], [1, 40, 7], 160, 8, 2, 64, 16),
     ([1, 1, 1], [1, 40, 7], 161, 8, 2, 64, 16),           # the prefix ends inside a page
     ([1] * 4, [9, 200, 30, 150], 2048, 32, 8, 64, 16),
     ([1] * 16, [50 + 31 * i for i in range(16)], 3000, 8, 2, 128, 64),
     ([1] * 70, [1 + 13 * i for i in range(70)], 777, 4, 1, 64, 32),
     ([1] * 300, [1 + i % 50 for i in range(300)], 1111, 4, 4, 64, 16),
-    ([1, 1], [3000, 5], 96, 4, 4, 128, 32),
+    ([1, 1, 1], [3000, 5, 64], 96, 4, 4, 128, 32),
     ([2, 3, 1, 5], [2, 3, 900, 77], 500, 4, 2, 64, 16),
     ([4, 0, 4], [4, 0, 60], 6000, 16, 4, 128, 128),
     ([16, 9], [1000, 9], 400, 8, 2, 64, 64),
@@ -260,7 +271,7 @@ PREFIX = [
     ([128, 1], [200, 1], 640, 2, 2, 64, 16),
     ([40] * 70, [40 + 9 * i for i in range(70)], 640, 3, 1, 64, 16),
     ([5] * 40, [5 + 11 * i for i in range(40)], 20000, 8, 2, 64, 256),
-    ([2, 2], [2, 2], 5, 4, 2, 64, 16),                    # shorter than a page: nothing is shared
+    ([2] * 5, [2] * 5, 5, 4, 2, 64, 16),                  # shorter than a page: nothing is shared
     ([200, 3], [200, 3], 300, 4, 2, 64, 16),              # as attn_paged
     ([7], [70], 300, 4, 2, 64, 16),
 ]
@@ -269,10 +280,11 @@ PREFIX = [
 @pytest.mark.parametrize("q_lens,own,prefix,heads,kv_heads,D,page", PREFIX)
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("causal", [True, False])
-def test_prefix(Q, q_lens, own, prefix, heads, kv_heads, D, page, dtype, causal):
+@pytest.mark.parametrize("loose", [True, False])
+def test_prefix(Q, q_lens, own, prefix, heads, kv_heads, D, page, dtype, causal, loose):
     x = Shared(q_lens, own, prefix, heads, kv_heads, D, page, dtype, seed=len(q_lens) + sum(own))
     out = torch.full_like(x.q, float("nan"))
-    Q.attn_paged_prefix(*x.shared(), causal=causal, out=out)
+    Q.attn_paged_prefix(*x.shared(loose), causal=causal, out=out)
     check(x, out, before(causal), joined=True)
 
 
@@ -295,15 +307,18 @@ def test_prefix_of_any_length(Q, q_len):
         check(x, Q.attn_paged_prefix(*x.shared()), before(True), joined=True)
     x.len.fill_(100)
     check(x, Q.attn_paged_prefix(*x.args(), x.table[1], x.len), before(True), joined=True)
-    check(x, Q.attn_paged_prefix(*x.args(), x.table[1], x.len, max_prefix=100), before(True), joined=True)
     check(x, Q.attn_paged_prefix(*x.args(), x.table[1], x.len, max_prefix=0), before(True), joined=True)
-    assert Q.device_status(clear=True)[0] == Q.Q8A_OK   # attn_paged's kernels read no length there
-    x.len.fill_(200)
-    check(x, Q.attn_paged_prefix(*x.args(), x.table[1], x.len, max_prefix=100), before(True), joined=True)
-    assert Q.device_status(clear=True)[0] == Q.Q8A_ERR_INVALID_ARG
-    x.len.fill_(-1)
-    check(x, Q.attn_paged_prefix(*x.shared()), before(True), joined=True)
-    assert Q.device_status(clear=True)[0] == Q.Q8A_ERR_INVALID_ARG
+    assert Q.device_status(clear=True)[0] == Q.Q8A_OK
+    for n, most in ((300000, 200000), (-1, None), (-(1 << 31), None), ((1 << 31) - 1, None)):   # beyond the bound
+        x.len.fill_(n)
+        if n > 0:   # the keys up to the bound are taken: the prefix's own pages have to reach that far
+            x.kv_lens.fill_(0)
+            out = Q.attn_paged_prefix(*x.shared(), max_prefix=most)
+            assert (out == 0).all()
+            x.kv_lens.copy_(torch.tensor(x.kv_lens_host))
+        else:
+            check(x, Q.attn_paged_prefix(*x.shared(), max_prefix=most), before(True), joined=True)
+        assert Q.device_status(clear=True)[0] == Q.Q8A_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("q_len", [1, 3, 25])
@@ -316,7 +331,9 @@ def test_prefix_beyond_some_sequences(Q, q_len):
         full = x.kv_lens_host, x.k, x.v
         x.kv_lens_host = kv
         x.k, x.v = ([t[:n] for t, n in zip(ts, kv)] for ts in full[1:])
-        out = Q.attn_paged_prefix(x.q, x.k_pages, x.v_pages, x.table, x.kv_lens, x.cu_q, q_len, max(full[0]), x.pages, x.len)
+        x.kv_lens_host = full[0]
+        out = Q.attn_paged_prefix(*x.shared())
+        x.kv_lens_host = kv
         check(x, out, before(True), joined=True)
         x.kv_lens_host, x.k, x.v = full
 
@@ -327,7 +344,7 @@ def test_prefix_is_read_from_its_own_table(Q):
         x = Shared([q_len] * 4, [100, 40, 61, 33], 640, 8, 2, 64, 16, F16)
         want = Q.attn_paged_prefix(*x.shared())
         x.table[:, :640 // 16] = 0x7FFFFFF0
-        assert torch.equal(want, Q.attn_paged_prefix(*x.shared()))
+        assert torch.equal(want, Q.attn_paged_prefix(*x.shared()))   # and no index is recorded
 
 
 def test_prefix_rows_streams_and_repeats(Q):
@@ -338,7 +355,7 @@ def test_prefix_rows_streams_and_repeats(Q):
         Q.attn_paged_prefix(*x.shared(), out=out)
         check(x, out, before(True), joined=True)
         assert (out[x.n_rows:] == 9.0).all()
-        floats = Q.paged_prefix_workspace_floats(6, x.q.shape[0], 8, 2, q_len, 2500, 2016, D)
+        floats = Q.paged_prefix_workspace_floats(6, x.q.shape[0], 8, 2, q_len, x.shared()[7], 1 << 19, D)
         ws = torch.full((floats,), float("nan"), device="cuda")
         torch.cuda.synchronize()
         s = torch.cuda.Stream()
@@ -361,8 +378,9 @@ def test_prefix_captured(Q, q_len):
     x = Shared([q_len] * 5, [400, 20, 33, 90, 250], 900, 8, 2, 128, 16, BF16)
     out = torch.empty_like(x.q)
     graph = torch.cuda.CUDAGraph()
+    args = x.shared()
     with torch.cuda.graph(graph):
-        Q.attn_paged_prefix(*x.shared(), out=out)
+        Q.attn_paged_prefix(*args, out=out)
     for n in (900, 64, 0, 560):
         x.len.fill_(n)
         x.q.normal_()
@@ -384,16 +402,17 @@ def test_prefix_nan_and_infinite_queries_stay_in_their_rows(Q):
 
 
 def test_prefix_refusals(Q):
-    x = Shared([1, 1], [30, 40], 100, 4, 2, 64, 16, F16)
+    x = Shared([1] * 4, [30, 40, 60, 70], 100, 4, 2, 64, 16, F16)
     i32 = dict(dtype=torch.int32, device="cuda")
     Q.attn_paged_prefix(*x.shared())
     for table, length, kw in ((x.pages.long(), x.len, {}), (x.pages.cpu(), x.len, {}), (x.pages, x.len.long(), {}),
                               (x.pages, torch.zeros(2, **i32), {}), (x.pages, None, {}), (x.pages, x.len, dict(max_prefix=-1)),
                               (x.pages, x.len, dict(max_prefix=7 * 16 + 1)), (x.pages, x.len, dict(out=x.q)),
-                              (x.pages[::2], x.len, {}), (x.pages, x.len, dict(scale=-1.0)),
-                              (x.pages, x.len, dict(workspace=torch.empty(8, device="cuda")))):
+                              (x.pages[::2], x.len, {}), (x.pages, x.len, dict(scale=-1.0))):
         with pytest.raises(Q.Q8AttnError):
             Q.attn_paged_prefix(*x.args(), table, length, **kw)
+    with pytest.raises(Q.Q8AttnError):
+        Q.attn_paged_prefix(*x.shared(), workspace=torch.empty(8, device="cuda"))
     with pytest.raises(Q.Q8AttnError):
         Q.paged_prefix_workspace_floats(2, 2, 4, 2, 1, 100, -1)
     with pytest.raises(Q.Q8AttnError):
@@ -407,6 +426,9 @@ def test_prefix_bad_pages_are_recorded(Q):
         got = Q.attn_paged_prefix(*x.shared())
         assert Q.device_status(clear=True)[0] == Q.Q8A_ERR_INVALID_ARG
         check(x, got, before(True), sequences=[1, 2], joined=True)
+        x.table[0, 30] = x.table[0, 31]
+        Q.attn_paged_prefix(*x.shared())
+        assert Q.device_status(clear=True)[0] == Q.Q8A_OK
         x.pages[3] = x.k_pages.shape[0]
         Q.attn_paged_prefix(*x.shared())
         assert Q.device_status(clear=True)[0] == Q.Q8A_ERR_INVALID_ARG
@@ -458,6 +480,7 @@ def test_a_server_of_these_calls(Q, D, dtype):
         x.k.append(rows[0].double())
         x.v.append(rows[1].double())
     x.q = torch.randn((6, heads, D), generator=g, device="cuda").to(dtype)
-    got = Q.attn_paged_prefix(x.q, k_pages, v_pages, table, lens, i32(0, 2, 3, 4, 6), 2, width * page, table[0, :6].contiguous(),
-                              i32(96))
-    check(x, got, before(True), joined=True)
+    args = (x.q, k_pages, v_pages, torch.cat([table, torch.zeros((B, 1 << 15), dtype=torch.int32, device="cuda")], 1), lens,
+            i32(0, 2, 3, 4, 6), 2, 1 << 19, torch.cat([table[0, :6], torch.zeros(1 << 15, dtype=torch.int32, device="cuda")]), i32(96))
+    for max_prefix in (1 << 19, 96):   # shared, and not
+        check(x, Q.attn_paged_prefix(*args, max_prefix=max_prefix), before(True), joined=True)
