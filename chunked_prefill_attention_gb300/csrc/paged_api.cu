@@ -125,23 +125,31 @@ constexpr int64_t kFewRows = 16;
 // A number of keys, cut to the most that a sequence can have.
 int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; }
 
-// Whether the few-row kernel takes a CTA per (sequence, K/V head) where the keys of a sequence are bounded: by a
-// window, or behind a prefix.  No second launch then, but the longest CTA sets the time.  Against shares of all tiles,
-// 8 K/V heads, single tokens, us: windows of 2,048 keys of 64 channels (8 tiles a warp) 13 and 15 for one sequence, 19
-// and 21 for 16; of 4,096 22 and 16, 31 and 27.  At 128 channels 1,024 keys 14 and 17, 20 and 25; 2,048 keys 23 and
-// 18, 33 and 31.  Where the units are whole waves of two CTAs an SM longer ones gain too: 38 sequences
-// (304 units) 35 and 51 (4,096 of 64 channels), 63 and 86 (of 128); 64 sequences (512 units, 84 % of two
-// waves) 65 and 69, 120 and 125.  Up to 40 tiles a warp: a batch with one long sequence waits 50 us for it.
-bool few_direct(int64_t batch, int32_t kv_heads, int64_t keys, int32_t head_dim) {
-  const int64_t units = batch * kv_heads, slots = 2 * 152;
-  const int64_t per_warp = (keys + 8 * (2048 / head_dim) - 1) / (8 * (2048 / head_dim));   // tiles of 32 or 16 keys
-  const int64_t waves = (units + slots - 1) / slots;
-  return units <= 0x7FFFFFFF && (per_warp <= 8 || (per_warp <= 40 && units * 100 >= waves * slots * 84));
+// Where the keys of a sequence are bounded, by a window or behind a prefix, the few-row kernel can take a cluster of
+// CTAs per (sequence, K/V head): no second launch then, but the longest unit sets the time.  The CTAs of a cluster, or 0:
+// shares of all tiles and a join.  As many as fit one wave of two CTAs an SM (the CTAs beyond cost a wave, and a
+// cluster's start) and have two tiles a warp.  Us of shares, 1, 2, 4, 8 CTAs, single tokens, 8 K/V heads:
+//   one sequence, windows of 1,024, 4,096, 16,384 keys of 64 channels   15  9  8  8  8 | 16 22 15 11 11 | 18 73 40 24 19
+//   4 sequences, 4,096 keys of 64, of 128 channels                      17 22 17 14 13 | 23 40 27 22 18
+//   16 sequences, 4,096                                                 26 31 21 28 46 | 46 60 38 47 69
+//   38 sequences (304 units)                                            51 35 43 64 104 | 86 64 73 100 150
+//   64 sequences (512 units, 84 % of two waves)                         69 65 72 99 170 | 125 121 124 155 244
+// Longer units than 8 tiles a warp only where they fill their waves, and up to 40: a batch with one long sequence
+// waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).
+int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t keys, int32_t head_dim) {
+  const int64_t units = batch * kv_heads, slots = 2 * 152, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
+  const int64_t tiles = (keys + keys_of_warps - 1) / keys_of_warps;   // of a warp of one CTA
+  int32_t ctas = 1;
+  while (ctas < 8 && units * 2 * ctas <= slots && tiles >= 4 * ctas) ctas *= 2;
+  const int64_t waves = (units * ctas + slots - 1) / slots, each = (tiles + ctas - 1) / ctas;
+  if (units * ctas > 0x7FFFFFFF) return 0;
+  return each <= 8 || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
 }
 
 // The launches of a call, from its bounds alone.
 struct Plan {
   bool few, direct, tiles;
+  int32_t cluster;
   q8a::TilesPlan t;
   int64_t few_rows;   // rows a K/V head of the few-row kernel's sequences, at most: it sizes its tiles
                       // and their partial states, so workspace and launch both take it from here
@@ -172,7 +180,8 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.direct = window ? few_direct(batch, kv_heads, few_kv, head_dim) : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
+  p.cluster = window ? few_cluster(batch, kv_heads, few_kv, head_dim) : 0;
+  p.direct = window ? p.cluster > 0 : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
@@ -311,6 +320,7 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
   if (int rc = check_workspace(fn, c, plan.floats, &a)) return rc;
   a.window = static_cast<int32_t>(window);
   a.sinks = static_cast<int32_t>(sinks);
+  a.cluster = plan.cluster;
   cudaError_t e = cudaSuccess;
   if (plan.tiles) {
     const q8a::PagedArgs b =
@@ -330,7 +340,7 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
 // over the prefix, whose join takes those states in.  Not `share`: attn_paged.
 struct PrefixPlan {
   bool share, own_few, own_direct;
-  int32_t join_rows;
+  int32_t join_rows, cluster;
   int64_t own_rows;
   q8a::TilesPlan own, prefix;
   int64_t state_floats, floats;
@@ -368,7 +378,8 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   p.own_rows = max_q * group;
   p.own_few = p.own_rows <= kFewRows;
   if (p.own_few) {
-    p.own_direct = few_direct(batch, kv_heads, own_kv, head_dim);
+    p.cluster = few_cluster(batch, kv_heads, own_kv, head_dim);
+    p.own_direct = p.cluster > 0;
     own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
   } else {
     // of many sequences the shares are planned here, from the keys that any of them can have
@@ -470,6 +481,7 @@ int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int6
   a.prefix_len = prefix_len;
   a.prefix_most = keys_at_most(max_prefix);
   a.state = workspace;
+  a.cluster = plan.cluster;
   a.part = workspace + plan.state_floats;
   cudaError_t e;
   if (plan.own_few) {

@@ -220,7 +220,26 @@ __device__ __forceinline__ float weight_of(float m, float l, float top) {
   return kMode == kPlain ? join_weight(m, top) : state_weight(m, l, top);
 }
 
-// kDirect: a CTA per unit, its tiles dealt to the eight warps, nothing left to join.
+// The CTAs of a cluster (kDirect, not kPlain).
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A word of another CTA's shared memory, at the place of this CTA's `addr`.
+__device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+
+// kDirect: a CTA per unit, its tiles dealt to the eight warps, nothing left to join; or (not kPlain) a cluster of CTAs
+// per unit, whose first one takes the others' states from their shared memory.
 // kMode: a window has two edges.  A key is hidden from a row behind either, so the keys that every row, or any
 // row, sees are the intervals' intersection and union; a tile of neither edge needs no mask.
 template <typename QT, int D, int NT, bool kDirect, int kMode>
@@ -242,6 +261,8 @@ paged_few_kernel(const PagedArgs a) {
   pdl_wait();
 
   const int start_key = kMode == kOwn ? prefix_keys(a) : 0;
+  const int ranks = kDirect && kMode != kPlain ? a.cluster : 1;
+  const int rank = kDirect && kMode != kPlain ? static_cast<int>(cluster_rank()) : 0;
   // ---- this warp's share of all key tiles: [pos, end) of the tiles laid end to end
   int64_t total, share, gw, pos0, pos, end, cta_end, base = 0;
   int b;
@@ -250,13 +271,13 @@ paged_few_kernel(const PagedArgs a) {
   float* parts = a.part + kMaxWarps * kDescInts;
   if (kDirect) {
     // tiles of this unit alone; a sequence has one row tile
-    b = blockIdx.x / a.kv_heads;
+    b = blockIdx.x / ranks / a.kv_heads;
     const auto un = units_of<D, NT, kMode>(a, read_seq(a, b), start_key);
     if (un.row_tiles == 0) return;   // uniform
     total = cta_end = un.tiles;
-    share = (un.tiles + kWarps - 1) / kWarps;
+    share = (un.tiles + ranks * kWarps - 1) / (ranks * kWarps);
     gw = pos0 = 0;
-    pos = warp * share;
+    pos = (rank * kWarps + warp) * share;
     end = i64min(total, pos + share);
     inner = true;
   } else {
@@ -330,7 +351,7 @@ paged_few_kernel(const PagedArgs a) {
     }
     const int64_t unit = ((inner ? pos0 : pos) - base) / un.tiles;
     const int tile0 = static_cast<int>(pos - base - unit * un.tiles);
-    const int kvh = kDirect ? static_cast<int>(blockIdx.x % a.kv_heads) : static_cast<int>(unit / un.row_tiles);
+    const int kvh = kDirect ? static_cast<int>(blockIdx.x / ranks % a.kv_heads) : static_cast<int>(unit / un.row_tiles);
     const int rt = kDirect ? 0 : static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
     const int n = static_cast<int>(inner ? i64max(0, end - pos) : i64min(un.tiles - tile0, end - pos));
     const int n_rows = sq.n_q * a.group;
@@ -781,6 +802,54 @@ paged_few_kernel(const PagedArgs a) {
         __syncthreads();
       }
       if (warp > 0) return;
+      if (kDirect && kMode != kPlain && ranks > 1) {
+        // the CTAs' states, in order; nobody leaves before they are read
+        if (rank > 0) {
+          float* dst = xch + lane;
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) dst[32 * i] = o[i / (4 * NT)][i / 4 % NT][i & 3];
+#pragma unroll
+          for (int i = 0; i < 2 * NT; ++i) {
+            dst[32 * (NREG + i)] = m[i / 2][i & 1];
+            dst[32 * (NREG + 2 * NT + i)] = l[i / 2][i & 1];
+          }
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank > 0) {
+          cluster_arrive();
+          cluster_wait();
+          return;
+        }
+        const uint32_t src = smem_u32(xch + lane);
+#pragma unroll 1
+        for (int k = 1; k < ranks; ++k) {
+          float v[NREG];
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) v[i] = cluster_load(src + 128 * i, k);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float wa[2], wb[2];
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const float mb = cluster_load(src + 128 * (NREG + 2 * nt + cc), k);
+              const float lb = cluster_load(src + 128 * (NREG + 2 * NT + 2 * nt + cc), k);
+              const float top = fmaxf(m[nt][cc], mb);
+              wa[cc] = weight_of<kMode>(m[nt][cc], l[nt][cc], top);
+              wb[cc] = weight_of<kMode>(mb, lb, top);
+              m[nt][cc] = top;
+              l[nt][cc] = fmaf(wa[cc], l[nt][cc], wb[cc] * lb);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[i][nt][e] = fmaf(wa[e & 1], o[i][nt][e], wb[e & 1] * v[(i * NT + nt) * 4 + e]);
+          }
+        }
+        cluster_arrive();
+        cluster_wait();
+      }
     }
     {
       const bool whole = inner ? tile0 == 0 && cta_end - pos0 == un.tiles : n == un.tiles;
@@ -1011,7 +1080,7 @@ cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  e = launch_kernel(kernel, dim3(ctas), dim3(kThreads), smem, stream, a);
+  e = launch_kernel_cluster(kernel, kDirect && kMode != kPlain ? a.cluster : 1, dim3(ctas), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess || kDirect) return e;
   return launch_kernel(paged_few_join_kernel<QT, D, NT, kMode>, dim3(ctas, kJoinY), dim3(kThreads), 0, stream, a);
 }
@@ -1021,7 +1090,7 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStre
   // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
   // of 106 at 64 channels, 277 instead of 198 at 128
   if (direct) {
-    const int ctas = a.batch * a.kv_heads;
+    const int ctas = a.batch * a.kv_heads * (kMode == kPlain ? 1 : a.cluster);
     return rows <= 8 ? launch_few<QT, D, 1, true, kMode>(a, ctas, stream) : launch_few<QT, D, 2, true, kMode>(a, ctas, stream);
   }
   int dev = 0, sms = 0;

@@ -199,7 +199,7 @@ def test_window_refusals(Q):
                dict(window=10, out=x.q), dict(window=10, workspace=torch.empty(0, device="cuda").half())):
         with pytest.raises(Q.Q8AttnError):
             Q.attn_paged_window(*x.args(), **kw)
-    long = Batch([1], [5000], 4, 2, 64, 16, F16)
+    long = Batch([20], [5000], 4, 2, 64, 16, F16)
     with pytest.raises(Q.Q8AttnError):
         Q.attn_paged_window(*long.args(), 4000, workspace=torch.empty(64, device="cuda"))
     none = Q.attn_paged_window(x.q[:0], *x.args()[1:5], torch.zeros(2, dtype=torch.int32, device="cuda"), 1, 100, 10)

@@ -193,7 +193,7 @@ def test_window_and_prefix_refusals(lib):
         assert call(batch=0) == call(total=0, q=P(0)) == call(max_q=0) == Q.Q8A_OK
     for kw in (dict(window=0), dict(window=-1), dict(sinks=-1)):
         assert window(**kw) == bad, kw
-    long = dict(max_kv=16 * 5000, width=5000, max_q=1, total=3, batch=3)
+    long = dict(max_kv=16 * 5000, width=5000, max_q=20, total=60, batch=3)
     assert window(window=30000, floats=10, **long) == bad and window(window=30000, ws=P(0), **long) == bad
     assert window(window=30000, ws=P(A[0].value + 64), **long) == bad and "overlap" in lib.q8a_last_error().decode()
     for kw in (dict(most=-1), dict(entries=-1), dict(entries=1 << 31), dict(most=161), dict(ptab=P(0)), dict(plen=P(0))):
