@@ -311,7 +311,7 @@ q8a::PagedArgs tiles_args(const q8a::PagedArgs& a, const q8a::TilesPlan& t, int3
   return b;
 }
 
-// attn_paged, or attn_paged_window where `window` is not 0.
+// attn_paged, or where `window` is not 0 attn_paged_window (not causal: of a window beyond every length).
 int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cudaStream_t st) {
   q8a::PagedArgs a{};
   if (int rc = check_call(fn, c, &a)) return rc;
@@ -337,14 +337,15 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
 }
 
 // A call behind a shared prefix: first the rows' states over their own keys (own_few or own), then all rows together
-// over the prefix, whose join takes those states in.  Not `share`: attn_paged.
+// over the prefix, whose join takes those states in.  Not `share`: attn_paged, or where clusters of the few-row
+// kernel take the call (4 sequences of 2,250 keys, 8 x 64: 16 us, 11 so) a window that hides nothing.
 struct PrefixPlan {
+  int64_t window;   // not `share`: run_paged's
   bool share, own_few, own_direct;
   int32_t join_rows, cluster;
   int64_t own_rows;
   q8a::TilesPlan own, prefix;
   int64_t state_floats, floats;
-  Plan plain;
 };
 // Sequences of more rows per K/V head than this fill the tiles of the tensor cores by themselves.
 constexpr int64_t kShareRows = 128;
@@ -368,8 +369,10 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   if (max_prefix > max_kv) max_prefix = max_kv;
   p.share = max_q * group <= kShareRows && share_pays(batch, total_q * group, max_q * group, kv_heads, max_prefix, head_dim);
   if (!p.share) {
-    p.plain = plan_paged(batch, total_q, max_q, group, kv_heads, max_kv, head_dim);
-    p.floats = p.plain.floats;
+    const Plan w = plan_paged(batch, total_q, max_q, group, kv_heads, max_kv, head_dim, q8a::kMaxKeys, 0);
+    const Plan plain = plan_paged(batch, total_q, max_q, group, kv_heads, max_kv, head_dim);
+    p.window = !w.tiles && w.direct && !plain.direct ? q8a::kMaxKeys : 0;
+    p.floats = p.window ? w.floats : plain.floats;
     return p;
   }
   // the own keys are those behind the prefix, as far as the bounds tell
@@ -475,7 +478,7 @@ int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int6
   if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))
     return refuse(Q8A_ERR_MISALIGNED, fn, "prefix_table and prefix_len need 4-byte alignment");
   const PrefixPlan plan = plan_prefix(batch, total_q, max_q, a.group, kv_heads, max_kv, max_prefix, head_dim);
-  if (!plan.share) return run_paged(fn, c, 0, 0, static_cast<cudaStream_t>(stream));
+  if (!plan.share) return run_paged(fn, c, plan.window, 0, static_cast<cudaStream_t>(stream));
   if (int rc = check_workspace(fn, c, plan.floats, &a)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.prefix_len = prefix_len;

@@ -24,9 +24,9 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // row is a new token's, and that token's thread writes the page's number into the table.
 //
 // A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no block waits
-// for another's results.  A step of few tokens is one block's.  Many tokens are dealt to blocks that write what
-// belongs to the tokens (kTokens); a second launch then writes the lengths and the number of free
-// pages (kLens), which may lie in the place of those that the first one reads.
+// for another's results.  Many tokens are dealt to blocks, the first of which writes the lengths and the number of free
+// pages too (kWhole); but where these lie in the place of those that the other blocks read, a second
+// launch does that (kTokens, then kLens).
 
 constexpr int kExtThreads = 1024;
 enum : int { kWhole, kTokens, kLens };
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtendArgs
     page0[tid] = static_cast<int32_t>(p - need - had);   // page i of the sequence is the free one page0 + i
     if (kPart != kLens && lead && have) a.cu_q[b + 1] = static_cast<int32_t>(i64min(r, a.total_q));
     __syncthreads();
-    if (kPart != kTokens && have) a.kv_out[b] = static_cast<int32_t>(granted ? kv + n : kv);
+    if (kPart != kTokens && lead && have) a.kv_out[b] = static_cast<int32_t>(granted ? kv + n : kv);
     const int64_t end = i64min(all_r, a.total_q);
     int half = 1;   // of the search: the sequences of this round are at most 2 * half
     while (2 * half < i64min(a.batch - b0, blockDim.x)) half *= 2;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtendArgs
     a.positions[t] = 0;
   }
   if (a.batch == 0) __syncthreads();
-  if (kPart != kTokens && tid == 0) a.n_free_out[0] = static_cast<int32_t>(n_free - taken);
+  if (kPart != kTokens && lead && tid == 0) a.n_free_out[0] = static_cast<int32_t>(n_free - taken);
   if (wrong) record_index(a.status);
 }
 
@@ -458,6 +458,8 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   if (a.total_q <= 4096)
     return launch_kernel(extend_kernel<kWhole>, dim3(1), dim3(a.batch <= 256 && a.total_q <= 1024 ? 256 : kExtThreads), 0, stream, a);
   const int64_t most = (a.total_q + kExtThreads - 1) / kExtThreads, blocks = most < 152 ? most : 152;
+  if (a.kv_out != a.kv_lens && a.n_free_out != a.n_free)
+    return launch_kernel(extend_kernel<kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(kExtThreads), 0, stream, a);
   const cudaError_t e = launch_kernel(extend_kernel<kTokens>, dim3(static_cast<unsigned>(blocks)), dim3(kExtThreads), 0, stream, a);
   return e != cudaSuccess ? e : launch_kernel(extend_kernel<kLens>, dim3(1), dim3(kExtThreads), 0, stream, a);
 }
