@@ -263,7 +263,10 @@ __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float* f) {
 // A thread keeps to one token, its two vectors and the heads of one tensor (a block's), so its angles are formed
 // once, and with them the weights: a pair becomes r (a A - b B), r (a C + b E), r the row's factor, with
 //   A = w_a cos t, B = w_b sin t, C = w_a sin t, E = w_b cos t
-// in registers.
+// in registers.  HBM bounds it: 16,384 tokens, 32 + 8 heads x 128 bf16, all channels turned in halves, 54 us, 91 % of the
+// copy rate; three axes, interleaved, 9,001 tokens, 24 + 24 x 64 fp16, 17 us, 95 %.  Folding the weights into the angles and
+// keeping to one tensor a block took the first from 113 to 57 us (the issue slots were 57 % busy), four heads in
+// flight instead of two to 54 (with three blocks an SM and two heads 57, one 65).
 template <typename T, int kD, bool kInter>
 __global__ void __launch_bounds__(256, 2)
 norm_rope_kernel(const NormRopeArgs a, int32_t heads_per_thread, int32_t q_groups) {
@@ -428,11 +431,12 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
     wide = wide && (a.x_stride[i] | a.out_stride[i]) % N == 0 &&
            (reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i])) % 16 == 0;
   if (wide) {
-    // as many heads a thread as leave every SM its threads
-    constexpr int64_t kThreads = 152 * 512;
+    // as many heads a thread as leave every SM most of its two blocks: 9,001 tokens, 24 + 24 heads x 64 fp16, 28 us with 4
+    // heads a thread, 21 with 8, 19 with 16, 17 with all 24; 16,384 tokens, 32 + 8 x 128 bf16, 67, 55, 55, 54
+    constexpr int64_t kThreads = 152 * 450;
     auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
     int hpt = 1;
-    while (hpt < 16 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads) hpt *= 2;
+    while (hpt < 32 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads) hpt *= 2;
     const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L), groups = groups_of(hpt);
     if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
     return launch_kernel(a.interleaved ? norm_rope_kernel<T, kD, true> : norm_rope_kernel<T, kD, false>,
