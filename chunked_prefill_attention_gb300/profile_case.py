@@ -48,7 +48,11 @@ With --paged few or tiles it runs attn_paged: single tokens of 16 sequences of
 32,768 keys (32 heads on 8, 128 channels; 1.1 GB of pages), or 9,728 tokens on
 16,384 keys (8 heads, --head-dim channels, no mask), three calls; --bf16 for bf16
 queries instead of fp16.  With --paged append it runs q8kv_append_paged: 16,384 tokens of
-32 heads of 64 channels, fp16, all rotated in interleaved pairs.
+32 heads of 64 channels, fp16, all rotated in interleaved pairs.  With --paged norm it runs
+attn_norm_rope: 16,384 tokens of 32 + 8 heads of 128 channels, bf16.  With --paged window it runs
+attn_paged_window: single tokens of 64 sequences of 8,192 keys in windows of 4,096 with 4 sinks; with
+--paged prefix attn_paged_prefix: single tokens of 64 sequences with 1,024 keys of their own behind a
+shared prefix of 32,768 (both 32 heads on 8, 128 channels, bf16).
 
   ncu --set full --clock-control none -k regex:paged_few_kernel -s 2 -c 1 \\
       python -m chunked_prefill_attention_gb300.profile_case --paged few
@@ -56,6 +60,12 @@ queries instead of fp16.  With --paged append it runs q8kv_append_paged: 16,384 
       python -m chunked_prefill_attention_gb300.profile_case --paged tiles
   ncu --set full --clock-control none -k regex:append_kernel -s 2 -c 1 \\
       python -m chunked_prefill_attention_gb300.profile_case --paged append
+  ncu --set full --clock-control none -k regex:norm_rope_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged norm
+  ncu --set full --clock-control none -k regex:paged_few_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged window
+  ncu --set full --clock-control none -k regex:paged_tiles_kernel -s 2 -c 1 \\
+      python -m chunked_prefill_attention_gb300.profile_case --paged prefix
 """
 
 import argparse
@@ -70,7 +80,7 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=16384)
     p.add_argument("--chunk", type=int, default=8192)
     p.add_argument("--index", type=int, default=1)
-    p.add_argument("--paged", choices=("few", "tiles", "append"))
+    p.add_argument("--paged", choices=("few", "tiles", "append", "norm", "window", "prefix"))
     p.add_argument("--bf16", action="store_true")
     p.add_argument("--reps", type=int, default=2)
     p.add_argument("--burst", type=int, default=0)
@@ -83,7 +93,7 @@ def main(argv=None):
     if a.pipelined:
         return pipelined(a)
     if a.paged:
-        return append(a) if a.paged == "append" else paged(a)
+        return {"append": append, "norm": norm, "window": ranges, "prefix": ranges}.get(a.paged, paged)(a)
     if a.burst > 0:
         return burst(a)
     if a.quantize > 0:
@@ -246,6 +256,65 @@ def append(a):
     torch.cuda.synchronize()
     us = ev[0].elapsed_time(ev[1]) / 6 * 1e3
     print(f"q8kv_append_paged: {us:.1f} us per call, {2 * T * H * (2 * D + Q.row_bytes(D)) / us / 1e3:.0f} GB/s")
+
+
+def norm(a):
+    import torch
+
+    from chunked_prefill_attention_gb300 import q8attn as Q
+
+    T, H, H_kv, D = 16384, 32, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn((T, H + 2 * H_kv, D), generator=g, device="cuda").bfloat16()
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    at, f = torch.arange(T, device="cuda"), Q.rope_inv_freq(D, device="cuda")
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for i in range(8):   # two first, so that the host runs ahead
+        if i == 2:
+            ev[0].record()
+        Q.attn_norm_rope(qkv[:, :H], qkv[:, H:H + H_kv], w, w, at, f)
+    ev[1].record()
+    torch.cuda.synchronize()
+    us = ev[0].elapsed_time(ev[1]) / 6 * 1e3
+    print(f"attn_norm_rope: {us:.1f} us per call, {4 * T * (H + H_kv) * D / us / 1e3:.0f} GB/s")
+
+
+def ranges(a):
+    import torch
+
+    from chunked_prefill_attention_gb300 import q8attn as Q
+
+    batch, H, H_kv, D, page = 64, 32, 8, 128, 64
+    prefix, own = (0, 8192) if a.paged == "window" else (32768, 1024)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    shared, each = prefix // page, own // page
+    n_pages = shared + batch * each
+    pages = [torch.empty((n_pages, H_kv, page, Q.row_bytes(D)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for first in range(0, n_pages, 512):
+        n = min(512, n_pages - first) * page
+        k, v = (torch.randn((n, H_kv, D), generator=g, device="cuda").half() for _ in range(2))
+        Q.q8kv_append_paged(k, v, *pages, first * page + torch.arange(n, device="cuda"))
+    table = torch.arange(shared, n_pages, dtype=torch.int32, device="cuda").view(batch, each)
+    head = torch.arange(shared, dtype=torch.int32, device="cuda")
+    table = torch.cat([head.expand(batch, -1), table], 1).contiguous()
+    lens = torch.full((batch,), prefix + own, dtype=torch.int32, device="cuda")
+    cu = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    q = torch.randn((batch, H, D), generator=g, device="cuda").bfloat16()
+    args = (q, *pages, table, lens, cu, 1, prefix + own)
+    length = torch.tensor([prefix], dtype=torch.int32, device="cuda")
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for i in range(8):
+        if i == 2:
+            ev[0].record()
+        if a.paged == "window":
+            Q.attn_paged_window(*args, 4096, 4)
+        else:
+            Q.attn_paged_prefix(*args, head, length)
+    ev[1].record()
+    torch.cuda.synchronize()
+    us = ev[0].elapsed_time(ev[1]) / 6 * 1e3
+    keys = batch * 4100 if a.paged == "window" else prefix + batch * own
+    print(f"attn_paged_{a.paged}: {us:.1f} us per call, {2 * keys * H_kv * Q.row_bytes(D) / us / 1e3:.0f} GB/s of Q8_0 KV")
 
 
 if __name__ == "__main__":
