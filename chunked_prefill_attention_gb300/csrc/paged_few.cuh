@@ -360,19 +360,22 @@ paged_few_kernel(const PagedArgs a) {
     // ---- copies of this warp's tiles
     const int32_t* table = a.table + b * a.table_stride;
     const int64_t head_off = (static_cast<int64_t>(kvh) << a.page_shift) * (RW * 4);
-    auto fetch = [&](int j) -> int {   // page of this lane's piece of tile j
-      const int key = key_of<kMode, KT>(span, tile0 + j) + (lane << piece_shift);
-      return (lane < pieces && j < n && key < sq.kv && piece_needed<kMode>(a, span, key, piece_shift)) ? table[key >> a.page_shift] : 0;
+    auto fetch = [&](int j, int key0) -> int {   // page of this lane's piece of tile j
+      const int key = key0 + (lane << piece_shift);
+      return (lane < pieces && j < n && key < sq.kv) ? table[key >> a.page_shift] : 0;
     };
     int issued = 0;
-    auto issue = [&](int j, int page) {
+    auto issue = [&](int j, int page, int key0) {
       if (j >= n || waiter.bad) return;
       issued = j + 1;
       const uint32_t c = it + j, s = c % kStages;
-      const int key0 = key_of<kMode, KT>(span, tile0 + j);
       const int have = max(0, min(pieces, (sq.kv - key0 + (1 << piece_shift) - 1) >> piece_shift));
-      const bool take = lane < have && piece_needed<kMode>(a, span, key0 + (lane << piece_shift), piece_shift);
-      const int copies = kMode == kWindow ? __popc(__ballot_sync(kFull, take)) : have;
+      bool take = lane < have;
+      int copies = have;
+      if (kMode == kWindow && key0 < span.low) {   // uniform: the sinks' tiles
+        take = take && piece_needed<kMode>(a, span, key0 + (lane << piece_shift));
+        copies = __popc(__ballot_sync(kFull, take));
+      }
       if (lane == 0) mbar_arrive_expect_tx(bar_u + 8 * s, 2 * copies * piece_bytes);
       __syncwarp();
       if (take) {
@@ -390,11 +393,12 @@ paged_few_kernel(const PagedArgs a) {
     {
       int pg[kStages];
 #pragma unroll
-      for (int j = 0; j < kStages; ++j) pg[j] = fetch(j);
+      for (int j = 0; j < kStages; ++j) pg[j] = fetch(j, key_of<kMode, KT>(span, tile0 + j));
 #pragma unroll
-      for (int j = 0; j < kStages; ++j) issue(j, pg[j]);
+      for (int j = 0; j < kStages; ++j) issue(j, pg[j], key_of<kMode, KT>(span, tile0 + j));
     }
-    int next_page = fetch(kStages);
+    int next_key = key_of<kMode, KT>(span, tile0 + kStages);
+    int next_page = fetch(kStages, next_key);
 
     // ---- Q^T fragments: lane (g, t) holds row 8 nt + g, the channels of its words
     uint32_t qf[Sh::QS ? 1 : NT][P][4][2];
@@ -742,8 +746,9 @@ paged_few_kernel(const PagedArgs a) {
           }
       }
       __syncwarp();
-      issue(j + kStages, next_page);
-      next_page = fetch(j + kStages + 1);
+      issue(j + kStages, next_page, kMode == kPlain ? (tile0 + j + kStages) * KT : next_key);
+      next_key = key_of<kMode, KT>(span, tile0 + j + kStages + 1);
+      next_page = fetch(j + kStages + 1, next_key);
     }
     it += n;
 

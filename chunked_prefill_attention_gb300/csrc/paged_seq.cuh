@@ -43,23 +43,22 @@ __device__ __forceinline__ int prefix_keys(const PagedArgs& a) {
   return static_cast<int>(i64max(0, i64min(n, a.prefix_most)) >> a.page_shift << a.page_shift);
 }
 
-// The key tiles of a run of rows: `sink` tiles from key 0 on, the others from key `base` on; `base` starts a
-// piece of a page (kPlain: all from key 0).
+// The key tiles of a run of rows: `sink` tiles from key 0 on, the others `skip` keys further on than they would be;
+// the first of these starts a piece of a page (kPlain: all from key 0 on).
 struct Span {
-  int32_t sink, base;
-  int32_t low;   // kWindow: the first key of the first row's window
+  int32_t sink, skip;
+  int32_t low;   // kWindow: where the pieces of the first row's window start
 };
-// Whether any row needs the piece of 2^shift keys from `key` on.  Those between the sinks and the window are not copied
-// (their pages may have been given away), so a tile has there whatever its buffer held.
-template <int kMode>
-__device__ __forceinline__ bool piece_needed(const PagedArgs& a, const Span& s, int key, int shift) {
-  return kMode != kWindow || key < a.sinks || key + (1 << shift) > s.low;
-}
 template <int kMode, int KT>
 __device__ __forceinline__ int key_of(const Span& s, int tile) {
   if (kMode == kPlain || kMode == kPrefix) return tile * KT;
-  if (kMode == kOwn) return s.base + tile * KT;
-  return tile < s.sink ? tile * KT : s.base + (tile - s.sink) * KT;
+  return tile * KT + (kMode == kWindow && tile < s.sink ? 0 : s.skip);
+}
+// Whether any row needs the piece that starts at `key`.  Those between the sinks and the window are not copied (their
+// pages may have been given away), so a tile has there whatever its buffer held.
+template <int kMode>
+__device__ __forceinline__ bool piece_needed(const PagedArgs& a, const Span& s, int key) {
+  return kMode != kWindow || key >= s.low || key < a.sinks;
 }
 // Of rows whose first token is at position p0 and whose last sees the keys before `end`; start: the first own key.
 template <int kMode, int KT>
@@ -67,17 +66,17 @@ __device__ __forceinline__ Span span_of(const PagedArgs& a, int64_t p0, int end,
   if (kMode == kOwn) return Span{0, start, 0};
   if (kMode != kWindow) return Span{0, 0, 0};
   Span s;
-  s.low = static_cast<int32_t>(i64max(0, p0 - a.window + 1));
-  s.base = s.low >> piece_shift << piece_shift;
+  s.low = static_cast<int32_t>(i64max(0, p0 - a.window + 1) >> piece_shift << piece_shift);
   s.sink = (max(0, min(a.sinks, end)) + KT - 1) / KT;
-  if (static_cast<int64_t>(s.sink) * KT >= s.base) s.sink = s.base = 0;   // one run
+  const int64_t skip = s.low - static_cast<int64_t>(s.sink) * KT;
+  s.skip = static_cast<int32_t>(i64max(0, skip));
+  if (skip <= 0) s.sink = 0;   // one run
   return s;
 }
 // Tiles that reach the keys before `end`.
 template <int kMode, int KT>
 __device__ __forceinline__ int span_tiles(const Span& s, int end) {
-  if (kMode == kPlain || kMode == kPrefix) return (max(end, 0) + KT - 1) / KT;
-  return s.sink + (max(end - s.base, 0) + KT - 1) / KT;
+  return (max(end - (kMode == kPlain || kMode == kPrefix ? 0 : s.skip), kMode == kWindow ? s.sink * KT : 0) + KT - 1) / KT;
 }
 
 // Weight of a partial state (reference m, sum l) under the joint reference top.  A row whose scores

@@ -391,7 +391,7 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
   const int64_t head_off = (static_cast<int64_t>(u.kvh) << a.page_shift) * G::RB;
   auto fetch = [&](int t) -> int {
     const int key = key_of<kMode, G::BN>(u.span, u.t0 + t) + (lane << shift);
-    return (lane < pieces && t < T && key < u.sq.kv && piece_needed<kMode>(a, u.span, key, shift)) ? table[key >> a.page_shift] : 0;
+    return (lane < pieces && t < T && key < u.sq.kv) ? table[key >> a.page_shift] : 0;
   };
   int page = fetch(0);
   int t = 0;
@@ -401,7 +401,7 @@ __device__ __forceinline__ void producer(const PagedArgs& a, const Unit& u, int 
     if (!wait_bar(bar(G::B_RAWEMPTY + s), ((t / G::NR) & 1) ^ 1, ctl, budget, a.status)) break;
     const int key0 = key_of<kMode, G::BN>(u.span, u.t0 + t);
     const int have = min(pieces, (u.sq.kv - key0 + (1 << shift) - 1) >> shift);   // > 0: the tile has a visible key
-    const bool take = lane < have && piece_needed<kMode>(a, u.span, key0 + (lane << shift), shift);
+    const bool take = lane < have && piece_needed<kMode>(a, u.span, key0 + (lane << shift));
     const int copies = kMode == kWindow ? __popc(__ballot_sync(kFull, take)) : have;
     if (lane == 0) mbar_arrive_expect_tx(bar(G::B_RAWFULL + s), 2 * copies * bytes);
     __syncwarp();
@@ -468,7 +468,7 @@ __device__ __forceinline__ void dequant_group(const PagedArgs& a, const Span& sp
   uint8_t* hi = tile + (blk >> 1) * G::ATOM + row * 128;
   uint8_t* lo = hi + G::TILE;
   const int chunk0 = odd ? 4 : 0;
-  if (row < kv - key0 && piece_needed<kMode>(a, span, key0 + (row >> shift << shift), shift)) {
+  if (row < kv - key0 && piece_needed<kMode>(a, span, key0 + (row >> shift << shift))) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(raw + row * G::RB) + 17 * (blk >> 1) + (odd ? 8 : 0);
     uint32_t c[9];
 #pragma unroll
