@@ -353,9 +353,10 @@ constexpr int64_t kShareRows = 128;
 // to 8 rows) 1, 1.35 for up to 16 rows, 2.4 in the tile kernel; read once, 2.4 for every 256 rows of the batch (what bounds the
 // tile kernel there is dequantisation, whose cost a byte is that much above the few-row kernel's).  The gain has to
 // outweigh the launches that sharing adds, 12 us, which is 3e7 channels, and twice that where the own keys are the tile
-// kernel's (32 rows a sequence, one K/V head, 128 channels, 64 sequences of 2,048 keys 40 and 32, of 8,192 44 and 70).  Shared and not, us (q rows a sequence): 8 K/V
-// heads, group 4, 64 channels, 4 sequences of 32,768 keys 38 and 36; 16 of 2,048 24 and 20, of 8,192 30 and 37,
-// of 32,768 39 and 102; 64 of 512 30 and 17, of 2,048 30 and 40, of 32,768 48 and 362; 128 channels, 64 of 32,768 74 and 726.
+// kernel's (32 rows a sequence, one K/V head, 128 channels, 64 sequences of 2,048 keys 40 and 32, of 8,192 44 and 70).  Shared and not, us: 8 K/V
+// heads, group 4, 64 channels, single tokens, 4 sequences of 32,768 keys 38 and 35; 16 of 2,048 24 and 20, of 8,192 23 and
+// 36, of 32,768 33 and 101; 64 of 512 30 and 17, of 2,048 29 and 39, of 32,768 47 and 361; 128 channels, 64 of
+// 32,768 72 and 724, 4 of 32,768 43 and 62.
 bool share_pays(int64_t batch, int64_t total_rows, int64_t max_rows, int32_t kv_heads, int64_t max_prefix, int32_t head_dim) {
   const double each = max_rows <= 8 ? 1.0 : max_rows <= kFewRows ? 1.35 : 2.4;
   const double units = static_cast<double>((total_rows + 255) / 256);

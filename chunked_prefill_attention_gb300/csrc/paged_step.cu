@@ -26,7 +26,9 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no block waits
 // for another's results.  Many tokens are dealt to blocks, the first of which writes the lengths and the number of free
 // pages too (kWhole); but where these lie in the place of those that the other blocks read, a second
-// launch does that (kTokens, then kLens).
+// launch does that (kTokens, then kLens).  On the device: 64 sequences, a token each, 2.4 us (with 1,024 threads instead of
+// 256 5.7); 1,000 sequences, 8,500 rows, 6.8; 48 prompts, 197,000 tokens, 6.8 (in place 10.9; one cluster of
+// eight blocks 36).
 
 constexpr int kExtThreads = 1024;
 enum : int { kWhole, kTokens, kLens };

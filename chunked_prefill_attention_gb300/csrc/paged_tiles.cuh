@@ -1,7 +1,7 @@
 // paged_tiles.cuh -- attention of many query rows per K/V head over a paged Q8_0
 // cache: prompts and chunks of prompts.
 //
-// The function is the one of paged_few.cu.  With hundreds of rows per key the
+// The function is the one of paged_few.cuh.  With hundreds of rows per key the
 // bound is the tensor cores, so the products run on tcgen05 with the
 // accumulators in TMEM:
 //   S = Q K_hi^T + Q K_lo^T,   O += P V_hi (+ P V_lo),
