@@ -360,8 +360,10 @@ paged_few_kernel(const PagedArgs a) {
     // ---- copies of this warp's tiles
     const int32_t* table = a.table + b * a.table_stride;
     const int64_t head_off = (static_cast<int64_t>(kvh) << a.page_shift) * (RW * 4);
+    // The first key of tile j; but for kPlain, where a product gives it, it is formed once, when its page is fetched.
+    auto first_key = [&](int j) { return key_of<kMode, KT>(span, tile0 + j); };
     auto fetch = [&](int j, int key0) -> int {   // page of this lane's piece of tile j
-      const int key = key0 + (lane << piece_shift);
+      const int key = (kMode == kPlain ? (tile0 + j) * KT : key0) + (lane << piece_shift);
       return (lane < pieces && j < n && key < sq.kv) ? table[key >> a.page_shift] : 0;
     };
     int issued = 0;
@@ -369,6 +371,7 @@ paged_few_kernel(const PagedArgs a) {
       if (j >= n || waiter.bad) return;
       issued = j + 1;
       const uint32_t c = it + j, s = c % kStages;
+      if (kMode == kPlain) key0 = (tile0 + j) * KT;
       const int have = max(0, min(pieces, (sq.kv - key0 + (1 << piece_shift) - 1) >> piece_shift));
       bool take = lane < have;
       int copies = have;
@@ -393,11 +396,11 @@ paged_few_kernel(const PagedArgs a) {
     {
       int pg[kStages];
 #pragma unroll
-      for (int j = 0; j < kStages; ++j) pg[j] = fetch(j, key_of<kMode, KT>(span, tile0 + j));
+      for (int j = 0; j < kStages; ++j) pg[j] = fetch(j, first_key(j));
 #pragma unroll
-      for (int j = 0; j < kStages; ++j) issue(j, pg[j], key_of<kMode, KT>(span, tile0 + j));
+      for (int j = 0; j < kStages; ++j) issue(j, pg[j], first_key(j));
     }
-    int next_key = key_of<kMode, KT>(span, tile0 + kStages);
+    int next_key = kMode == kPlain ? 0 : first_key(kStages);
     int next_page = fetch(kStages, next_key);
 
     // ---- Q^T fragments: lane (g, t) holds row 8 nt + g, the channels of its words
@@ -746,8 +749,8 @@ paged_few_kernel(const PagedArgs a) {
           }
       }
       __syncwarp();
-      issue(j + kStages, next_page, kMode == kPlain ? (tile0 + j + kStages) * KT : next_key);
-      next_key = key_of<kMode, KT>(span, tile0 + j + kStages + 1);
+      issue(j + kStages, next_page, next_key);
+      if (kMode != kPlain) next_key = first_key(j + kStages + 1);
       next_page = fetch(j + kStages + 1, next_key);
     }
     it += n;

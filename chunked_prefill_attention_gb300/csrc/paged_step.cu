@@ -438,18 +438,18 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
     constexpr int64_t kThreads = 152 * 450;
     auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
     int hpt = 1;
-    while (hpt < 32 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads) hpt *= 2;
+    while (groups_of(hpt) > 65535 || (hpt < 32 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads)) hpt *= 2;
     const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L), groups = groups_of(hpt);
-    if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch_kernel(a.interleaved ? norm_rope_kernel<T, kD, true> : norm_rope_kernel<T, kD, false>,
                          dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(256), 0, stream, a,
                          static_cast<int32_t>(hpt), static_cast<int32_t>((a.heads[0] + hpt - 1) / hpt));
   }
   constexpr int64_t kFill = 152 * 64;   // warps
   int hpw = 16;
-  while (hpw > 1 && a.n_tokens * ((heads + hpw - 1) / hpw) < kFill) hpw /= 2;
+  while (hpw > 2 && a.n_tokens * ((heads + hpw - 1) / hpw) < kFill) hpw /= 2;   // 2: at most 65,535 groups
   const int64_t blocks = (a.n_tokens + 7) / 8, groups = (heads + hpw - 1) / hpw;
-  if (blocks > 0x7FFFFFFF || groups > 65535) return cudaErrorInvalidValue;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_kernel(norm_rope_any_kernel<T, kD>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)),
                        dim3(256), 0, stream, a, static_cast<int32_t>(hpw));
 }

@@ -593,8 +593,38 @@ def attn_paged(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, s
     and kv_lens[b] keys (int32 [B], the new tokens' own keys last) in the pages block_table[b] (int32
     [B, width]).  max_q, max_kv: bounds of the rows and keys of a sequence.  `workspace`: fp32 CUDA tensor
     of paged_workspace_floats(...) elements (allocated here when None).  Returns [total_q, H, D]."""
-    return _attention("attn_paged", q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, (), scale,
-                      (1 if causal else 0,), out, workspace, paged_workspace_floats, ())
+    device = _device_of(q)
+    code, T, H, D, stride = _packed("q", q, device)
+    n_pages, kv_heads, page_tokens, head_dim, page_stride = _pool(k_pages, v_pages, device)
+    if D != head_dim:
+        _refuse(f"q has head_dim {D}, the pages {head_dim}")
+    if not (isinstance(block_table, torch.Tensor) and block_table.dtype == torch.int32 and block_table.dim() == 2 and
+            block_table.is_contiguous() and block_table.get_device() == device):
+        _refuse(f"block_table: a contiguous int32 tensor [batch, width] on cuda:{device} is needed")
+    B, width = block_table.shape
+    lens = _index("kv_lens", kv_lens, torch.int32, B, device)
+    cu = _index("cu_q", cu_q, torch.int32, B + 1, device)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif not (isinstance(out, torch.Tensor) and out.dtype == q.dtype and out.get_device() == device and
+              out.shape == q.shape and out.is_contiguous()):
+        _refuse(f"out: a contiguous tensor {(T, H, D)} of {q.dtype} on cuda:{device} is needed")
+    ws = floats = 0
+    if workspace is None:
+        floats = paged_workspace_floats(B, T, H, kv_heads, max_q, max_kv, D)
+        if floats:
+            workspace = torch.empty(floats, dtype=torch.float32, device=q.device)
+            ws = workspace.data_ptr()
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.float32 and
+              workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse(f"workspace: a contiguous fp32 tensor on cuda:{device} is needed")
+    else:
+        ws, floats = workspace.data_ptr(), workspace.numel()
+    _call(load().attn_paged, device, q.data_ptr(), code, stride, T, H, kv_heads, D, k_pages.data_ptr(),
+          v_pages.data_ptr(), n_pages, page_tokens, page_stride, block_table.data_ptr(), width, lens, cu, B, max_q,
+          max_kv, 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, out.data_ptr(),
+          ws, floats)
+    return out
 
 
 def _attention(name, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, max_kv, before, scale, after, out, workspace,

@@ -626,7 +626,8 @@ int q8kv_extend_paged(const int32_t *new_lens, const int32_t *kv_lens, int64_t b
  *                taken for 0); NULL with one axis.
  *   inv_freq, rot_dim, layout, mscale   as for attn_rope.
  * Numerics: fp32, rounded once to the type; the angles are those of attn_rope.  The sum of the
- * squares is fp32 too: a row with values beyond 2^60 gives 0 where the formula does not.
+ * squares is fp32 too: a row with values beyond 2^60 gives 0 where the formula does not, and one with none
+ * above 2^-60 loses bits where eps does not outweigh its squares.
  * Errors: as attn_rope.
  */
 int attn_norm_rope(const void *q, void *q_out, int32_t heads, int64_t q_token_stride,

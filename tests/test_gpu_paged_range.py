@@ -8,12 +8,11 @@ off by 2^-24 of itself and by log2's 2^-23, at most 2^-24 (1.5 G + 32) + 2^-23 f
 
 import math
 
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_paged import BF16, F16, Batch, clean_status, gen, rows_of, unit   # noqa: F401  (a fixture among them)
+from tests.test_gpu_paged import BF16, F16, Batch, clean_status, gen, unit   # noqa: F401  (a fixture among them)
 
 pytestmark = pytest.mark.gpu
 
@@ -447,7 +446,8 @@ def test_a_server_of_these_calls(Q, D, dtype):
     width, n_pages = 20, 100
     k_pages, v_pages = (torch.zeros((n_pages, kv, page, D // 32 * 34), dtype=torch.uint8, device="cuda") for _ in range(2))
     table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
-    free, n_free, lens = torch.randperm(n_pages, generator=g, device="cuda").int(), i32(n_pages), torch.zeros(B, **dict(dtype=torch.int32, device="cuda"))
+    free = torch.randperm(n_pages, generator=g, device="cuda").int()
+    n_free, lens = i32(n_pages), torch.zeros(B, dtype=torch.int32, device="cuda")
     qw, kw = ((1 + 0.1 * torch.randn(D, generator=g, device="cuda")).to(dtype) for _ in range(2))
     x = Batch.__new__(Batch)
     x.group, x.D, x.page = heads // kv, D, page

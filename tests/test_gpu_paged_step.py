@@ -360,6 +360,19 @@ def test_norm_rope_far_apart_tokens(Q):
     assert y.shape == none.shape
 
 
+@pytest.mark.parametrize("odd", [False, True])
+def test_norm_rope_most_heads(Q, odd):
+    """The most heads of queries and keys that the call takes, one token."""
+    D, n = 64, 65535
+    flat = torch.randn(2 * n * D + 1, generator=gen(9), device="cuda").half()
+    flat = flat[1:] if odd else flat[:-1]
+    q, k = flat[:n * D].view(1, n, D), flat[n * D:].view(1, n, D)
+    pos, f, w = torch.tensor([77], device="cuda"), Q.rope_inv_freq(D, device="cuda"), torch.ones(D, device="cuda")
+    got = Q.attn_norm_rope(q, k, w, w, pos, f)
+    for y, x in zip(got, (q, k)):
+        near(y, *norm_rope64(x, w, pos, f, None, 1e-6, False))
+
+
 def test_norm_rope_bad_axis(Q):
     """An axis that does not exist is recorded and taken for axis 0."""
     q = torch.randn((2, 1, 64), generator=gen(6), device="cuda")
