@@ -133,6 +133,7 @@ struct PagedArgs {
   const int32_t* prefix_len;  // [1] on the device
   int64_t prefix_most;        // what it may be at most
   int32_t seqs;               // kPrefix: sequences of kv_lens and cu_q (batch is 1)
+  int32_t row_tiles;          // few-row kernel, direct, kWindow and kOwn: tiles of 16 rows (8 where one is enough) of a unit
   int32_t cluster;            // few-row kernel, direct, kWindow and kOwn: CTAs of a unit (1, 2, 4 or 8)
   int32_t join_rows;          // kPrefix: rows of a block of the join, 8 (a warp each) or 1
   float* state;               // [total_q][heads][D] and then [total_q][heads]: outputs over the own keys,

@@ -146,10 +146,23 @@ int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t keys, int32_t head_
   return each <= 8 || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
 }
 
+// Whether sequences of more than 16 rows per K/V head, with bounded keys, go to the few-row kernel as well, a cluster for
+// every 16 rows: it reads the keys again for each, but needs neither the tile kernel's start nor its join.  Tile kernel and
+// few-row kernel, us, 8 K/V heads; windows of 512, 1,024, 4,096 keys:
+//   32 rows, 64 channels: one sequence 21 14 | 19 16 | 23 20; 4: 23 14 | 21 18 | 28 24; 16: 28 16 | 36 21 | 62 45;
+//     64: 104 52 | 123 64 | 225 150.  128 channels: 20 17 | 21 23 | 27 35; 21 21 | 23 26 | 32 39; 36 25 | 43 33 | 86 88;
+//     123 80 | 150 114 | 307 294
+//   64 rows, 64 channels: 22 15 | 20 17 | 23 27; 24 16 | 21 20 | 28 30; 30 29 | 38 40 | 64 87; 112 98 | 132 123 | 235 291.
+//     128 channels: 21 18 | 22 25 | 27 36; 40 44 | 46 62 | 89 167 (16)
+bool few_takes(int64_t rows, int64_t units, int64_t keys, int32_t head_dim) {
+  if (rows <= 32) return head_dim == 64 || keys <= 640 || units >= 128;
+  return rows <= 64 && head_dim == 64 && keys <= 640;
+}
+
 // The launches of a call, from its bounds alone.
 struct Plan {
   bool few, direct, tiles;
-  int32_t cluster;
+  int32_t cluster, row_tiles;
   q8a::TilesPlan t;
   int64_t few_rows;   // rows a K/V head of the few-row kernel's sequences, at most: it sizes its tiles
                       // and their partial states, so workspace and launch both take it from here
@@ -169,6 +182,18 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
     max_kv = q8a::window_tiles(max_kv, window, sinks, static_cast<int32_t>(group), max_q * group <= 128, head_dim) * bn;
   }
   p.tiles = max_q * group > kFewRows;
+  p.row_tiles = 1;
+  if (window && p.tiles && few_takes(max_q * group, batch * kv_heads, few_kv, head_dim)) {
+    const int32_t row_tiles = static_cast<int32_t>((max_q * group + kFewRows - 1) / kFewRows);
+    p.cluster = few_cluster(batch, kv_heads * row_tiles, few_kv, head_dim);
+    if (p.cluster > 0) {
+      p.tiles = false;
+      p.few = p.direct = true;
+      p.row_tiles = row_tiles;
+      p.few_rows = max_q * group;
+      return p;
+    }
+  }
   if (p.tiles) p.t = q8a::plan_paged_tiles(batch, total_q * group, max_q * group, kv_heads, max_kv, head_dim);
   // The tile kernel takes every sequence of a call of at most 128 rows each (one of few
   // rows costs it no more than one of many, the other kernel's launches 8 us), and of a
@@ -321,6 +346,7 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
   a.window = static_cast<int32_t>(window);
   a.sinks = static_cast<int32_t>(sinks);
   a.cluster = plan.cluster;
+  a.row_tiles = plan.row_tiles;
   cudaError_t e = cudaSuccess;
   if (plan.tiles) {
     const q8a::PagedArgs b =
@@ -342,7 +368,7 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
 struct PrefixPlan {
   int64_t window;   // not `share`: run_paged's
   bool share, own_few, own_direct;
-  int32_t join_rows, cluster;
+  int32_t join_rows, cluster, row_tiles;
   int64_t own_rows;
   q8a::TilesPlan own, prefix;
   int64_t state_floats, floats;
@@ -380,9 +406,12 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   const int64_t own_kv = max_kv > max_prefix ? max_kv - max_prefix : max_kv;
   int64_t own_floats = 0;
   p.own_rows = max_q * group;
-  p.own_few = p.own_rows <= kFewRows;
+  p.row_tiles = 1;
+  // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so)
+  if (p.own_rows > kFewRows && p.own_rows <= 32 && head_dim == 64 && own_kv <= 1100) p.row_tiles = 2;
+  p.cluster = few_cluster(batch, kv_heads * p.row_tiles, own_kv, head_dim);
+  p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster > 0);
   if (p.own_few) {
-    p.cluster = few_cluster(batch, kv_heads, own_kv, head_dim);
     p.own_direct = p.cluster > 0;
     own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
   } else {
@@ -486,6 +515,7 @@ int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int6
   a.prefix_most = keys_at_most(max_prefix);
   a.state = workspace;
   a.cluster = plan.cluster;
+  a.row_tiles = plan.row_tiles;
   a.part = workspace + plan.state_floats;
   cudaError_t e;
   if (plan.own_few) {

@@ -261,8 +261,10 @@ paged_few_kernel(const PagedArgs a) {
   pdl_wait();
 
   const int start_key = kMode == kOwn ? prefix_keys(a) : 0;
-  const int ranks = kDirect && kMode != kPlain ? a.cluster : 1;
-  const int rank = kDirect && kMode != kPlain ? static_cast<int>(cluster_rank()) : 0;
+  // CTAs and row tiles of a unit; they are read where they are needed, since the registers of the main loop are few
+  constexpr bool kCluster = kDirect && kMode != kPlain;
+  auto ranks = [&] { return kCluster ? a.cluster : 1; };
+  auto unit_of = [&] { return kCluster ? blockIdx.x / a.cluster : blockIdx.x; };   // of row tiles
   // ---- this warp's share of all key tiles: [pos, end) of the tiles laid end to end
   int64_t total, share, gw, pos0, pos, end, cta_end, base = 0;
   int b;
@@ -271,13 +273,13 @@ paged_few_kernel(const PagedArgs a) {
   float* parts = a.part + kMaxWarps * kDescInts;
   if (kDirect) {
     // tiles of this unit alone; a sequence has one row tile
-    b = blockIdx.x / ranks / a.kv_heads;
+    b = unit_of() / (kCluster ? a.row_tiles : 1) / a.kv_heads;
     const auto un = units_of<D, NT, kMode>(a, read_seq(a, b), start_key);
-    if (un.row_tiles == 0) return;   // uniform
+    if ((kCluster ? static_cast<int>(unit_of() % a.row_tiles) : 0) >= un.row_tiles) return;   // uniform
     total = cta_end = un.tiles;
-    share = (un.tiles + ranks * kWarps - 1) / (ranks * kWarps);
+    share = (un.tiles + ranks() * kWarps - 1) / (ranks() * kWarps);
     gw = pos0 = 0;
-    pos = (rank * kWarps + warp) * share;
+    pos = ((kCluster ? static_cast<int>(cluster_rank()) : 0) * kWarps + warp) * share;
     end = i64min(total, pos + share);
     inner = true;
   } else {
@@ -351,8 +353,9 @@ paged_few_kernel(const PagedArgs a) {
     }
     const int64_t unit = ((inner ? pos0 : pos) - base) / un.tiles;
     const int tile0 = static_cast<int>(pos - base - unit * un.tiles);
-    const int kvh = kDirect ? static_cast<int>(blockIdx.x / ranks % a.kv_heads) : static_cast<int>(unit / un.row_tiles);
-    const int rt = kDirect ? 0 : static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles);
+    const int kvh = kDirect ? static_cast<int>(unit_of() / (kCluster ? a.row_tiles : 1) % a.kv_heads) : static_cast<int>(unit / un.row_tiles);
+    const int rt = !kDirect ? static_cast<int>(unit - static_cast<int64_t>(kvh) * un.row_tiles)
+                            : kCluster ? static_cast<int>(unit_of() % a.row_tiles) : 0;
     const int n = static_cast<int>(inner ? i64max(0, end - pos) : i64min(un.tiles - tile0, end - pos));
     const int n_rows = sq.n_q * a.group;
     const Span span = few_span<D, NT, kMode>(a, sq, start_key);
@@ -810,7 +813,8 @@ paged_few_kernel(const PagedArgs a) {
         __syncthreads();
       }
       if (warp > 0) return;
-      if (kDirect && kMode != kPlain && ranks > 1) {
+      if (kCluster && ranks() > 1) {
+        const int rank = static_cast<int>(cluster_rank());
         // the CTAs' states, in order; nobody leaves before they are read
         if (rank > 0) {
           float* dst = xch + lane;
@@ -831,10 +835,7 @@ paged_few_kernel(const PagedArgs a) {
         }
         const uint32_t src = smem_u32(xch + lane);
 #pragma unroll 1
-        for (int k = 1; k < ranks; ++k) {
-          float v[NREG];
-#pragma unroll
-          for (int i = 0; i < NREG; ++i) v[i] = cluster_load(src + 128 * i, k);
+        for (int k = 1; k < ranks(); ++k) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float wa[2], wb[2];
@@ -848,11 +849,16 @@ paged_few_kernel(const PagedArgs a) {
               m[nt][cc] = top;
               l[nt][cc] = fmaf(wa[cc], l[nt][cc], wb[cc] * lb);
             }
+            // 16 words in flight: all of a state's beside O's own would spill
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int i = 0; i < D / 16; i += 4) {
+              float v[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[i][nt][e] = fmaf(wa[e & 1], o[i][nt][e], wb[e & 1] * v[(i * NT + nt) * 4 + e]);
+              for (int e = 0; e < 16; ++e) v[e] = cluster_load(src + 128 * (((i + e / 4) * NT + nt) * 4 + e % 4), k);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[i + e / 4][nt][e % 4] = fmaf(wa[e & 1], o[i + e / 4][nt][e % 4], wb[e & 1] * v[e]);
+            }
           }
         }
         cluster_arrive();
@@ -1098,7 +1104,7 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStre
   // tiles of 8 or 16 rows: 16 cost 16 sequences of 32,768 keys (8 K/V heads) 142 us instead
   // of 106 at 64 channels, 277 instead of 198 at 128
   if (direct) {
-    const int ctas = a.batch * a.kv_heads * (kMode == kPlain ? 1 : a.cluster);
+    const int ctas = a.batch * a.kv_heads * (kMode == kPlain ? 1 : a.cluster * a.row_tiles);
     return rows <= 8 ? launch_few<QT, D, 1, true, kMode>(a, ctas, stream) : launch_few<QT, D, 2, true, kMode>(a, ctas, stream);
   }
   int dev = 0, sms = 0;
