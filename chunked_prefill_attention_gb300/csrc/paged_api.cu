@@ -134,13 +134,15 @@ int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; 
 //   16 sequences, 4,096                                                 26 31 21 28 46 | 46 60 38 47 69
 //   38 sequences (304 units)                                            51 35 43 64 104 | 86 64 73 100 150
 //   64 sequences (512 units, 84 % of two waves)                         69 65 72 99 170 | 125 121 124 155 244
+// Of more than 8 rows at most four CTAs, whose states are twice as large (one sequence of 16 rows, 4,096 keys of 64 channels,
+// 1, 2, 4, 8 CTAs 31 21 18 19; 4 sequences 34 27 23 26; 2,048 keys of 128 channels 36 27 25 29, 36 30 28 34).
 // Longer units than 8 tiles a warp only where they fill their waves, and up to 40: a batch with one long sequence
 // waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).
-int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t keys, int32_t head_dim) {
+int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim) {
   const int64_t units = batch * kv_heads, slots = 2 * 152, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
   const int64_t tiles = (keys + keys_of_warps - 1) / keys_of_warps;   // of a warp of one CTA
   int32_t ctas = 1;
-  while (ctas < 8 && units * 2 * ctas <= slots && tiles >= 4 * ctas) ctas *= 2;
+  while (ctas < (rows <= 8 ? 8 : 4) && units * 2 * ctas <= slots && tiles >= 4 * ctas) ctas *= 2;
   const int64_t waves = (units * ctas + slots - 1) / slots, each = (tiles + ctas - 1) / ctas;
   if (units * ctas > 0x7FFFFFFF) return 0;
   return each <= 8 || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
@@ -185,7 +187,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   p.row_tiles = 1;
   if (window && p.tiles && few_takes(max_q * group, batch * kv_heads, few_kv, head_dim)) {
     const int32_t row_tiles = static_cast<int32_t>((max_q * group + kFewRows - 1) / kFewRows);
-    p.cluster = few_cluster(batch, kv_heads * row_tiles, few_kv, head_dim);
+    p.cluster = few_cluster(batch, kv_heads * row_tiles, max_q * group, few_kv, head_dim);
     if (p.cluster > 0) {
       p.tiles = false;
       p.few = p.direct = true;
@@ -205,7 +207,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.cluster = window ? few_cluster(batch, kv_heads, few_kv, head_dim) : 0;
+  p.cluster = window ? few_cluster(batch, kv_heads, max_q * group, few_kv, head_dim) : 0;
   p.direct = window ? p.cluster > 0 : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
@@ -409,7 +411,7 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   p.row_tiles = 1;
   // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so)
   if (p.own_rows > kFewRows && p.own_rows <= 32 && head_dim == 64 && own_kv <= 1100) p.row_tiles = 2;
-  p.cluster = few_cluster(batch, kv_heads * p.row_tiles, own_kv, head_dim);
+  p.cluster = few_cluster(batch, kv_heads * p.row_tiles, p.own_rows, own_kv, head_dim);
   p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster > 0);
   if (p.own_few) {
     p.own_direct = p.cluster > 0;
