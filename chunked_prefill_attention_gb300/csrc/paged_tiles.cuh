@@ -271,11 +271,6 @@ constexpr int kPlanned = 64;   // most sequences of a call whose shares are plan
 template <int D, bool kPair, int kMode>
 __device__ __forceinline__ int plan_shares(const PagedArgs& a, int lane) {
   if (a.share_tiles > 0) return a.share_tiles;
-  if (kMode == kPrefix) {   // one sequence: every unit has the same tiles, cut so that the grid is filled once
-    const Load one = load_of<D, kPair, kMode>(a, 0);
-    const int parts = static_cast<int>(max(static_cast<int64_t>(1), a.ctas / (static_cast<int64_t>(max(one.units, 1)) * a.kv_heads)));
-    return max(4, (one.tiles + parts - 1) / parts);
-  }
   Load mine[kPlanned / 32];
   int top = 0;
 #pragma unroll
@@ -346,6 +341,28 @@ __device__ __forceinline__ void locate(const PagedArgs& a, int64_t x, int per, C
     ctl->first = static_cast<int32_t>(first);
     if (found >= 0) ctl->sq = seq_at<kMode>(a, found);
   }
+}
+
+// kPrefix: every unit has the same tiles, cut so that the grid is filled once, and block x of the grid, or pair x of row
+// unit and K/V head, follows from the prefix's length alone.
+template <int D, bool kPair, bool kShares>
+__device__ __forceinline__ void locate_prefix(const PagedArgs& a, int64_t x, Ctl* ctl) {
+  using G = Geo<D, kPair>;
+  const int64_t units = (a.total_q * a.group + G::ROWS - 1) / G::ROWS, pairs = units * a.kv_heads;
+  const Seq sq = seq_at<kPrefix>(a, 0);
+  const int tiles = (sq.kv + G::BN - 1) / G::BN;
+  const int parts = static_cast<int>(i64max(1, a.ctas / pairs));
+  const int per = a.share_tiles > 0 ? a.share_tiles : max(4, (tiles + parts - 1) / parts);
+  const int shares = (tiles + per - 1) / per;
+  const int64_t pair = kShares ? (shares > 0 ? x / shares : pairs) : x;
+  const int unit = static_cast<int>(pair / a.kv_heads);
+  ctl->b = pair < pairs ? 0 : -1;
+  ctl->unit = unit;
+  ctl->kvh = static_cast<int>(pair - static_cast<int64_t>(unit) * a.kv_heads);
+  ctl->share = kShares ? static_cast<int>(x - pair * shares) : 0;
+  ctl->per = per;
+  ctl->first = static_cast<int32_t>(pair * shares);
+  ctl->sq = sq;
 }
 
 // Step n <-> (key tile t, tile x), the key tiles counted from t0: A and B in turn, then the
@@ -844,7 +861,9 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
   const int warp = threadIdx.x >> 5, wg = warp >> 2;
   if (warp == 0) {
     const int lane = threadIdx.x & 31;
-    if (kPair || kMode == kPrefix || a.shares)
+    if (kMode == kPrefix) {
+      if (lane == 0) locate_prefix<D, kPair, true>(a, blockIdx.x, ctl);
+    } else if (kPair || a.shares)
       locate<D, kPair, kMode, true>(a, blockIdx.x, plan_shares<D, kPair, kMode>(a, lane), ctl, lane);
     else
       locate<D, kPair, kMode, false>(a, blockIdx.x, 0x3FFFFFFF, ctl, lane);
@@ -910,13 +929,19 @@ __global__ void __launch_bounds__(Geo<D, kPair>::kThreads, 1) paged_tiles_kernel
 // Joins the shares of a unit's rows, a warp per row, in order; behind a prefix also the row's state over its own keys.
 template <typename QT, int D, bool kPair, int kMode>
 __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a) {
-  __shared__ Ctl ctl;
+  __shared__ Ctl shared_ctl;
   __shared__ float sums[kMode == kPrefix ? 8 : 1][D + 1];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) locate<D, kPair, kMode, false>(a, blockIdx.x, plan_shares<D, kPair, kMode>(a, lane), &ctl, lane);
-  __syncthreads();
+  Ctl own_ctl;   // kPrefix: every thread's, in registers
+  Ctl& ctl = kMode == kPrefix ? own_ctl : shared_ctl;
+  if (kMode == kPrefix) {
+    locate_prefix<D, kPair, false>(a, blockIdx.x, &ctl);
+  } else {
+    if (warp == 0) locate<D, kPair, kMode, false>(a, blockIdx.x, plan_shares<D, kPair, kMode>(a, lane), &ctl, lane);
+    __syncthreads();
+  }
   if (ctl.b < 0) return;
   const Unit u = make_unit<D, kPair, kMode>(a, &ctl, 0);
   // kPrefix with few rows: a block per row, its warps deal the states out among themselves
@@ -924,6 +949,17 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   const int in_unit = one ? blockIdx.y : blockIdx.y * 8 + warp;
   const int row = u.r0 + in_unit;
   if (row >= u.n_rows) return;
+  const int tok = row / a.group;
+  const int64_t out_row = (u.sq.q0 + tok) * a.heads + u.kvh * a.group + row - tok * a.group;
+  // kPrefix: the row's state over its own keys, on its way before the prefix's length is needed
+  float own = 0.0f, own_y[D / 32];
+  bool in_seq = true;
+  if (kMode == kPrefix) {
+    in_seq = tok >= a.cu_q[0] && tok < a.cu_q[a.seqs];
+    own = a.state[a.total_q * a.heads * D + out_row];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) own_y[i] = a.state[out_row * D + 32 * i + lane];
+  }
   const int tiles = tiles_of<D, kPair, kMode>(a, u.sq, u.span, u.r0 + in_unit / BM * BM, u.n_rows);
   // states of this row's tile: one for each share with key tiles of it (tile in_unit / 128 of
   // the CTA's two); in pairs two, but one for a share of a single key tile
@@ -937,8 +973,6 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
   const int64_t step = two ? BM : 2 * BM;
   const int64_t at0 = static_cast<int64_t>(ctl.first) * 2 * BM + in_unit;
   const float2* ml = reinterpret_cast<const float2*>(a.part + a.part_ml);
-  const int tok = row / a.group;
-  const int64_t out_row = (u.sq.q0 + tok) * a.heads + u.kvh * a.group + row - tok * a.group;
   float top = -INFINITY;
   float l = 0.0f, y[D / 32] = {};
   if (kMode == kPlain) {
@@ -954,13 +988,7 @@ __global__ void __launch_bounds__(256) paged_tiles_join_kernel(const PagedArgs a
     }
   } else {
     // the states' references and sums a lane each, then their values, eight in flight
-    float own = 0.0f, own_y[D / 32];
-    if (kMode == kPrefix) {
-      if (tok < a.cu_q[0] || tok >= a.cu_q[a.seqs]) return;   // a row of no sequence stays as it is
-      own = a.state[a.total_q * a.heads * D + out_row];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) own_y[i] = a.state[out_row * D + 32 * i + lane];
-    }
+    if (!in_seq) return;   // a row of no sequence stays as it is
 #pragma unroll 4
     for (int z = lane; z < n; z += 32) top = fmaxf(top, ml[at0 + z * step].x);
 #pragma unroll
