@@ -1,7 +1,7 @@
 // paged_tiles_prefix.cu -- the launches of the tile kernel (paged_tiles.cuh) over a shared prefix and over the keys
 // behind it.  The rows of the whole batch (tokens x heads of a group) fill its tiles, so a key of the prefix is
 // dequantised once for every 256 rows instead of once a sequence.  64 single tokens, 8 x 128 bf16, 32,768 keys: 47 us
-// (1.3 us a tile of 64 keys, 14 us to start and end), and 6 us for the join; 16 bursts of 2 to 8 tokens, 8 x 64 fp16,
+// (1.3 us a tile of 64 keys, 14 us to start and end), and 5 us for the join; 16 bursts of 2 to 8 tokens, 8 x 64 fp16,
 // 100,001 keys (320 rows, two units): 136 us, 1.1 us a tile of 96.
 
 #include "paged_tiles.cuh"
