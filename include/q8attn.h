@@ -587,9 +587,11 @@ int64_t q8a_paged_prefix_workspace_floats(int64_t batch, int64_t total_q, int32_
  * free pages, dealt to the sequences in order (their numbers go into its row of the table).
  * What comes out is what q8kv_append_paged and attn_paged take.
  *   new_lens, kv_lens  int32 [batch]; 0 new tokens are allowed.
- *   block_table        int32 [batch][table_stride]; only the entries of new pages are written.
+ *   block_table        int32 [batch][table_stride]; only the entries of new pages are written.  A
+ *                      sequence's last page, where it is not full, must be its own: its new tokens go there.
  *   free_pages         int32 [free_capacity], a stack: n_free[0] page numbers, the next one last;
- *                      it is not written.  n_free: int32 [1].
+ *                      it is not written (pages that come back are put on top by the caller, and
+ *                      counted).  n_free: int32 [1].
  *   total_q            rows of the packed tensors: at least the sum of new_lens; those
  *                      behind the last sequence get slot -1 and position 0 (padding).
  *   kv_lens_out        int32 [batch], may be kv_lens.  n_free_out: int32 [1], may be n_free.
