@@ -433,13 +433,20 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
     wide = wide && (a.x_stride[i] | a.out_stride[i]) % N == 0 &&
            (reinterpret_cast<uintptr_t>(a.x[i]) | reinterpret_cast<uintptr_t>(a.out[i])) % 16 == 0;
   if (wide) {
-    // as many heads a thread as leave every SM most of its two blocks: 9,001 tokens, 24 + 24 heads x 64 fp16, 28 us with 4
-    // heads a thread, 21 with 8, 19 with 16, 17 with all 24; 16,384 tokens, 32 + 8 x 128 bf16, 67, 55, 55, 54
-    constexpr int64_t kThreads = 152 * 450;
+    // The fewest heads a thread with which the blocks are one wave, two an SM: every block starts with its
+    // angles, and a few blocks beyond a wave cost another.  32 + 8 heads x 128 bf16, us with 1, 2, 3, 5, 8, 12, 16, 24, 32:
+    //   256 tokens 6.3 4.8 4.8 4.4 5.1 6.1 7.1 9.2 11; 512: 9.1 6.9 5.3 5.6 5.8 6.2 7.2 9.1 11; 1,024: 14 9.8 7.7 6.1 6.9 7.9 8.7 11 11;
+    //   2,048: 26 16 12 10 10 8.5 9.8 12 15; 4,096: 48 29 22 18 15 14 14 13 16; 16,384: 181 106 82 67 56 55 55 55 55
+    // More than 16 only where the wave is full of rows, too (9,001 tokens, 24 + 24 x 64: 19 with 16, 17 with 24); else
+    // 16, or 32 for many waves.
+    constexpr int64_t kWave = 2 * 152;
     auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
+    const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L);
     int hpt = 1;
-    while (groups_of(hpt) > 65535 || (hpt < 32 && a.n_tokens * L * groups_of(2 * hpt) >= kThreads)) hpt *= 2;
-    const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L), groups = groups_of(hpt);
+    while (hpt < 32 && blocks * groups_of(hpt) > kWave) ++hpt;
+    if (blocks * groups_of(hpt) > kWave || (hpt > 16 && blocks * heads * 10 < kWave * hpt * 7))
+      hpt = blocks * groups_of(32) > 2 * kWave ? 32 : 16;
+    const int64_t groups = groups_of(hpt);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch_kernel(a.interleaved ? norm_rope_kernel<T, kD, true> : norm_rope_kernel<T, kD, false>,
                          dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(256), 0, stream, a,
