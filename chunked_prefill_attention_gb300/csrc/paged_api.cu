@@ -136,29 +136,37 @@ int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; 
 //   64 sequences (512 units, 84 % of two waves)                         69 65 72 99 170 | 125 121 124 155 244
 // Of more than 8 rows at most four CTAs, whose states are twice as large (one sequence of 16 rows, 4,096 keys of 64 channels,
 // 1, 2, 4, 8 CTAs 31 21 18 19; 4 sequences 34 27 23 26; 2,048 keys of 128 channels 36 27 25 29, 36 30 28 34).
+// 16 rows of 128 channels in one CTA an SM, shares, 1, 2, 4 CTAs: one sequence, 1,024 and 4,096 keys 31 19 16 16 | 30 47 30 23;
+// 4: 32 19 16 16 | 39 48 31 24; 8, with at most 2: 34 20 17 26 | 50 48 31 39; 16, with 1: 45 20 26 | 80 51 56.
 // Longer units than 8 tiles a warp only where they fill their waves, and up to 40: a batch with one long sequence
 // waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).
 int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim) {
-  const int64_t units = batch * kv_heads, slots = 2 * 152, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
+  const int64_t units = batch * kv_heads, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
+  const bool only = rows > 8 && head_dim == 128 && units <= 152;   // one CTA an SM, see there
+  const int64_t slots = only ? 152 : 2 * 152;
   const int64_t tiles = (keys + keys_of_warps - 1) / keys_of_warps;   // of a warp of one CTA
   int32_t ctas = 1;
   while (ctas < (rows <= 8 ? 8 : 4) && units * 2 * ctas <= slots && tiles >= 4 * ctas) ctas *= 2;
   const int64_t waves = (units * ctas + slots - 1) / slots, each = (tiles + ctas - 1) / ctas;
   if (units * ctas > 0x7FFFFFFF) return 0;
-  return each <= 8 || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
+  return each <= (only ? 12 : 8) || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
 }
 
 // Whether sequences of more than 16 rows per K/V head, with bounded keys, go to the few-row kernel as well, a cluster for
 // every 16 rows: it reads the keys again for each, but needs neither the tile kernel's start nor its join.  Tile kernel and
 // few-row kernel, us, 8 K/V heads; windows of 512, 1,024, 4,096 keys:
 //   32 rows, 64 channels: one sequence 21 14 | 19 16 | 23 20; 4: 23 14 | 21 18 | 28 24; 16: 28 16 | 36 21 | 62 45;
-//     64: 104 52 | 123 64 | 225 150.  128 channels: 20 17 | 21 23 | 27 35; 21 21 | 23 26 | 32 39; 36 25 | 43 33 | 86 88;
+//     64: 104 52 | 123 64 | 225 150.  128 channels: 20 13 | 21 17 | 27 24; 21 15 | 23 17 | 33 31; 37 25 | 43 33 | 87 88;
 //     123 80 | 150 114 | 307 294
 //   64 rows, 64 channels: 22 15 | 20 17 | 23 27; 24 16 | 21 20 | 28 30; 30 29 | 38 40 | 64 87; 112 98 | 132 123 | 235 291.
-//     128 channels: 21 18 | 22 25 | 27 36; 40 44 | 46 62 | 89 167 (16)
+//     128 channels: 21 13 | 22 17 | 28 24; 22 15 | 23 20 | 33 48; 40 44 | 46 62 | 90 168; 64 of 128 keys 115 100
+// `units`: pairs of sequence and K/V head.
 bool few_takes(int64_t rows, int64_t units, int64_t keys, int32_t head_dim) {
-  if (rows <= 32) return head_dim == 64 || keys <= 640 || units >= 128;
-  return rows <= 64 && head_dim == 64 && keys <= 640;
+  if (rows <= 32) return true;
+  if (rows > 64) return false;
+  if (head_dim == 64) return keys <= 640;
+  const int64_t clusters = units * ((rows + 15) / 16);
+  return keys <= 200 || (clusters <= 152 && keys <= 1100) || (clusters <= 76 && keys <= 2200);
 }
 
 // The launches of a call, from its bounds alone.

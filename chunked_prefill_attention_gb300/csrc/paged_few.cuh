@@ -242,8 +242,11 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, uint32_t rank) {
 // per unit, whose first one takes the others' states from their shared memory.
 // kMode: a window has two edges.  A key is hidden from a row behind either, so the keys that every row, or any
 // row, sees are the intervals' intersection and union; a tile of neither edge needs no mask.
-template <typename QT, int D, int NT, bool kDirect, int kMode>
-__global__ void __launch_bounds__(kThreads, 2)
+// kOnly: one CTA an SM, with the registers of two.  Where a grid has no more CTAs than the GPU has SMs, 16 rows of 128
+// channels lose their spills by it: one sequence in windows of 1,024 keys 20 -> 16 us, four 24 -> 16; of 2,048 keys 25 -> 19
+// and 28 -> 18; 64 sequences of 1,024, with two CTAs an SM, take 67 us and 79 so.
+template <typename QT, int D, int NT, bool kDirect, int kMode, bool kOnly>
+__global__ void __launch_bounds__(kThreads, kOnly ? 1 : 2)
 paged_few_kernel(const PagedArgs a) {
   using Sh = Shape<D, NT>;
   using Pt = Part<D, NT>;
@@ -1081,9 +1084,9 @@ __global__ void __launch_bounds__(kThreads) paged_few_join_kernel(const PagedArg
   }
 }
 
-template <typename QT, int D, int NT, bool kDirect, int kMode>
+template <typename QT, int D, int NT, bool kDirect, int kMode, bool kOnly = false>
 cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
-  auto kernel = paged_few_kernel<QT, D, NT, kDirect, kMode>;
+  auto kernel = paged_few_kernel<QT, D, NT, kDirect, kMode, kOnly>;
   constexpr int smem = Shape<D, NT>::SMEM;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -1105,6 +1108,8 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStre
   // of 106 at 64 channels, 277 instead of 198 at 128
   if (direct) {
     const int ctas = a.batch * a.kv_heads * (kMode == kPlain ? 1 : a.cluster * a.row_tiles);
+    if constexpr (kMode != kPlain && D == 128)
+      if (rows > 8 && ctas <= 152) return launch_few<QT, D, 2, true, kMode, true>(a, ctas, stream);
     return rows <= 8 ? launch_few<QT, D, 1, true, kMode>(a, ctas, stream) : launch_few<QT, D, 2, true, kMode>(a, ctas, stream);
   }
   int dev = 0, sms = 0;
