@@ -140,13 +140,23 @@ int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; 
 // 4: 32 19 16 16 | 39 48 31 24; 8, with at most 2: 34 20 17 26 | 50 48 31 39; 16, with 1: 45 20 26 | 80 51 56.
 // Longer units than 8 tiles a warp only where they fill their waves, and up to 40: a batch with one long sequence
 // waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).
-int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim) {
+// `most` (behind a prefix): keys that a sequence can have beyond `keys`, which are those that it has where the prefix is as
+// long as its bound.  The clusters are made for them as far as they fit one wave, since the CTAs that a sequence has no tiles
+// for leave at once (ranks_of): single tokens, 8 x 128 bf16, max_kv 32,768, max_prefix 32,000, us for prefixes of 0, 64, 2,048, 16,384
+// and 32,000 keys, in clusters made for `keys` and for `most` (attn_paged whatever the prefix):
+//   4 sequences   170 202 187 119 45 |  66  74  73  60 45 (61)      16 sequences, 2 heads  168 200 194 118 35 |  68  73  74  57 34 (61)
+//   8 sequences   198 203 195 123 46 | 112 118 115  83 46 (106)     32 sequences, 1 head   136 145 142 120 36 |  65  74  75  57 36 (61)
+// and 4 bursts of 4 tokens (16 rows) 169 178 171 115 55 | 97 108 105 81 55 (88).
+// Sequences that differ are not evened out: 63 of 500 to 934 keys and one of 32,768, nothing shared, 265, but 57 in the shares
+// that max_prefix = max_kv plans (attn_paged 48).
+int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim, int64_t most) {
   const int64_t units = batch * kv_heads, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
   const bool only = rows > 8 && head_dim == 128 && units <= 152;   // one CTA an SM, see there
   const int64_t slots = only ? 152 : 2 * 152;
   const int64_t tiles = (keys + keys_of_warps - 1) / keys_of_warps;   // of a warp of one CTA
   int32_t ctas = 1;
-  while (ctas < (rows <= 8 ? 8 : 4) && units * 2 * ctas <= slots && tiles >= 4 * ctas) ctas *= 2;
+  const int64_t at_most = (most + keys_of_warps - 1) / keys_of_warps;
+  while (ctas < (rows <= 8 ? 8 : 4) && units * 2 * ctas <= slots && at_most >= 4 * ctas) ctas *= 2;
   const int64_t waves = (units * ctas + slots - 1) / slots, each = (tiles + ctas - 1) / ctas;
   if (units * ctas > 0x7FFFFFFF) return 0;
   return each <= (only ? 12 : 8) || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
@@ -195,7 +205,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   p.row_tiles = 1;
   if (window && p.tiles && few_takes(max_q * group, batch * kv_heads, few_kv, head_dim)) {
     const int32_t row_tiles = static_cast<int32_t>((max_q * group + kFewRows - 1) / kFewRows);
-    p.cluster = few_cluster(batch, kv_heads * row_tiles, max_q * group, few_kv, head_dim);
+    p.cluster = few_cluster(batch, kv_heads * row_tiles, max_q * group, few_kv, head_dim, few_kv);
     if (p.cluster > 0) {
       p.tiles = false;
       p.few = p.direct = true;
@@ -215,7 +225,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.cluster = window ? few_cluster(batch, kv_heads, max_q * group, few_kv, head_dim) : 0;
+  p.cluster = window ? few_cluster(batch, kv_heads, max_q * group, few_kv, head_dim, few_kv) : 0;
   p.direct = window ? p.cluster > 0 : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
@@ -412,21 +422,29 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
     p.floats = p.window ? w.floats : plain.floats;
     return p;
   }
-  // the own keys are those behind the prefix, as far as the bounds tell
+  // the own keys are those behind the prefix if it is as long as its bound; the launches have to do with any from there to
+  // max_kv, where a bound serves shorter prefixes too
   const int64_t own_kv = max_kv > max_prefix ? max_kv - max_prefix : max_kv;
   int64_t own_floats = 0;
   p.own_rows = max_q * group;
   p.row_tiles = 1;
   // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so)
   if (p.own_rows > kFewRows && p.own_rows <= 32 && head_dim == 64 && own_kv <= 1100) p.row_tiles = 2;
-  p.cluster = few_cluster(batch, kv_heads * p.row_tiles, p.own_rows, own_kv, head_dim);
+  p.cluster = few_cluster(batch, kv_heads * p.row_tiles, p.own_rows, own_kv, head_dim, max_kv);
   p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster > 0);
   if (p.own_few) {
     p.own_direct = p.cluster > 0;
     own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
   } else {
-    // of many sequences the shares are planned here, from the keys that any of them can have
-    p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, batch <= 64 ? own_kv : max_kv, head_dim);
+    // Shares for the keys that a sequence can have: up to 64 sequences cut them on the device, by what they have, and of more
+    // the shares are planned here.  But of more than two thirds of a wave of units, shares for few keys are not worth their
+    // grid.  By own_kv and by max_kv, bounds and prefixes as at few_cluster, 200 own keys, us:
+    //   4 sequences of 64 rows, 8 x 128 (32 units)   419 430 413 248  71 | 124 135 135 102  71 (attn_paged 118)
+    //   8 sequences of 64 rows, 8 x 64 (64 units)    255 264 251 161  67 | 138 148 142 106  69 (131)
+    //   16 sequences of 32 rows, 8 x 128 (128 units) 427 439 418 269 109 | 431 444 422 274 113 (413)
+    p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, max_kv, head_dim);
+    if (batch <= 64 && p.own.slots > 152 * 2 / 3)
+      p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, own_kv, head_dim);
     own_floats = p.own.floats;
   }
   p.prefix = q8a::plan_paged_tiles(1, total_q * group, total_q * group, kv_heads, max_prefix, head_dim);

@@ -556,7 +556,11 @@ int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_
  *   prefix_len    int32 [1] on the device, 0..max_prefix (where it is read, a value out of range is
  *                 recorded and taken for the nearest): keys that the sequences share.  Of a prefix that ends inside a
  *                 page the whole pages are shared; what is left is read as the sequences' own.
- *   max_prefix    upper bound of prefix_len, at most prefix_pages * page_tokens.
+ *   max_prefix    upper bound of prefix_len, at most prefix_pages * page_tokens.  The launches are made
+ *                 for sequences of about max_kv - max_prefix keys of their own, or where max_prefix is
+ *                 max_kv or more, for any.  Shorter prefixes are right all the same, and sequences that are
+ *                 alike then take about attn_paged's time; but one of many own keys beside short ones waits for
+ *                 few blocks.  Where prefix_len may be anything, max_prefix should be max_kv.
  *   block_table   each row names the prefix's pages too, as for attn_paged: the first
  *                 prefix_len / page_tokens entries may be read or not.  kv_lens counts the prefix's keys;
  *                 a sequence may be shorter than the prefix, and sees its first kv_lens keys.

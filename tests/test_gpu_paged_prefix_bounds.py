@@ -1,0 +1,59 @@
+"""attn_paged_prefix with bounds made for long prefixes while the prefix on the device is short, or none: the launches for the own
+keys find out there how many they are.
+
+Tolerances: those of test_gpu_paged_range.py."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_paged import BF16, F16, Q, clean_status   # noqa: F401 (fixtures)
+from tests.test_gpu_paged_range import Shared, before, check
+
+pytestmark = pytest.mark.gpu
+
+
+def is_shared(Q, x, args, most):
+    """Whether the call shares the prefix: then its workspace holds a state of every row."""
+    heads, kv_heads = x.q.shape[1], x.k_pages.shape[1]
+    floats = Q.paged_prefix_workspace_floats(len(x.q_lens), x.q.shape[0], heads, kv_heads, args[6], args[7], most, x.D)
+    return floats >= x.q.shape[0] * heads * (x.D + 1)
+
+
+OWN = [
+    # new tokens, own keys, prefix, heads, kv heads: from own keys of less than a tile to the most that a cluster takes
+    ([1] * 4, [1, 300, 2000, 7000], 3000, 8, 2),                        # clusters of eight, of which one to eight work
+    ([1] * 40, [1 + 160 * i for i in range(40)], 900, 8, 2),            # of two
+    ([4, 1, 2, 4], [4, 300, 2000, 7000], 3000, 8, 2),                   # 16 rows, clusters of four
+    ([8, 1, 5, 8], [8, 100, 1000, 500], 3000, 8, 2),                    # 32 rows
+    ([16, 3, 16, 1], [16, 60, 170, 100], 3000, 8, 2),                   # the tile kernel, in shares
+    ([30] * 12, [30 + 11 * i for i in range(12)], 3000, 16, 8),
+]
+
+
+@pytest.mark.parametrize("q_lens,own,prefix,heads,kv_heads", OWN)
+@pytest.mark.parametrize("D,dtype,page", [(64, F16, 16), (128, BF16, 64)])
+def test_prefix_far_below_its_bound(Q, q_lens, own, prefix, heads, kv_heads, D, dtype, page):
+    x = Shared(q_lens, own, prefix, heads, kv_heads, D, page, dtype, seed=sum(own))
+    args = x.shared()
+    assert is_shared(Q, x, args, 1 << 19)
+    for n in (prefix, 0, 64, prefix // 2, page - 1):
+        x.len.fill_(n)
+        out = Q.attn_paged_prefix(*args, out=torch.full_like(x.q, float("nan")))
+        check(x, out, before(True), joined=True)
+        assert torch.equal(out, Q.attn_paged_prefix(*args))
+
+
+@pytest.mark.parametrize("q_len", [1, 4, 16])
+def test_prefix_captured_for_any_length(Q, q_len):
+    """One graph, replayed from a prefix of all keys but a few down to none and back."""
+    x = Shared([q_len] * 4, [q_len, 200, 3000, 40], 4000, 8, 2, 128, 16, BF16, seed=q_len)
+    args, out, graph = x.shared(), torch.empty_like(x.q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.attn_paged_prefix(*args, out=out)
+    for n in (4000, 0, 1000, 15, 4000):
+        x.len.fill_(n)
+        x.q.normal_()
+        out.fill_(float("nan"))
+        graph.replay()
+        check(x, out, before(True), joined=True)
