@@ -20,8 +20,10 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // Sequence b gets new_lens[b] tokens behind its kv_lens[b] keys.  With P tokens a page it needs
 //   ceil((kv + n) / P) - ceil(kv / P)
 // more pages; the sums of the rows and of the pages before b (two exclusive scans) say where its rows start
-// and which of the free pages are its own, so nothing depends on the order in which blocks run.  A new page's first
-// row is a new token's, and that token's thread writes the page's number into the table.
+// and which of the free pages are its own, so nothing depends on the order in which blocks run.  The pages' scan counts what
+// refused sequences lack too, so that a sequence's pages suffice if all before it had theirs as well: pages go to the first ones, and
+// nobody overtakes a sequence that waits for more than are left.  A new page's first row is a new token's, and that token's
+// thread writes the page's number into the table.
 //
 // A step's work is a few kilobytes: latency bounds it.  Every block scans the lengths itself, so no block waits
 // for another's results.  Many tokens are dealt to blocks, the first of which writes the lengths and the number of free

@@ -719,8 +719,10 @@ def q8kv_extend_paged(new_lens, kv_lens, block_table, free_pages, n_free, page_t
     row of block_table (int32 [B, width], written in place).  Returns (kv_lens, cu_q, slots, positions, n_free): the new
     lengths, int32 [B + 1] first rows, int64 [total_q] slots and positions of the packed tokens (-1 and 0 behind the
     last sequence), and int32 [1] pages left.  A sequence for which pages, the table's row or total_q do not suffice
-    stays as it was, its tokens get slot -1, and the failure is recorded (device_status).  `out`: those five tensors to write into, of which the first and the
-    last may be kv_lens and n_free themselves."""
+    stays as it was, its tokens get slot -1, and the failure is recorded (device_status).  Pages are dealt in order and no
+    sequence overtakes another: from the first one on that lacks more pages than are left, only those that need none go on (put
+    first what has to).  `out`: those five tensors to write into, of which the first and the last may be kv_lens and n_free
+    themselves."""
     device = _device_of(new_lens)
     B = new_lens.shape[0] if new_lens.dim() == 1 else -1
     new = _index("new_lens", new_lens, torch.int32, B, device)

@@ -600,7 +600,10 @@ int64_t q8a_paged_prefix_workspace_floats(int64_t batch, int64_t total_q, int32_
  *                      behind the last sequence get slot -1 and position 0 (padding).
  *   kv_lens_out        int32 [batch], may be kv_lens.  n_free_out: int32 [1], may be n_free.
  *   cu_q               int32 [batch + 1].  slots, positions: int64 [total_q].
- * A sequence whose pages are more than are left, that passes its table's row or total_q,
+ * Pages are dealt in the order of the sequences, and none overtakes another: from the first one
+ * on whose pages are more than are left, no sequence gets any, however few it needs, and those left stay free
+ * (n_free_out counts them).  A caller that may run short puts the sequences that have to go on first.
+ * A sequence that gets no pages but needs some, that passes its table's row or total_q,
  * or whose lengths are negative is left as it was: its kv_lens stays, its tokens get slot
  * -1 and position 0 (cu_q counts their rows, up to total_q), and the failure is recorded as an
  * index out of range.  Sequences that need no page are served all the same.  A page number
