@@ -691,6 +691,8 @@ def attn_paged_prefix(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, ma
                       max_prefix=None, scale=None, causal=True, out=None, workspace=None):
     """attn_paged for sequences whose first prefix_len[0] keys (int32 [1]) are the same pages, prefix_table (int32 [n]):
     these are read once for all rows.  block_table names them too, and kv_lens counts their keys; whole pages are shared.
+    Where sharing pays (by the bounds), scales of the prefix's values count as at most 515.5 and with bf16 its values are
+    rounded to fp16, as in attn_paged's calls of many rows, for single tokens too.
     max_prefix: a bound of prefix_len (default: what prefix_table's pages hold); the launches are made for max_kv - max_prefix
     own keys a sequence, or for any where it is max_kv or more, as prefixes of any length in a captured step want.  `workspace`: of
     paged_prefix_workspace_floats(...) elements (allocated here when None)."""

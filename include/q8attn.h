@@ -551,7 +551,7 @@ int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_
  * attn_paged_prefix -- attn_paged for sequences whose first keys are the same pages (a system
  * prompt, a document that many ask about): the pages of the shared prefix are read once for all
  * rows of all sequences, those behind it for each sequence, and a row's two states are joined.
- * The result is attn_paged's, up to rounding.
+ * The result is attn_paged's, up to the numerics below.
  *   prefix_table  int32 [prefix_pages] on the device: the prefix's pages.
  *   prefix_len    int32 [1] on the device, 0..max_prefix (where it is read, a value out of range is
  *                 recorded and taken for the nearest): keys that the sequences share.  Of a prefix that ends inside a
@@ -566,8 +566,12 @@ int64_t q8a_paged_window_workspace_floats(int64_t batch, int64_t total_q, int32_
  *                 a sequence may be shorter than the prefix, and sees its first kv_lens keys.
  * Calls whose sequences have more than 128 rows per K/V head, and those whose bounds say that the
  * launches that sharing adds would cost more than it saves (few sequences, short prefixes), run as attn_paged.
- * Numerics: attn_paged's with max_q * group above 16 for the prefix; an output joins two
- * states in fp32.  Rows of sequences beyond the bounds max_q, max_kv get unspecified results.  Errors: as
+ * Numerics: a call that does not share has attn_paged's.  One that does takes the prefix as attn_paged takes
+ * max_q * group above 16, for single tokens too: with bf16 output its values are rounded once to fp16, a scale of
+ * V above 515.5 (or NaN) counts as 515.5, and K of values beyond fp16's range gives NaN to the rows that see it, where attn_paged
+ * of few rows takes all of these as they are.  The keys behind the prefix are taken as attn_paged takes them, the
+ * rest of a prefix that ends inside a page among them, and an output joins the two states in fp32.  Which of the two a call
+ * is follows from its bounds alone.  Rows of sequences beyond the bounds max_q, max_kv get unspecified results.  Errors: as
  * attn_paged.  The workspace holds q8a_paged_prefix_workspace_floats(...) floats.
  */
 int attn_paged_prefix(const void *q, int32_t dtype, int64_t q_token_stride, int64_t total_q,

@@ -57,3 +57,34 @@ def test_prefix_captured_for_any_length(Q, q_len):
         out.fill_(float("nan"))
         graph.replay()
         check(x, out, before(True), joined=True)
+
+
+def set_scale(x, pages, kept, b, key, bits, value, sequences):
+    """Block 0 of row `key` of sequence b gets the scale of these bits; the sequences keep it as `value`."""
+    slot = int(x.slots(b, torch.tensor([key], device="cuda")))
+    block = pages[slot // x.page, :, slot % x.page, :34]
+    block[:, 0], block[:, 1] = bits & 255, bits >> 8
+    codes = block[:, 2:].contiguous().view(torch.int8).double().cpu()
+    for s in sequences:
+        kept[s] = torch.as_tensor(kept[s]).clone()
+        kept[s][key, :, :32] = codes * value
+
+
+@pytest.mark.parametrize("q_len", [1, 3])
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16)])
+def test_prefix_scales_beyond_fp16(Q, q_len, D, dtype):
+    """Scales of V above 515.5, infinite and NaN: 515.5 in a prefix that is shared; as they are behind it, and in a call
+    that does not share."""
+    x = Shared([q_len] * 4, [300, 40, 100, 200], 640, 8, 2, D, 16, dtype, seed=q_len)
+    every = range(4)
+    set_scale(x, x.v_pages, x.v, 0, 100, 0x67D0, 515.5, every)         # 2000
+    args = x.shared()
+    assert is_shared(Q, x, args, 1 << 19) and not is_shared(Q, x, x.args(), 640)
+    check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
+    set_scale(x, x.v_pages, x.v, 1, 650, 0x6400, 1024.0, [1])          # sequence 1's own
+    check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
+    set_scale(x, x.v_pages, x.v, 0, 100, 0x67D0, 2000.0, every)
+    check(x, Q.attn_paged_prefix(*x.args(), x.pages, x.len), before(True), joined=True)
+    for bits in (0x7C00, 0x7E00):
+        set_scale(x, x.v_pages, x.v, 0, 100, bits, 515.5, every)
+        check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
