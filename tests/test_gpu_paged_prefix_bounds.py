@@ -13,11 +13,13 @@ from tests.test_gpu_paged_range import Shared, before, check
 pytestmark = pytest.mark.gpu
 
 
-def is_shared(Q, x, args, most):
-    """Whether the call shares the prefix: then its workspace holds a state of every row."""
-    heads, kv_heads = x.q.shape[1], x.k_pages.shape[1]
-    floats = Q.paged_prefix_workspace_floats(len(x.q_lens), x.q.shape[0], heads, kv_heads, args[6], args[7], most, x.D)
-    return floats >= x.q.shape[0] * heads * (x.D + 1)
+def is_shared(Q, x, args):
+    """Whether the call shares the prefix: then what the sequences' own tables name for it is not read, else it is recorded."""
+    assert Q.device_status(clear=True)[0] == Q.Q8A_OK and int(x.len) >= x.page
+    table = args[3].clone()
+    table[:, :int(x.len) // x.page] = 0x7FFFFFF0
+    Q.attn_paged_prefix(*args[:3], table, *args[4:])
+    return Q.device_status(clear=True)[0] == Q.Q8A_OK
 
 
 OWN = [
@@ -36,7 +38,7 @@ OWN = [
 def test_prefix_far_below_its_bound(Q, q_lens, own, prefix, heads, kv_heads, D, dtype, page):
     x = Shared(q_lens, own, prefix, heads, kv_heads, D, page, dtype, seed=sum(own))
     args = x.shared()
-    assert is_shared(Q, x, args, 1 << 19)
+    assert is_shared(Q, x, args)
     for n in (prefix, 0, 64, prefix // 2, page - 1):
         x.len.fill_(n)
         out = Q.attn_paged_prefix(*args, out=torch.full_like(x.q, float("nan")))
@@ -79,7 +81,7 @@ def test_prefix_scales_beyond_fp16(Q, q_len, D, dtype):
     every = range(4)
     set_scale(x, x.v_pages, x.v, 0, 100, 0x67D0, 515.5, every)         # 2000
     args = x.shared()
-    assert is_shared(Q, x, args, 1 << 19) and not is_shared(Q, x, x.args(), 640)
+    assert is_shared(Q, x, args) and not is_shared(Q, x, (*x.args(), x.pages, x.len))
     check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
     set_scale(x, x.v_pages, x.v, 1, 650, 0x6400, 1024.0, [1])          # sequence 1's own
     check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
@@ -88,3 +90,19 @@ def test_prefix_scales_beyond_fp16(Q, q_len, D, dtype):
     for bits in (0x7C00, 0x7E00):
         set_scale(x, x.v_pages, x.v, 0, 100, bits, 515.5, every)
         check(x, Q.attn_paged_prefix(*args), before(True), joined=True)
+
+
+@pytest.mark.parametrize("q_lens,own,prefix", [([1, 1, 1], [1, 1, 1], 16), ([1, 0, 1, 1], [1, 0, 33, 7], 40), ([2, 1, 3], [2, 90, 3], 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_smallest_shared_batches(Q, q_lens, own, prefix, causal):
+    """One K/V head, one query head, few keys: a prefix of a page, with bounds long enough for it to be shared."""
+    x = Shared(q_lens, own, prefix, 1, 1, 64, 16, F16, seed=len(q_lens))
+    entries = (1 << 23) // 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.full((len(q_lens), entries + 8), 0x7FFFFFFF, **i32)
+    table[:, :x.table.shape[1]] = x.table
+    pages = torch.full((entries,), 0x7FFFFFFF, **i32)
+    pages[:len(x.pages)] = x.pages
+    args = x.q, x.k_pages, x.v_pages, table, x.kv_lens, x.cu_q, max(q_lens), entries * 16 + 100
+    assert is_shared(Q, x, (*args, pages, x.len))
+    check(x, Q.attn_paged_prefix(*args, pages, x.len, causal=causal), before(causal), joined=True)

@@ -24,8 +24,9 @@ def child(cases):
     rec.record_own.argtypes = [P]
     got = (ctypes.c_int64 * 8)()
     rec.record_own(got)
-    for batch, q, group, kv, D, max_kv, most in cases:
-        page, total, heads = 64, batch * q, kv * group
+    for batch, q, group, kv, D, max_kv, most, *rows in cases:
+        page, heads = 64, kv * group
+        total = rows[0] if rows else batch * q
         floats = lib.q8a_paged_prefix_workspace_floats(batch, total, heads, kv, q, max_kv, most, D)
         rc = lib.attn_paged_prefix(P(1 << 36), 0, heads * D, total, heads, kv, D, P(0x200000), P(0x300000), 4, page,
                                    kv * page * D // 32 * 34, P(0x400000), -(-max_kv // page), P(0x500000), P(0x600000), batch, q,
@@ -86,3 +87,19 @@ def test_clusters_of_a_call_with_few_sequences(plans):
     for batch, q, kv, D, cluster in ((4, 1, 8, 128, 8), (8, 1, 8, 128, 4), (16, 1, 8, 128, 2), (64, 1, 8, 128, 1), (4, 4, 8, 128, 4),
                                      (16, 4, 8, 64, 2)):
         assert plans([(batch, q, 4, kv, D, 32768, 32000)])[0]["cluster"] == cluster, (batch, q, kv, D)
+
+
+def test_which_batches_share(plans):
+    """Of the batches that tests/test_gpu_paged_range.py calls behind a prefix of any length, those that share it: with bounds of
+    2^19 keys all but one sequence, two single tokens, three of one K/V head of 64 channels, and rows that fill the tiles by
+    themselves; with their own bounds only two large ones."""
+    pytest.importorskip("torch")
+    from tests.test_gpu_paged_range import PREFIX
+
+    def shared(bounds):
+        return [i for i, p in enumerate(plans([(len(q), max(q), heads // kv, kv, D, *bounds(prefix, max(own), page), sum(q))
+                                               for q, own, prefix, heads, kv, D, page in PREFIX])) if p["shared"]]
+
+    loose = shared(lambda prefix, own, page: ((1 << 19) + own, 1 << 19))
+    assert [PREFIX[i][0] for i in range(len(PREFIX)) if i not in loose] == [[1, 1], [1, 1, 1], [200, 3], [7]]
+    assert [PREFIX[i][0] for i in shared(lambda prefix, own, page: (prefix + own, -(-prefix // page) * page))] == [[1] * 300, [5] * 40]
