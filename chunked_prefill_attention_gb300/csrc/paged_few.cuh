@@ -283,7 +283,8 @@ paged_few_kernel(const PagedArgs a) {
   int32_t* desc = nullptr;
   float* parts = a.part + kMaxWarps * kDescInts;
   if (kDirect) {
-    // tiles of this unit alone; a sequence has one row tile
+    // tiles of this unit alone: kPlain, a sequence and K/V head, whose rows are one tile; else one of its a.row_tiles tiles
+    // of rows
     b = unit_of() / (kCluster ? a.row_tiles : 1) / a.kv_heads;
     const auto un = units_of<D, NT, kMode>(a, read_seq(a, b), start_key);
     if ((kCluster ? static_cast<int>(unit_of() % a.row_tiles) : 0) >= un.row_tiles) return;   // uniform

@@ -55,14 +55,16 @@
 extern "C" {
 #endif
 
-/* Raised whenever an entry point is added or its contract changes.  2: the
+/* Raised when an entry point's contract changes, and up to 7 with each that was added.  2: the
  * split, allocation-free split, pipelined and grouped-query calls.  3: the
  * pipelined call streams K and V through two chunk slots (kv_slots).  4:
  * head_dim 128 and q8a_plane_stride_bytes_for.  5: the captured prefill
  * (q8a_prefill_graph_*).  6: attn_prefill_pipelined and the split calls at
  * head_dim 128, q8a_prefill_slot_floats_for, q8a_split_workspace_floats_for and
- * attn_chunk_step_split_gqa.  7: q8a_status; the paged cache's calls and
- * attn_rope came to it later and change no earlier call. */
+ * attn_chunk_step_split_gqa.  7: q8a_status; attn_rope and the paged cache's calls came to it
+ * later, then attn_paged_window, attn_paged_prefix, q8kv_extend_paged and attn_norm_rope.  These change
+ * no earlier call and did not raise it: whether a library of version 7 has one is what a lookup
+ * of its name (dlsym) tells. */
 #define Q8A_ABI_VERSION 7u
 
 enum {
