@@ -93,6 +93,8 @@ struct ExtendArgs {
 };
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream);
 
+constexpr int kSms = 152;   // of a GB300: what the rules fill waves of
+
 // Most keys of a sequence: lengths are int32, and a tile's end must not pass 2^31.
 constexpr int64_t kMaxKeys = 0x7FFF0000;
 
@@ -135,6 +137,7 @@ struct PagedArgs {
   int32_t seqs;               // kPrefix: sequences of kv_lens and cu_q (batch is 1)
   int32_t row_tiles;          // few-row kernel, direct, kWindow and kOwn: tiles of 16 rows (8 where one is enough) of a unit
   int32_t cluster;            // few-row kernel, direct, kWindow and kOwn: CTAs of a unit (1, 2, 4 or 8)
+  int32_t only;               // and whether each has an SM for itself, by the plan
   int32_t join_rows;          // kPrefix: rows of a block of the join, 8 (a warp each) or 1
   float* state;               // [total_q][heads][D] and then [total_q][heads]: outputs over the own keys,
                               // and the logarithms (base 2) of their sums of weights

@@ -149,17 +149,22 @@ int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; 
 // and 4 bursts of 4 tokens (16 rows) 169 178 171 115 55 | 97 108 105 81 55 (88).
 // Sequences that differ are not evened out: 63 of 500 to 934 keys and one of 32,768, nothing shared, 265, but 57 in the shares
 // that max_prefix = max_kv plans (attn_paged 48).
-int32_t few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim, int64_t most) {
+struct Cluster {
+  int32_t ctas;
+  bool only;   // each has an SM for itself: the instance of the few-row kernel for that
+};
+Cluster few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys, int32_t head_dim, int64_t most) {
   const int64_t units = batch * kv_heads, keys_of_warps = 8 * (2048 / head_dim);   // a tile each
-  const bool only = rows > 8 && head_dim == 128 && units <= 152;   // one CTA an SM, see there
-  const int64_t slots = only ? 152 : 2 * 152;
+  const bool only = rows > 8 && head_dim == 128 && units <= q8a::kSms;   // see kOnly there
+  const int64_t slots = only ? q8a::kSms : 2 * q8a::kSms;
   const int64_t tiles = (keys + keys_of_warps - 1) / keys_of_warps;   // of a warp of one CTA
   int32_t ctas = 1;
   const int64_t at_most = (most + keys_of_warps - 1) / keys_of_warps;
   while (ctas < (rows <= 8 ? 8 : 4) && units * 2 * ctas <= slots && at_most >= 4 * ctas) ctas *= 2;
   const int64_t waves = (units * ctas + slots - 1) / slots, each = (tiles + ctas - 1) / ctas;
-  if (units * ctas > 0x7FFFFFFF) return 0;
-  return each <= (only ? 12 : 8) || (each <= 40 && units * ctas * 100 >= waves * slots * 84) ? ctas : 0;
+  if (units * ctas > 0x7FFFFFFF) return Cluster{0, false};
+  const bool takes = each <= (only ? 12 : 8) || (each <= 40 && units * ctas * 100 >= waves * slots * 84);
+  return takes ? Cluster{ctas, only} : Cluster{0, false};
 }
 
 // Whether sequences of more than 16 rows per K/V head, with bounded keys, go to the few-row kernel as well, a cluster for
@@ -176,13 +181,14 @@ bool few_takes(int64_t rows, int64_t units, int64_t keys, int32_t head_dim) {
   if (rows > 64) return false;
   if (head_dim == 64) return keys <= 640;
   const int64_t clusters = units * ((rows + 15) / 16);
-  return keys <= 200 || (clusters <= 152 && keys <= 1100) || (clusters <= 76 && keys <= 2200);
+  return keys <= 200 || (clusters <= q8a::kSms && keys <= 1100) || (clusters <= q8a::kSms / 2 && keys <= 2200);
 }
 
 // The launches of a call, from its bounds alone.
 struct Plan {
   bool few, direct, tiles;
-  int32_t cluster, row_tiles;
+  Cluster cluster;
+  int32_t row_tiles;
   q8a::TilesPlan t;
   int64_t few_rows;   // rows a K/V head of the few-row kernel's sequences, at most: it sizes its tiles
                       // and their partial states, so workspace and launch both take it from here
@@ -206,7 +212,7 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   if (window && p.tiles && few_takes(max_q * group, batch * kv_heads, few_kv, head_dim)) {
     const int32_t row_tiles = static_cast<int32_t>((max_q * group + kFewRows - 1) / kFewRows);
     p.cluster = few_cluster(batch, kv_heads * row_tiles, max_q * group, few_kv, head_dim, few_kv);
-    if (p.cluster > 0) {
+    if (p.cluster.ctas > 0) {
       p.tiles = false;
       p.few = p.direct = true;
       p.row_tiles = row_tiles;
@@ -225,8 +231,8 @@ Plan plan_paged(int64_t batch, int64_t total_q, int64_t max_q, int64_t group, in
   // 63 single tokens and a burst of 16 (300 to 16,384 keys, 128 channels) 395 and 452.
   p.few = !p.tiles || (!p.t.pair && (total_q - (batch - 1) * max_q) * group <= kFewRows);
   p.few_rows = p.tiles ? kFewRows : max_q * group;
-  p.cluster = window ? few_cluster(batch, kv_heads, max_q * group, few_kv, head_dim, few_kv) : 0;
-  p.direct = window ? p.cluster > 0 : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
+  p.cluster = window ? few_cluster(batch, kv_heads, max_q * group, few_kv, head_dim, few_kv) : Cluster{};
+  p.direct = window ? p.cluster.ctas > 0 : q8a::paged_few_direct(batch, kv_heads, few_kv, head_dim);
   p.few_floats = p.few && !p.direct ? q8a::paged_few_floats(head_dim, p.few_rows) : 0;
   p.floats = p.few_floats + p.t.floats;
   return p;
@@ -365,7 +371,8 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
   if (int rc = check_workspace(fn, c, plan.floats, &a)) return rc;
   a.window = static_cast<int32_t>(window);
   a.sinks = static_cast<int32_t>(sinks);
-  a.cluster = plan.cluster;
+  a.cluster = plan.cluster.ctas;
+  a.only = plan.cluster.only;
   a.row_tiles = plan.row_tiles;
   cudaError_t e = cudaSuccess;
   if (plan.tiles) {
@@ -388,7 +395,8 @@ int run_paged(const char* fn, const Call& c, int64_t window, int64_t sinks, cuda
 struct PrefixPlan {
   int64_t window;   // not `share`: run_paged's
   bool share, own_few, own_direct;
-  int32_t join_rows, cluster, row_tiles;
+  int32_t join_rows, row_tiles;
+  Cluster cluster;
   int64_t own_rows;
   q8a::TilesPlan own, prefix;
   int64_t state_floats, floats;
@@ -431,9 +439,9 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so)
   if (p.own_rows > kFewRows && p.own_rows <= 32 && head_dim == 64 && own_kv <= 1100) p.row_tiles = 2;
   p.cluster = few_cluster(batch, kv_heads * p.row_tiles, p.own_rows, own_kv, head_dim, max_kv);
-  p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster > 0);
+  p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster.ctas > 0);
   if (p.own_few) {
-    p.own_direct = p.cluster > 0;
+    p.own_direct = p.cluster.ctas > 0;
     own_floats = p.own_direct ? 0 : q8a::paged_few_floats(head_dim, p.own_rows);
   } else {
     // Shares for the keys that a sequence can have: up to 64 sequences cut them on the device, by what they have, and of more
@@ -443,7 +451,7 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
     //   8 sequences of 64 rows, 8 x 64 (64 units)    255 264 251 161  67 | 138 148 142 106  69 (131)
     //   16 sequences of 32 rows, 8 x 128 (128 units) 427 439 418 269 109 | 431 444 422 274 113 (413)
     p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, max_kv, head_dim);
-    if (batch <= 64 && p.own.slots > 152 * 2 / 3)
+    if (batch <= 64 && p.own.slots > q8a::kSms * 2 / 3)
       p.own = q8a::plan_paged_tiles(batch, total_q * group, p.own_rows, kv_heads, own_kv, head_dim);
     own_floats = p.own.floats;
   }
@@ -454,7 +462,7 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
     p.prefix.floats = p.prefix.ctas * 256 * (head_dim + 2);
   }
   // a warp a row where they are enough for the machine, else a block a row
-  p.join_rows = total_q * group * kv_heads >= 152 * 8 ? 8 : 1;
+  p.join_rows = total_q * group * kv_heads >= q8a::kSms * 8 ? 8 : 1;
   p.state_floats = (total_q * group * kv_heads * (head_dim + 1) + 7) / 8 * 8;
   p.floats = p.state_floats + (own_floats > p.prefix.floats ? own_floats : p.prefix.floats);
   return p;
@@ -542,7 +550,8 @@ int attn_paged_prefix(const void* q, int32_t dtype, int64_t q_token_stride, int6
   a.prefix_len = prefix_len;
   a.prefix_most = keys_at_most(max_prefix);
   a.state = workspace;
-  a.cluster = plan.cluster;
+  a.cluster = plan.cluster.ctas;
+  a.only = plan.cluster.only;
   a.row_tiles = plan.row_tiles;
   a.part = workspace + plan.state_floats;
   cudaError_t e;

@@ -125,7 +125,7 @@ cudaError_t launch_rope_n(const T* x, T* out, int64_t n_tokens, int32_t heads, i
   const int items = (two ? r.rot / 2 / N : r.rot / N) + (head_dim - r.rot) / N;
   const int tokens = kRopeThreads / items;
   // as many heads a thread as leave every SM its threads
-  constexpr int64_t kFill = 152 * 2048;
+  constexpr int64_t kFill = kSms * 2048;
   int hpt = 16;
   while (hpt > 1 && n_tokens * items * ((heads + hpt - 1) / hpt) < kFill) hpt /= 2;
   const int64_t blocks = (n_tokens + tokens - 1) / tokens;

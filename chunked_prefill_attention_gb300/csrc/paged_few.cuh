@@ -1123,7 +1123,7 @@ cudaError_t launch_few_d(const PagedArgs& a, int64_t rows, bool direct, cudaStre
   if (direct) {
     const int ctas = a.batch * a.kv_heads * (kMode == kPlain ? 1 : a.cluster * a.row_tiles);
     if constexpr (kMode != kPlain && D == 128)
-      if (rows > 8 && ctas <= 152) return launch_few<QT, D, 2, true, kMode, true>(a, ctas, stream);
+      if (a.only) return launch_few<QT, D, 2, true, kMode, true>(a, ctas, stream);
     return rows <= 8 ? launch_few<QT, D, 1, true, kMode>(a, ctas, stream) : launch_few<QT, D, 2, true, kMode>(a, ctas, stream);
   }
   int dev = 0, sms = 0;

@@ -441,7 +441,7 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
     //   2,048: 26 16 12 10 10 8.5 9.8 12 15; 4,096: 48 29 22 18 15 14 14 13 16; 16,384: 181 106 82 67 56 55 55 55 55
     // More than 16 only where the wave is full of rows, too (9,001 tokens, 24 + 24 x 64: 19 with 16, 17 with 24); else
     // 16, or 32 for many waves.
-    constexpr int64_t kWave = 2 * 152;
+    constexpr int64_t kWave = 2 * kSms;
     auto groups_of = [&](int hpt) { return (a.heads[0] + hpt - 1) / hpt + (a.heads[1] + hpt - 1) / hpt; };
     const int64_t blocks = (a.n_tokens + 256 / L - 1) / (256 / L);
     int hpt = 1;
@@ -454,7 +454,7 @@ cudaError_t launch_norm_rope_d(const NormRopeArgs& a, cudaStream_t stream) {
                          dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(groups)), dim3(256), 0, stream, a,
                          static_cast<int32_t>(hpt), static_cast<int32_t>((a.heads[0] + hpt - 1) / hpt));
   }
-  constexpr int64_t kFill = 152 * 64;   // warps
+  constexpr int64_t kFill = kSms * 64;   // warps
   int hpw = 16;
   while (hpw > 2 && a.n_tokens * ((heads + hpw - 1) / hpw) < kFill) hpw /= 2;   // 2: at most 65,535 groups
   const int64_t blocks = (a.n_tokens + 7) / 8, groups = (heads + hpw - 1) / hpw;
@@ -472,7 +472,7 @@ cudaError_t launch_norm_rope_t(const NormRopeArgs& a, int32_t head_dim, cudaStre
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   if (a.total_q <= 4096)
     return launch_kernel(extend_kernel<kWhole>, dim3(1), dim3(a.batch <= 256 && a.total_q <= 1024 ? 256 : kExtThreads), 0, stream, a);
-  const int64_t most = (a.total_q + kExtThreads - 1) / kExtThreads, blocks = most < 152 ? most : 152;
+  const int64_t most = (a.total_q + kExtThreads - 1) / kExtThreads, blocks = most < kSms ? most : kSms;
   if (a.kv_out != a.kv_lens && a.n_free_out != a.n_free)
     return launch_kernel(extend_kernel<kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(kExtThreads), 0, stream, a);
   const cudaError_t e = launch_kernel(extend_kernel<kTokens>, dim3(static_cast<unsigned>(blocks)), dim3(kExtThreads), 0, stream, a);

@@ -262,7 +262,6 @@ __device__ __forceinline__ Load load_of(const PagedArgs& a, int b) {
   return Load{rows > a.row_limit ? static_cast<int32_t>((rows + G::ROWS - 1) / G::ROWS) : 0, tiles};
 }
 
-constexpr int kSms = 152;   // CTAs of a wave: one per SM
 constexpr int kEnds = 6;    // a CTA's start and end, in key tiles
 constexpr int kPlanned = 64;   // most sequences of a call whose shares are planned here
 

@@ -6,7 +6,7 @@
 #include "../chunked_prefill_attention_gb300/csrc/paged.h"
 
 namespace {
-int64_t g_own[8];   // kind (0 few rows, 1 tiles, -1 none), direct, cluster, row tiles, rows, shares, CTAs, shared
+int64_t g_own[9];   // kind (0 few rows, 1 tiles, -1 none), direct, cluster, row tiles, rows, shares, CTAs, shared, only
 uint32_t g_words[64];
 }  // namespace
 
@@ -14,7 +14,7 @@ namespace q8a {
 uint32_t* host_status_words() { return g_words; }
 cudaError_t launch_paged_few(const PagedArgs&, int32_t, int32_t, int64_t, bool, cudaStream_t) { return cudaSuccess; }
 cudaError_t launch_paged_few_range(const PagedArgs& a, int mode, int32_t, int32_t, int64_t rows, bool direct, cudaStream_t) {
-  if (mode == kOwn) g_own[0] = 0, g_own[1] = direct, g_own[2] = a.cluster, g_own[3] = a.row_tiles, g_own[4] = rows;
+  if (mode == kOwn) g_own[0] = 0, g_own[1] = direct, g_own[2] = a.cluster, g_own[3] = a.row_tiles, g_own[4] = rows, g_own[8] = a.only;
   return cudaSuccess;
 }
 cudaError_t launch_paged_tiles(const PagedArgs&, int32_t, int32_t, const TilesPlan&, cudaStream_t) { return cudaSuccess; }
@@ -30,7 +30,7 @@ cudaError_t launch_paged_tiles_prefix(const PagedArgs&, int32_t, int32_t, const 
 }  // namespace q8a
 
 extern "C" void record_own(int64_t* out) {
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 9; ++i) {
     out[i] = g_own[i];
     g_own[i] = i == 0 ? -1 : 0;
   }

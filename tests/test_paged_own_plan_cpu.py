@@ -22,7 +22,7 @@ def child(cases):
     from chunked_prefill_attention_gb300 import q8attn as Q
     lib, rec, out = Q.load(), ctypes.CDLL(None), []
     rec.record_own.argtypes = [P]
-    got = (ctypes.c_int64 * 8)()
+    got = (ctypes.c_int64 * 9)()
     rec.record_own(got)
     for batch, q, group, kv, D, max_kv, most, *rows in cases:
         page, heads = 64, kv * group
@@ -34,7 +34,7 @@ def child(cases):
                                    P(0x7000000000), floats, P(0))
         assert rc == 0, lib.q8a_last_error()
         rec.record_own(got)
-        out.append(dict(zip(("kind", "direct", "cluster", "row_tiles", "rows", "shares", "ctas", "shared"), got)))
+        out.append(dict(zip(("kind", "direct", "cluster", "row_tiles", "rows", "shares", "ctas", "shared", "only"), got)))
     print(json.dumps(out))
 
 
@@ -73,7 +73,9 @@ def test_own_keys_are_planned_for_short_prefixes_too(plans):
         if p["kind"] == 0 and p["direct"]:
             few += 1
             ctas = batch * kv * p["row_tiles"] * p["cluster"]
-            wave = SMS * (1 if p["rows"] > 8 and D == 128 and batch * kv * p["row_tiles"] <= SMS else 2)
+            # the instance with an SM for each CTA, where the grid leaves one
+            assert p["only"] == (p["rows"] > 8 and D == 128 and batch * kv * p["row_tiles"] <= SMS), (case, p)
+            wave = SMS * (1 if p["only"] else 2)
             assert 2 * ctas > wave or p["cluster"] == (8 if p["rows"] <= 8 else 4), (case, p)
             assert p["cluster"] == 1 or ctas <= wave, (case, p)
         elif p["kind"] == 1 and batch <= 64:
