@@ -139,7 +139,11 @@ int64_t keys_at_most(int64_t n) { return n < q8a::kMaxKeys ? n : q8a::kMaxKeys; 
 // 16 rows of 128 channels in one CTA an SM, shares, 1, 2, 4 CTAs: one sequence, 1,024 and 4,096 keys 31 19 16 16 | 30 47 30 23;
 // 4: 32 19 16 16 | 39 48 31 24; 8, with at most 2: 34 20 17 26 | 50 48 31 39; 16, with 1: 45 20 26 | 80 51 56.
 // Longer units than 8 tiles a warp only where they fill their waves, and up to 40: a batch with one long sequence
-// waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).
+// waits 50 us for it (38 sequences of 512 to 4,096 keys of 128 channels: 60 in shares, 61 so).  Both bounds are for such batches;
+// of sequences of one length a CTA a unit still gains beyond them.  Us of shares and of one CTA, 128 channels, windows of 4,096:
+// 64 sequences (84 % of two waves) 124 116, 70 133 117, 76 (100 %) 143 118, 80 (70 % of three) 148 146, but 60 (79 %) 116 116, 56 (74 %)
+// 111 95, 30 (79 % of one) 71 61; 76 sequences in windows of 5,000 (40 tiles a warp) 168 140, of 5,200 (41) 173 144, of 8,000 249 211.
+// Around 8 tiles, 2 sequences in clusters of eight: windows of 14,400 23 23, of 16,384 24 25, of 20,800 26 28.
 // `most` (behind a prefix): keys that a sequence can have beyond `keys`, which are those that it has where the prefix is as
 // long as its bound.  The clusters are made for them as far as they fit one wave, since the CTAs that a sequence has no tiles
 // for leave at once (ranks_of): single tokens, 8 x 128 bf16, max_kv 32,768, max_prefix 32,000, us for prefixes of 0, 64, 2,048, 16,384
@@ -175,6 +179,11 @@ Cluster few_cluster(int64_t batch, int32_t kv_heads, int64_t rows, int64_t keys,
 //     123 80 | 150 114 | 307 294
 //   64 rows, 64 channels: 22 15 | 20 17 | 23 27; 24 16 | 21 20 | 28 30; 30 29 | 38 40 | 64 87; 112 98 | 132 123 | 235 291.
 //     128 channels: 21 13 | 22 17 | 28 24; 22 15 | 23 20 | 33 48; 40 44 | 46 62 | 90 168; 64 of 128 keys 115 100
+// On both sides of the edges, 64 rows.  64 channels, windows of 500, 640, 800, 1,100 keys: 4 sequences 24 16 | 22 17 | 22 19 | 22 20;
+//   16: 30 34 | 36 33 | 36 34 | 39 41; 64: 112 104 | 119 105 | 122 113 | 132 133.  128 channels, of 120, 200, 300 keys: 8 sequences
+//   26 17 | 26 19 | 28 21; 16: 32 31 | 31 34 | 34 39; 64: 120 101 | 120 109 | 130 123; of 1,100, 1,400 keys: 4 (128 clusters) 24 20 | 25 24,
+//   8 (256) 31 35 | 33 41; of 2,200, 3,000: 2 (64) 25 22 | 27 25, 4 28 31 | 30 38.  32 rows of 128 channels have no edge of their own: windows
+//   of 8,192, 4 sequences, 47 51, is the most that they lose.
 // `units`: pairs of sequence and K/V head.
 bool few_takes(int64_t rows, int64_t units, int64_t keys, int32_t head_dim) {
   if (rows <= 32) return true;
@@ -436,7 +445,10 @@ PrefixPlan plan_prefix(int64_t batch, int64_t total_q, int64_t max_q, int64_t gr
   int64_t own_floats = 0;
   p.own_rows = max_q * group;
   p.row_tiles = 1;
-  // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so)
+  // 32 rows a K/V head of few keys too, where that is one launch less (16 bursts of up to 8 tokens: 166 us, 159 so).  The whole
+  // call behind 65,536 keys, 8 x 64, 32 rows, the tile kernel and so, us, 200, 900, 1,100, 1,400, 2,000 own keys: 4 sequences 58 55 | 59 61 |
+  // 60 60 | 59 60 | 61 62; 16: 110 109 | 118 114 | 120 116 | 122 119 | 126 123; 32: 222 217 | 231 225 | 234 231 | 238 234 | 246 242.  With 128
+  // channels 82 82 | 83 88 | 84 88; 182 187 | 196 196 | 198 198; 378 377 | 394 402 | 400 406: no gain.
   if (p.own_rows > kFewRows && p.own_rows <= 32 && head_dim == 64 && own_kv <= 1100) p.row_tiles = 2;
   p.cluster = few_cluster(batch, kv_heads * p.row_tiles, p.own_rows, own_kv, head_dim, max_kv);
   p.own_few = p.own_rows <= kFewRows || (p.row_tiles > 1 && p.cluster.ctas > 0);
