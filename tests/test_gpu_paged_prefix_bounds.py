@@ -106,3 +106,16 @@ def test_smallest_shared_batches(Q, q_lens, own, prefix, causal):
     args = x.q, x.k_pages, x.v_pages, table, x.kv_lens, x.cu_q, max(q_lens), entries * 16 + 100
     assert is_shared(Q, x, (*args, pages, x.len))
     check(x, Q.attn_paged_prefix(*args, pages, x.len, causal=causal), before(causal), joined=True)
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 6, 20])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bound_of_all_keys(Q, q_len, D):
+    """max_prefix = max_kv, as for prefixes of any length: one long sequence among short ones, nothing to all of it shared."""
+    x = Shared([q_len] * 6, [q_len, 9000, 40, 300, 77, 21], 2000, 8, 2, D, 16, F16, seed=q_len)
+    q, k_pages, v_pages, table, lens, cu, max_q, max_kv, pages, length = x.shared()
+    args = q, k_pages, v_pages, table, lens, cu, max_q, pages.shape[0] * x.page, pages, length
+    assert is_shared(Q, x, args)
+    for n in (2000, 0, 1000, 16):
+        x.len.fill_(n)
+        check(x, Q.attn_paged_prefix(*args, out=torch.full_like(x.q, float("nan"))), before(True), joined=True)

@@ -105,3 +105,10 @@ def test_which_batches_share(plans):
     loose = shared(lambda prefix, own, page: ((1 << 19) + own, 1 << 19))
     assert [PREFIX[i][0] for i in range(len(PREFIX)) if i not in loose] == [[1, 1], [1, 1, 1], [200, 3], [7]]
     assert [PREFIX[i][0] for i in shared(lambda prefix, own, page: (prefix + own, -(-prefix // page) * page))] == [[1] * 300, [5] * 40]
+
+
+def test_a_prefix_of_any_length_is_planned_for_any(plans):
+    """max_prefix = max_kv: the own keys in shares, few rows or tiles, however many sequences fill the wave."""
+    for batch, q, kv, D in ((64, 1, 8, 128), (16, 1, 8, 64), (16, 4, 8, 128), (16, 8, 8, 64), (16, 8, 8, 128), (4, 16, 8, 128)):
+        p = plans([(batch, q, 4, kv, D, 32768, 32768)])[0]
+        assert p["shared"] and (not p["direct"] if p["kind"] == 0 else p["shares"]), (batch, q, kv, D, p)
